@@ -23,6 +23,11 @@ HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "h3.h")
 
 H3_OK, H3_ERR_NULL, H3_ERR_SHAPE, H3_ERR_ALIGN, H3_ERR_UNSUPPORTED = 0, 1, 2, 3, 4
 H3_ERR_INDEX, H3_ERR_CUDA, H3_ERR_TIMEOUT, H3_ERR_WORKSPACE, H3_ERR_BOUNDS = 5, 6, 7, 8, 9
+H3_BF16, H3_FP32 = 0, 1
+H3_ROPE_HALF, H3_ROPE_INTERLEAVED = 0, 1
+H3_ROPE_SCALE_NONE, H3_ROPE_SCALE_LINEAR, H3_ROPE_SCALE_NTK, H3_ROPE_SCALE_YARN = 0, 1, 2, 3
+H3_ROPE_FORWARD, H3_ROPE_BACKWARD = 0, 1
+H3_NORM_RMS, H3_NORM_LAYER = 0, 1
 N_STAGES = 8
 STAGE_NAMES = ("adaln_table", "norm1_modulate", "qkv_qknorm_rope", "attention", "out_proj_residual",
                "norm2_modulate", "fc1_swiglu", "fc2_residual")
@@ -53,6 +58,18 @@ class PackedMeta(ctypes.Structure):
                 ("timestep_index", c_void_p), ("pos_thw", c_void_p), ("t_cond", c_void_p)]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("n_axes", c_int32), ("n_freqs", c_int32), ("layout", c_int32),
+                ("dtype", c_int32), ("scaling", c_int32), ("scaled_axes", c_int32), ("theta", c_float),
+                ("factor", c_float), ("trained_length", c_float), ("alpha", c_float), ("beta", c_float),
+                ("magnitude", c_float)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("width", c_int32), ("dtype", c_int32), ("param_dtype", c_int32),
+                ("eps", c_float)]
+
+
 _lib = None
 
 
@@ -66,6 +83,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         i32, sz, vp = c_int32, c_size_t, c_void_p
         cfgp, wp, mp = ctypes.POINTER(BlockConfig), ctypes.POINTER(BlockWeights), ctypes.POINTER(PackedMeta)
+        ropep, normp = ctypes.POINTER(RopeConfig), ctypes.POINTER(NormConfig)
         sig = {
             "h3_block_workspace_bytes": (sz, [cfgp, i32, i32]),
             "h3_block_adaln_side_ctas": (i32, [cfgp, i32]),
@@ -85,6 +103,14 @@ def lib() -> ctypes.CDLL:
             "h3_qkv_projection": (i32, [cfgp, mp, vp, vp, vp, vp, vp, vp, vp]),
             "h3_rope_qknorm": (i32, [cfgp, i32, vp, vp, vp, c_int64, c_int64, vp, vp, vp]),
             "h3_attention": (i32, [i32, i32, vp, vp, vp, c_int64, c_int64, vp, vp, vp]),
+            "h3_attention_backward_workspace_bytes": (sz, [i32, i32]),
+            "h3_attention_backward": (i32, [i32, i32, vp, vp, vp, c_int64, c_int64, vp, vp, vp, vp, vp, vp, c_int64,
+                                            c_int64, vp, sz, vp]),
+            "h3_rope": (i32, [ropep, i32, vp, i32, vp, vp, i32, vp, vp, i32, c_int64, c_int64, c_int64, c_int64, vp]),
+            "h3_norm_forward": (i32, [normp, i32, i32, vp, c_int64, c_int64, vp, vp, vp, c_int64, c_int64, vp]),
+            "h3_norm_backward_workspace_bytes": (sz, [normp, i32, i32]),
+            "h3_norm_backward": (i32, [normp, i32, i32, vp, c_int64, c_int64, vp, vp, c_int64, c_int64, vp, c_int64,
+                                       c_int64, vp, vp, vp, sz, vp]),
             "h3_out_projection": (i32, [cfgp, mp, vp, vp, vp, vp, vp, vp, vp]),
             "h3_ffn_up_swiglu": (i32, [cfgp, i32, vp, vp, vp, vp, vp]),
             "h3_ffn_down_residual": (i32, [cfgp, mp, vp, vp, vp, vp, vp, vp, vp]),
@@ -178,6 +204,22 @@ def make_meta(token_tag, timestep_index, pos_thw, t_cond=None, n_timesteps: int 
                    _ptr(pos_thw), _ptr(t_cond))
     s._tensors = (token_tag, timestep_index, pos_thw, t_cond)
     return s
+
+
+def make_rope_config(head_dim: int, n_axes: int, n_freqs: int, layout: int = H3_ROPE_HALF, dtype: int = H3_BF16,
+                     theta: float = 10000.0, scaling: int = H3_ROPE_SCALE_NONE, factor: float = 1.0,
+                     scaled_axes: Optional[int] = None, trained_length: float = 1.0, alpha: float = 1.0,
+                     beta: float = 32.0, magnitude: float = 1.0) -> RopeConfig:
+    """scaled_axes: bit mask of the axes that `scaling` changes (all by default)."""
+    if scaled_axes is None:
+        scaled_axes = (1 << n_axes) - 1
+    return RopeConfig(head_dim, n_axes, n_freqs, layout, dtype, scaling, scaled_axes, theta, factor, trained_length,
+                      alpha, beta, magnitude)
+
+
+def make_norm_config(kind: int, width: int, dtype: int = H3_BF16, param_dtype: int = H3_BF16,
+                     eps: float = 1e-5) -> NormConfig:
+    return NormConfig(kind, width, dtype, param_dtype, eps)
 
 
 # ---------------------------------------------------------------------------
@@ -316,6 +358,48 @@ def h3_attention(n_rows: int, n_heads: int, q, k, v, row_stride: int, head_strid
                  stream=None) -> None:
     _check(lib().h3_attention(n_rows, n_heads, _ptr(q), _ptr(k), _ptr(v), row_stride, head_stride, _ptr(o),
                               _ptr(lse), _stream(stream)), "h3_attention")
+
+
+def h3_attention_backward_workspace_bytes(n_rows: int, n_heads: int) -> int:
+    return int(lib().h3_attention_backward_workspace_bytes(n_rows, n_heads))
+
+
+def h3_attention_backward(n_rows: int, n_heads: int, q, k, v, row_stride: int, head_stride: int, o, d_o, lse, dq, dk,
+                          dv, d_row_stride: int, d_head_stride: int, workspace, stream=None) -> None:
+    _check(lib().h3_attention_backward(n_rows, n_heads, _ptr(q), _ptr(k), _ptr(v), row_stride, head_stride, _ptr(o),
+                                       _ptr(d_o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), d_row_stride,
+                                       d_head_stride, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream(stream)), "h3_attention_backward")
+
+
+def h3_rope(cfg: RopeConfig, n_rows: int, pos, direction: int, q_in, q_out, n_q_heads: int, k_in, k_out,
+            n_k_heads: int, in_row_stride: int, in_head_stride: int, out_row_stride: int, out_head_stride: int,
+            stream=None) -> None:
+    _check(lib().h3_rope(ctypes.byref(cfg), n_rows, _ptr(pos), direction, _ptr(q_in), _ptr(q_out), n_q_heads,
+                         _ptr(k_in), _ptr(k_out), n_k_heads, in_row_stride, in_head_stride, out_row_stride,
+                         out_head_stride, _stream(stream)), "h3_rope")
+
+
+def h3_norm_forward(cfg: NormConfig, n_rows: int, n_heads: int, x, x_row_stride: int, x_head_stride: int, gain, bias,
+                    y, y_row_stride: int, y_head_stride: int, stream=None) -> None:
+    _check(lib().h3_norm_forward(ctypes.byref(cfg), n_rows, n_heads, _ptr(x), x_row_stride, x_head_stride, _ptr(gain),
+                                 _ptr(bias), _ptr(y), y_row_stride, y_head_stride, _stream(stream)),
+           "h3_norm_forward")
+
+
+def h3_norm_backward_workspace_bytes(cfg: NormConfig, n_rows: int, n_heads: int) -> int:
+    return int(lib().h3_norm_backward_workspace_bytes(ctypes.byref(cfg), n_rows, n_heads))
+
+
+def h3_norm_backward(cfg: NormConfig, n_rows: int, n_heads: int, x, x_row_stride: int, x_head_stride: int, gain, dy,
+                     dy_row_stride: int, dy_head_stride: int, dx, dx_row_stride: int, dx_head_stride: int, dgain,
+                     dbias, workspace, stream=None) -> None:
+    """workspace may be None when dgain and dbias are."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().h3_norm_backward(ctypes.byref(cfg), n_rows, n_heads, _ptr(x), x_row_stride, x_head_stride,
+                                  _ptr(gain), _ptr(dy), dy_row_stride, dy_head_stride, _ptr(dx), dx_row_stride,
+                                  dx_head_stride, _ptr(dgain), _ptr(dbias), _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "h3_norm_backward")
 
 
 def h3_out_projection(cfg, meta, table, o, w_o, b_o, x, x_out, stream=None) -> None:

@@ -59,7 +59,7 @@ std::mutex g_site_mu;
 // barrier's shared-memory byte offset / 8, or kSiteStreamKFlag).
 void note_error_site(uint32_t site) {
   static const char* const names[] = {"unknown", "gemm", "attention-1q", "attention-2q", "adaln-table",
-                                      "rope-qknorm"};
+                                      "rope-qknorm", "attention-backward"};
   const uint32_t k = site >> 24, lo = site & 0xFFFFFFu;
   const char* kn = k < sizeof(names) / sizeof(names[0]) ? names[k] : "unknown";
   std::lock_guard<std::mutex> lk(g_site_mu);
@@ -1221,6 +1221,289 @@ h3_status h3_attention(int32_t n_rows, int32_t n_heads, const void* q, const voi
   if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || (reinterpret_cast<uintptr_t>(lse_opt) & 3u))
     return H3_ERR_ALIGN;
   return run_attention(n_rows, n_heads, q, k, v, row_stride_elems, head_stride_elems, o, lse_opt, stream);
+}
+
+// ===========================================================================
+// gradients, rotary positions, row norms
+// ===========================================================================
+namespace {
+// elements from a strided [rows][heads][width] view's first to its last
+inline size_t view_elems(int64_t rows, int64_t heads, int64_t width, int64_t row_stride, int64_t head_stride) {
+  return (size_t)(rows - 1) * (size_t)row_stride + (size_t)(heads - 1) * (size_t)head_stride + (size_t)width;
+}
+size_t attn_bwd_ws_bytes(int64_t S, int64_t H) { return al256((size_t)((S + 127) / 128) * (size_t)H * 256 * 4); }
+
+// Strides of a [rows][heads][width] view (one head: its stride is not used).
+h3_status check_strides(int64_t width, int32_t heads, int64_t row_stride, int64_t head_stride, int64_t unit) {
+  if (row_stride < width || (heads > 1 && head_stride < width)) return H3_ERR_SHAPE;
+  if (row_stride % unit || (heads > 1 && head_stride % unit)) return H3_ERR_ALIGN;
+  return H3_OK;
+}
+
+h3_status check_rope(const h3_rope_config* c) {
+  if (!c) return H3_ERR_NULL;
+  if (c->dtype != H3_BF16 && c->dtype != H3_FP32) return H3_ERR_UNSUPPORTED;
+  if (c->layout != H3_ROPE_HALF && c->layout != H3_ROPE_INTERLEAVED) return H3_ERR_UNSUPPORTED;
+  if (c->scaling < H3_ROPE_SCALE_NONE || c->scaling > H3_ROPE_SCALE_YARN) return H3_ERR_UNSUPPORTED;
+  if (c->head_dim < 2 || c->head_dim > kRopeMaxWidth || (c->head_dim & 1)) return H3_ERR_UNSUPPORTED;
+  if (c->n_axes < 1 || c->n_axes > 4 || c->n_freqs < 1 || c->n_freqs > kRopeMaxPairs / c->n_axes ||
+      2 * c->n_axes * c->n_freqs > c->head_dim)
+    return H3_ERR_UNSUPPORTED;
+  if (!std::isfinite(c->theta) || !(c->theta > 1.0f)) return H3_ERR_SHAPE;
+  if (!std::isfinite(c->magnitude) || !(c->magnitude > 0.0f)) return H3_ERR_SHAPE;
+  if (c->scaling != H3_ROPE_SCALE_NONE) {
+    if (!std::isfinite(c->factor) || !(c->factor >= 1.0f)) return H3_ERR_SHAPE;
+    if (c->scaled_axes < 0 || c->scaled_axes >= (1 << c->n_axes)) return H3_ERR_SHAPE;
+  }
+  if (c->scaling == H3_ROPE_SCALE_NTK && c->n_freqs < 2) return H3_ERR_UNSUPPORTED;
+  if (c->scaling == H3_ROPE_SCALE_YARN) {
+    if (!std::isfinite(c->trained_length) || !(c->trained_length >= 1.0f)) return H3_ERR_SHAPE;
+    if (!std::isfinite(c->alpha) || !std::isfinite(c->beta) || c->alpha < 0.0f || !(c->alpha < c->beta))
+      return H3_ERR_SHAPE;
+  }
+  return H3_OK;
+}
+
+// Turns per position of every rotated pair in 64-bit fixed point; omega <= 1
+// radian, so a turn fraction below 1/6.  In long double: a position of 2^31
+// multiplies omega's rounding into 2^-24 turns where omega is a double.
+void fill_turns(const h3_rope_config& c, uint64_t* turns) {
+  typedef long double real;
+  const real kTwoPi = 6.283185307179586476925286766559005768L;
+  const int F = c.n_freqs;
+  for (int a = 0; a < c.n_axes; ++a)
+    for (int f = 0; f < F; ++f) {
+      const real e = -(real)f / F, s = c.factor;
+      real w = std::pow((real)c.theta, e);
+      if (c.scaling != H3_ROPE_SCALE_NONE && ((c.scaled_axes >> a) & 1)) {
+        if (c.scaling == H3_ROPE_SCALE_LINEAR) {
+          w /= s;
+        } else if (c.scaling == H3_ROPE_SCALE_NTK) {
+          w = std::pow((real)c.theta * std::pow(s, (real)F / (F - 1)), e);
+        } else {
+          real g = ((real)c.trained_length * w / kTwoPi - c.alpha) / ((real)c.beta - c.alpha);
+          g = g < 0 ? 0 : (g > 1 ? 1 : g);
+          w = g * w + (1 - g) * w / s;
+        }
+      }
+      turns[a * F + f] = (uint64_t)std::ldexp(w / kTwoPi, 64);
+    }
+}
+
+h3_status check_norm(const h3_norm_config* c, int32_t n_rows, int32_t n_heads) {
+  if (!c) return H3_ERR_NULL;
+  if (c->kind != H3_NORM_RMS && c->kind != H3_NORM_LAYER) return H3_ERR_UNSUPPORTED;
+  if ((c->dtype != H3_BF16 && c->dtype != H3_FP32) || (c->param_dtype != H3_BF16 && c->param_dtype != H3_FP32))
+    return H3_ERR_UNSUPPORTED;
+  if (c->width < 1) return H3_ERR_SHAPE;
+  if (c->width > kNormMaxWidth) return H3_ERR_UNSUPPORTED;
+  if (!(c->eps > 0.0f) || !std::isfinite(c->eps)) return H3_ERR_SHAPE;
+  if (n_rows < 1 || n_heads < 1) return H3_ERR_SHAPE;
+  return H3_OK;
+}
+int norm_part_width(int width) { return (width + 7) & ~7; }
+size_t norm_bwd_ws_bytes(const h3_norm_config& c, int64_t rows, int64_t heads) {
+  return al256((size_t)norm_bwd_ctas(rows * heads, c.width) * 2 * norm_part_width(c.width) * 4);
+}
+NormArgs norm_args(const h3_norm_config& c, int32_t n_rows, int32_t n_heads) {
+  NormArgs a{};
+  a.units = (long long)n_rows * n_heads;
+  a.heads = n_heads;
+  a.width = c.width;
+  a.layer = c.kind == H3_NORM_LAYER;
+  a.fp32 = c.dtype == H3_FP32;
+  a.param_fp32 = c.param_dtype == H3_FP32;
+  a.eps = c.eps;
+  a.part_width = norm_part_width(c.width);
+  a.err = device_error_word();
+  return a;
+}
+}  // namespace
+
+size_t h3_attention_backward_workspace_bytes(int32_t n_rows, int32_t n_heads) {
+  if (n_rows < 1 || n_heads < 1 || n_heads > 65535) return 0;
+  return attn_bwd_ws_bytes(n_rows, n_heads);
+}
+
+h3_status h3_attention_backward(int32_t n_rows, int32_t n_heads, const void* q, const void* k, const void* v,
+                                int64_t row_stride_elems, int64_t head_stride_elems, const void* o, const void* d_o,
+                                const float* lse, void* dq, void* dk, void* dv, int64_t d_row_stride_elems,
+                                int64_t d_head_stride_elems, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (n_rows < 1 || n_heads < 1 || n_heads > 65535) return H3_ERR_SHAPE;
+  if (!q || !k || !v || !o || !d_o || !lse || !dq || !dk || !dv || !workspace) return H3_ERR_NULL;
+  if (row_stride_elems < 128 || head_stride_elems < 128 || d_row_stride_elems < 128 || d_head_stride_elems < 128)
+    return H3_ERR_SHAPE;
+  if ((row_stride_elems & 7) || (head_stride_elems & 7) || (d_row_stride_elems & 7) || (d_head_stride_elems & 7))
+    return H3_ERR_ALIGN;
+  if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || !al16(d_o) || !al16(dq) || !al16(dk) || !al16(dv) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return H3_ERR_ALIGN;
+  const void* const in[] = {q, k, v, o, d_o, lse, workspace};
+  void* const out[] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* p : in)
+      if (out[i] == p) return H3_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return H3_ERR_SHAPE;
+  }
+  if (ws_bytes < attn_bwd_ws_bytes(n_rows, n_heads)) return H3_ERR_WORKSPACE;
+  CUtensorMap tq, tk, tv, to;
+  const uint64_t S = (uint64_t)n_rows, H = (uint64_t)n_heads;
+  if (!make_tmap_qkv(&tq, q, S, H, row_stride_elems, head_stride_elems, 128) ||
+      !make_tmap_qkv(&tk, k, S, H, row_stride_elems, head_stride_elems, 128) ||
+      !make_tmap_qkv(&tv, v, S, H, row_stride_elems, head_stride_elems, 128) ||
+      !make_tmap_qkv(&to, d_o, S, H, H * 128, 128, 128))
+    return H3_ERR_CUDA;
+  AttnBwdArgs a{};
+  a.S = n_rows;
+  a.H = n_heads;
+  a.tiles = (int)(((int64_t)n_rows + 127) / 128);
+  a.o = static_cast<const __nv_bfloat16*>(o);
+  a.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  a.lse = lse;
+  a.rowvals = static_cast<float*>(workspace);
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.d_row_stride = d_row_stride_elems;
+  a.d_head_stride = d_head_stride_elems;
+  a.scale = (float)(1.0 / std::sqrt(128.0));
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  a.o_elems = (size_t)S * H * 128;
+  a.lse_elems = (size_t)S * H;
+  a.rowval_elems = (size_t)a.tiles * H * 256;
+  a.d_elems = view_elems(n_rows, n_heads, 128, d_row_stride_elems, d_head_stride_elems);
+  a.err = device_error_word();
+  return cuda_st(launch_attention_bwd(tq, tk, tv, to, a, stream));
+}
+
+h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos, int32_t direction, const void* q_in,
+                  void* q_out, int32_t n_q_heads, const void* k_in, void* k_out, int32_t n_k_heads,
+                  int64_t in_row_stride_elems, int64_t in_head_stride_elems, int64_t out_row_stride_elems,
+                  int64_t out_head_stride_elems, cudaStream_t stream) {
+  h3_status s = check_rope(cfg);
+  if (s != H3_OK) return s;
+  if (n_rows < 1 || n_q_heads < 1 || n_k_heads < 0 || n_q_heads > 65535 || n_k_heads > 65535) return H3_ERR_SHAPE;
+  if (direction != H3_ROPE_FORWARD && direction != H3_ROPE_BACKWARD) return H3_ERR_UNSUPPORTED;
+  if (!pos || !q_in || !q_out || (n_k_heads > 0 && (!k_in || !k_out))) return H3_ERR_NULL;
+  const int heads = n_q_heads > n_k_heads ? n_q_heads : n_k_heads;
+  const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
+  if ((s = check_strides(cfg->head_dim, heads, in_row_stride_elems, in_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->head_dim, heads, out_row_stride_elems, out_head_stride_elems, unit)) != H3_OK) return s;
+  if (!al16(q_in) || !al16(q_out) || (n_k_heads > 0 && (!al16(k_in) || !al16(k_out))) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return H3_ERR_ALIGN;
+  const bool in_place = q_in == q_out;
+  if (n_k_heads > 0 && (in_place != (k_in == k_out) || k_out == q_out || k_out == q_in || q_out == k_in))
+    return H3_ERR_SHAPE;
+  if (in_place && (in_row_stride_elems != out_row_stride_elems ||
+                   (heads > 1 && in_head_stride_elems != out_head_stride_elems)))
+    return H3_ERR_SHAPE;
+  RopePosArgs a{};
+  a.rows = n_rows;
+  a.q_heads = n_q_heads;
+  a.k_heads = n_k_heads;
+  a.width = cfg->head_dim;
+  a.axes = cfg->n_axes;
+  a.freqs = cfg->n_freqs;
+  a.half = cfg->layout == H3_ROPE_HALF;
+  a.fp32 = cfg->dtype == H3_FP32;
+  a.in_place = in_place;
+  a.magnitude = cfg->magnitude;
+  a.sin_scale = direction == H3_ROPE_BACKWARD ? -cfg->magnitude : cfg->magnitude;
+  a.pos = pos;
+  a.q_in = q_in;
+  a.k_in = k_in;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.in_row = in_row_stride_elems;
+  a.in_head = heads > 1 ? in_head_stride_elems : 0;
+  a.out_row = out_row_stride_elems;
+  a.out_head = heads > 1 ? out_head_stride_elems : 0;
+  a.pos_elems = (size_t)n_rows * cfg->n_axes;
+  a.q_in_elems = view_elems(n_rows, n_q_heads, cfg->head_dim, a.in_row, a.in_head);
+  a.q_out_elems = view_elems(n_rows, n_q_heads, cfg->head_dim, a.out_row, a.out_head);
+  if (n_k_heads > 0) {
+    a.k_in_elems = view_elems(n_rows, n_k_heads, cfg->head_dim, a.in_row, a.in_head);
+    a.k_out_elems = view_elems(n_rows, n_k_heads, cfg->head_dim, a.out_row, a.out_head);
+  }
+  a.err = device_error_word();
+  fill_turns(*cfg, a.turns);
+  return cuda_st(launch_rope(a, stream));
+}
+
+h3_status h3_norm_forward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_heads, const void* x,
+                          int64_t x_row_stride_elems, int64_t x_head_stride_elems, const void* gain, const void* bias,
+                          void* y, int64_t y_row_stride_elems, int64_t y_head_stride_elems, cudaStream_t stream) {
+  h3_status s = check_norm(cfg, n_rows, n_heads);
+  if (s != H3_OK) return s;
+  if (!x || !y) return H3_ERR_NULL;
+  const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
+  if ((s = check_strides(cfg->width, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_heads, y_row_stride_elems, y_head_stride_elems, unit)) != H3_OK) return s;
+  if (!al16(x) || !al16(y) || !al16n(gain) || !al16n(bias)) return H3_ERR_ALIGN;
+  if (x == y && (x_row_stride_elems != y_row_stride_elems ||
+                 (n_heads > 1 && x_head_stride_elems != y_head_stride_elems)))
+    return H3_ERR_SHAPE;
+  NormArgs a = norm_args(*cfg, n_rows, n_heads);
+  a.x = x;
+  a.x_row = x_row_stride_elems;
+  a.x_head = n_heads > 1 ? x_head_stride_elems : 0;
+  a.y = y;
+  a.y_row = y_row_stride_elems;
+  a.y_head = n_heads > 1 ? y_head_stride_elems : 0;
+  a.gain = gain;
+  a.bias = bias;
+  a.x_elems = view_elems(n_rows, n_heads, cfg->width, a.x_row, a.x_head);
+  a.y_elems = view_elems(n_rows, n_heads, cfg->width, a.y_row, a.y_head);
+  return cuda_st(launch_norm_fwd(a, stream));
+}
+
+size_t h3_norm_backward_workspace_bytes(const h3_norm_config* cfg, int32_t n_rows, int32_t n_heads) {
+  if (check_norm(cfg, n_rows, n_heads) != H3_OK) return 0;
+  return norm_bwd_ws_bytes(*cfg, n_rows, n_heads);
+}
+
+h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_heads, const void* x,
+                           int64_t x_row_stride_elems, int64_t x_head_stride_elems, const void* gain, const void* dy,
+                           int64_t dy_row_stride_elems, int64_t dy_head_stride_elems, void* dx,
+                           int64_t dx_row_stride_elems, int64_t dx_head_stride_elems, float* dgain, float* dbias,
+                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  h3_status s = check_norm(cfg, n_rows, n_heads);
+  if (s != H3_OK) return s;
+  const bool params = dgain || dbias;
+  if (!x || !dy || !dx || (params && !workspace)) return H3_ERR_NULL;
+  const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
+  if ((s = check_strides(cfg->width, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_heads, dy_row_stride_elems, dy_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_heads, dx_row_stride_elems, dx_head_stride_elems, unit)) != H3_OK) return s;
+  if (!al16(x) || !al16(dy) || !al16(dx) || !al16n(gain) || (reinterpret_cast<uintptr_t>(dgain) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dbias) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return H3_ERR_ALIGN;
+  auto same = [&](const void* p, int64_t row, int64_t head) {
+    return p != dx || (row == dx_row_stride_elems && (n_heads == 1 || head == dx_head_stride_elems));
+  };
+  if (!same(x, x_row_stride_elems, x_head_stride_elems) || !same(dy, dy_row_stride_elems, dy_head_stride_elems) ||
+      (dgain && dgain == dbias))
+    return H3_ERR_SHAPE;
+  if (params && ws_bytes < norm_bwd_ws_bytes(*cfg, n_rows, n_heads)) return H3_ERR_WORKSPACE;
+  NormArgs a = norm_args(*cfg, n_rows, n_heads);
+  a.x = x;
+  a.x_row = x_row_stride_elems;
+  a.x_head = n_heads > 1 ? x_head_stride_elems : 0;
+  a.dy = dy;
+  a.dy_row = dy_row_stride_elems;
+  a.dy_head = n_heads > 1 ? dy_head_stride_elems : 0;
+  a.dx = dx;
+  a.dx_row = dx_row_stride_elems;
+  a.dx_head = n_heads > 1 ? dx_head_stride_elems : 0;
+  a.gain = gain;
+  a.part = params ? static_cast<float*>(workspace) : nullptr;
+  a.x_elems = view_elems(n_rows, n_heads, cfg->width, a.x_row, a.x_head);
+  a.dy_elems = view_elems(n_rows, n_heads, cfg->width, a.dy_row, a.dy_head);
+  a.dx_elems = view_elems(n_rows, n_heads, cfg->width, a.dx_row, a.dx_head);
+  a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width) * 2 * a.part_width : 0;
+  return cuda_st(launch_norm_bwd(a, dgain, dbias, stream));
 }
 
 h3_status h3_out_projection(const h3_block_config* cfg, const h3_packed_meta* meta, const void* table,

@@ -36,6 +36,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // Kernel ids of the first timed-out wait (top byte of the site word).
 enum : uint32_t {
   KID_GEMM = 1u, KID_ATTN_1Q = 2u, KID_ATTN_2Q = 3u, KID_ADALN = 4u, KID_ROPE = 5u,
+  KID_ATTN_BWD = 6u,
 };
 // Low 24 bits of the site word for a wait that is not on an mbarrier.
 constexpr uint32_t kSiteStreamKFlag = 0xFFFFFFu;

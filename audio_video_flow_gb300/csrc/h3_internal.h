@@ -275,6 +275,66 @@ cudaError_t launch_attention(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
                              const AttnArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// attention gradient (tcgen05, k_attention_bwd.cu)
+// ---------------------------------------------------------------------------
+struct AttnBwdArgs {
+  int S, H;
+  int tiles;              // 128-row tiles: ceil(S / 128)
+  const __nv_bfloat16* o;     // [S][H*128]
+  const __nv_bfloat16* d_o;   // [S][H*128]
+  const float* lse;           // [H][S]
+  float* rowvals;             // workspace [H][tiles][2][128]: lse * log2(e), rowsum(dO o O)
+  __nv_bfloat16 *dq, *dk, *dv;
+  int64_t d_row_stride, d_head_stride;
+  float scale;                // 1 / sqrt(128)
+  float scale_log2;           // log2(e) / sqrt(128)
+  size_t o_elems, lse_elems, rowval_elems, d_elems;   // extents for the bounds-checked build
+  uint32_t* err;
+};
+cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                 const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// row norms (k_norm.cu) and rotary positions (k_rope.cu)
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  long long units;            // rows x heads
+  int heads, width;
+  int layer, fp32, param_fp32;
+  float eps;
+  const void *x, *dy;
+  int64_t x_row, x_head, dy_row, dy_head;
+  void *y, *dx;
+  int64_t y_row, y_head, dx_row, dx_head;
+  const void *gain, *bias;    // nullable
+  float* part;                // backward: [ctas][2][part_width] sums of dgain and dbias, or null
+  int part_width;             // width rounded up to a multiple of 8
+  size_t x_elems, dy_elems, y_elems, dx_elems, part_elems;   // extents for the bounds-checked build
+  uint32_t* err;
+};
+constexpr int kNormMaxWidth = 8192;
+int norm_bwd_ctas(long long units, int width);   // CTAs of the backward kernel on this GPU
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs& a, float* dgain, float* dbias, cudaStream_t st);
+
+constexpr int kRopeMaxPairs = 128;    // rotated pairs of a head (axes x frequencies)
+constexpr int kRopeMaxWidth = 256;    // channels of a head
+struct RopePosArgs {
+  int rows, q_heads, k_heads, width;
+  int axes, freqs, half, fp32, in_place;
+  int heads_per_cta;          // set by the launcher
+  float magnitude, sin_scale; // sin_scale: -magnitude for the gradient
+  const int32_t* pos;         // [rows][axes]
+  const void *q_in, *k_in;
+  void *q_out, *k_out;
+  int64_t in_row, in_head, out_row, out_head;
+  size_t pos_elems, q_in_elems, k_in_elems, q_out_elems, k_out_elems;   // for the bounds-checked build
+  uint32_t* err;
+  uint64_t turns[kRopeMaxPairs];   // turns per position, 2^64 = one turn
+};
+cudaError_t launch_rope(RopePosArgs a, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
 // row-wise kernels
 // ---------------------------------------------------------------------------
 struct ModulateArgs {

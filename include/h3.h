@@ -337,6 +337,130 @@ h3_status h3_attention(int32_t n_rows, int32_t n_heads, const void *q, const voi
                        const void *v, int64_t row_stride_elems, int64_t head_stride_elems,
                        void *o, float *lse_opt, cudaStream_t stream);
 
+/* Gradient of h3_attention (RFC s5 lists backward kernels among the work
+ * items).  q, k, v and their strides as given to the forward call, o its
+ * output, lse its log-sum-exp (required here), d_o the gradient of o (bf16
+ * [S][H*128]).  With P = exp(q k^T / sqrt(128) - lse), recomputed, and
+ * D_i = sum_c d_o[i][c] o[i][c]:
+ *   dv_j = sum_i P_ij d_o_i
+ *   dS_ij = P_ij (d_o_i . v_j - D_i)
+ *   dq_i = sum_j dS_ij k_j / sqrt(128),   dk_j = sum_i dS_ij q_i / sqrt(128)
+ * in fp32, P and dS rounded to bf16 for the products, each result rounded
+ * once to bf16.  dq, dk, dv: element (row i, head h, channel c) at
+ * ptr + i*d_row_stride + h*d_head_stride + c (strides in elements, multiples
+ * of 8, as the slots of a packed [S][H][3][128] tensor or three tensors of
+ * their own); they must overlap neither each other nor any input
+ * (H3_ERR_SHAPE where two of the pointers are equal).  Nothing else is
+ * written.  The result is bitwise repeatable: no atomics.
+ * workspace: device, 256-byte aligned, at least
+ * h3_attention_backward_workspace_bytes (0 for invalid sizes); scratch of one
+ * call, so calls that can overlap on the GPU need one each. */
+size_t h3_attention_backward_workspace_bytes(int32_t n_rows, int32_t n_heads);
+h3_status h3_attention_backward(int32_t n_rows, int32_t n_heads, const void *q, const void *k,
+                                const void *v, int64_t row_stride_elems, int64_t head_stride_elems,
+                                const void *o, const void *d_o, const float *lse, void *dq, void *dk,
+                                void *dv, int64_t d_row_stride_elems, int64_t d_head_stride_elems,
+                                void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Element types of the norm and rotary calls below. */
+typedef enum { H3_BF16 = 0, H3_FP32 = 1 } h3_dtype;
+
+/* Rotary positions in their general form (h3_rope_qknorm is the H3 block's own
+ * fixed case, fused with the Q/K norm).  Of a head's head_dim channels the
+ * first 2 * n_axes * n_freqs are rotated, the others pass through.  Pair
+ * j = a * n_freqs + f holds channels
+ *   (j, j + n_axes * n_freqs)  (H3_ROPE_HALF)  or  (2j, 2j + 1)  (H3_ROPE_INTERLEAVED)
+ * and turns by the angle pos[i][a] * omega[a][f]:
+ *   (x0, x1) -> m (x0 cos - x1 sin, x0 sin + x1 cos),   m = magnitude.
+ * omega[a][f] = theta^(-f / n_freqs), changed on the axes in the bit mask
+ * scaled_axes, for positions beyond the trained length:
+ *   H3_ROPE_SCALE_NONE    omega
+ *   H3_ROPE_SCALE_LINEAR  omega / factor (position interpolation)
+ *   H3_ROPE_SCALE_NTK     (theta * factor^(F/(F-1)))^(-f/F), F = n_freqs >= 2: the
+ *                         highest frequency kept, the lowest divided by factor
+ *   H3_ROPE_SCALE_YARN    by parts: with r = trained_length * omega / (2 pi) turns
+ *                         over the trained length and g = (r - alpha) / (beta - alpha)
+ *                         clipped to [0, 1]:  g omega + (1 - g) omega / factor
+ * Angles are exact to 2^-31 of a turn for every 32-bit position, negative ones
+ * included.  Limits: head_dim even, 2 .. 256; n_axes 1 .. 4;
+ * 1 <= n_axes * n_freqs <= 128, 2 * n_axes * n_freqs <= head_dim
+ * (H3_ERR_UNSUPPORTED); theta > 1, factor >= 1, trained_length >= 1,
+ * 0 <= alpha < beta, magnitude finite and > 0, scaled_axes inside the axes
+ * (H3_ERR_SHAPE; factor, trained_length, alpha, beta and scaled_axes are only
+ * looked at where the scaling uses them). */
+typedef enum { H3_ROPE_HALF = 0, H3_ROPE_INTERLEAVED = 1 } h3_rope_layout;
+typedef enum {
+  H3_ROPE_SCALE_NONE = 0, H3_ROPE_SCALE_LINEAR = 1, H3_ROPE_SCALE_NTK = 2, H3_ROPE_SCALE_YARN = 3
+} h3_rope_scaling;
+typedef enum { H3_ROPE_FORWARD = 0, H3_ROPE_BACKWARD = 1 } h3_rope_direction;
+typedef struct {
+  int32_t head_dim, n_axes, n_freqs;
+  int32_t layout;              /* h3_rope_layout */
+  int32_t dtype;               /* h3_dtype of q and k */
+  int32_t scaling;             /* h3_rope_scaling */
+  int32_t scaled_axes;         /* bit a: axis a is scaled */
+  float theta, factor;
+  float trained_length, alpha, beta;   /* H3_ROPE_SCALE_YARN */
+  float magnitude;             /* 1 for none */
+} h3_rope_config;
+
+/* Rotary positions of q and k: element (row i, head h, channel c) at
+ * ptr + i*row_stride + h*head_stride + c, q with n_q_heads heads and k with
+ * n_k_heads (0 with k NULL: q alone), pos int32 [n_rows][n_axes].
+ * H3_ROPE_BACKWARD applies the transpose (the turn by the opposite angle, the
+ * same magnitude): from the gradients of the turned q and k to those of q and
+ * k.  fp32 arithmetic, one rounding.  Each output may be its input, with equal
+ * strides (in place: the channels that pass through are then not touched), else they must not
+ * overlap.  In place for one of q and k and not for the other is refused
+ * (H3_ERR_SHAPE).  Strides are in elements, multiples of 16 bytes. */
+h3_status h3_rope(const h3_rope_config *cfg, int32_t n_rows, const int32_t *pos, int32_t direction,
+                  const void *q_in, void *q_out, int32_t n_q_heads, const void *k_in, void *k_out,
+                  int32_t n_k_heads, int64_t in_row_stride_elems, int64_t in_head_stride_elems,
+                  int64_t out_row_stride_elems, int64_t out_head_stride_elems, cudaStream_t stream);
+
+/* Layer norm and RMS norm over rows of `width` channels (1 .. 8192, any
+ * number; H3_ERR_UNSUPPORTED beyond).  dtype: x, y and their gradients;
+ * param_dtype: gain and bias.  eps > 0. */
+typedef enum { H3_NORM_RMS = 0, H3_NORM_LAYER = 1 } h3_norm_kind;
+typedef struct {
+  int32_t kind;                /* h3_norm_kind */
+  int32_t width;
+  int32_t dtype, param_dtype;  /* h3_dtype */
+  float eps;
+} h3_norm_config;
+
+/* Forward, for every row i < n_rows and head h < n_heads (1 for plain rows),
+ * on the `width` channels at x + i*x_row_stride + h*x_head_stride:
+ *   c = x - mean(x) (H3_NORM_LAYER) or x (H3_NORM_RMS)
+ *   y = c / sqrt(mean(c^2) + eps) * gain + bias      (fp32, one rounding)
+ * gain and bias [width], each may be NULL (1 and 0).  y may be x with equal
+ * strides, else they must not overlap.  Strides are in elements, multiples of
+ * 16 bytes; with n_heads = 1 the head strides are not looked at. */
+h3_status h3_norm_forward(const h3_norm_config *cfg, int32_t n_rows, int32_t n_heads, const void *x,
+                          int64_t x_row_stride_elems, int64_t x_head_stride_elems, const void *gain,
+                          const void *bias, void *y, int64_t y_row_stride_elems,
+                          int64_t y_head_stride_elems, cudaStream_t stream);
+
+/* Backward of the same: from x (the forward's input; the statistics are
+ * computed again), gain (or NULL) and dy,
+ *   xhat = c / sqrt(mean(c^2) + eps),  w = dy * gain
+ *   dx = (w - xhat mean(w xhat) - mean(w)) / sqrt(mean(c^2) + eps)
+ *                                         (mean(w) for H3_NORM_LAYER alone)
+ *   dgain = sum over rows and heads of dy xhat,  dbias = the same sum of dy
+ * dgain, dbias: fp32 [width], overwritten, each may be NULL.  dx may be dy or x
+ * with equal strides, else it must not overlap them.  Bitwise repeatable: the
+ * parameter gradients are summed in an order fixed by the row count and the
+ * GPU.  workspace: device, 256-byte aligned, at least
+ * h3_norm_backward_workspace_bytes (0 for invalid arguments; not used and may
+ * be NULL when dgain and dbias are NULL); scratch of one call. */
+size_t h3_norm_backward_workspace_bytes(const h3_norm_config *cfg, int32_t n_rows, int32_t n_heads);
+h3_status h3_norm_backward(const h3_norm_config *cfg, int32_t n_rows, int32_t n_heads, const void *x,
+                           int64_t x_row_stride_elems, int64_t x_head_stride_elems, const void *gain,
+                           const void *dy, int64_t dy_row_stride_elems, int64_t dy_head_stride_elems,
+                           void *dx, int64_t dx_row_stride_elems, int64_t dx_head_stride_elems,
+                           float *dgain, float *dbias, void *workspace, size_t ws_bytes,
+                           cudaStream_t stream);
+
 /* Output projection + gated residual of the attention branch (RFC s5
  * h3_attention_o_gemm and adaln_gate_residual; s4: residual plus the row's
  * gate times the sublayer output, in that order):  x_out = bf16(x + gate_msa[r] bf16(o W_o^T + b_o)).
@@ -534,7 +658,7 @@ h3_status h3_last_kernel_info(char *buf, size_t len);
 /* Where the first device-side wait that ran out was, as recorded on the
  * device and read by the most recent h3_sync_check of this process that
  * returned H3_ERR_TIMEOUT: "none", or the kernel ("gemm", "attention-1q",
- * "attention-2q", "adaln-table", "rope-qknorm") and the wait (an mbarrier at
+ * "attention-2q", "adaln-table", "rope-qknorm", "attention-backward") and the wait (an mbarrier at
  * a shared-memory byte offset, or a stream-K partial-sum flag).  Diagnostic
  * only: the pages define no counterpart.  Writes a NUL-terminated string of
  * at most len bytes; H3_ERR_NULL when buf is NULL or len is 0. */
