@@ -1264,30 +1264,62 @@ h3_status check_rope(const h3_rope_config* c) {
   return H3_OK;
 }
 
-// Turns per position of every rotated pair in 64-bit fixed point; omega <= 1
-// radian, so a turn fraction below 1/6.  In long double: a position of 2^31
-// multiplies omega's rounding into 2^-24 turns where omega is a double.
+// High half of a 128 x 128-bit product: both factors fractions of 2^128.
+typedef unsigned __int128 u128;
+u128 mul_hi(u128 a, u128 b) {
+  const uint64_t al = (uint64_t)a, ah = (uint64_t)(a >> 64), bl = (uint64_t)b, bh = (uint64_t)(b >> 64);
+  const u128 ll = (u128)al * bl, lh = (u128)al * bh, hl = (u128)ah * bl, hh = (u128)ah * bh;
+  const u128 mid = (ll >> 64) + (uint64_t)lh + (uint64_t)hl;
+  return hh + (lh >> 64) + (hl >> 64) + (mid >> 64);
+}
+u128 fraction(long double x) {   // 0 <= x < 1
+  const long double hi = std::ldexp(x, 64);
+  const uint64_t top = (uint64_t)hi;
+  return ((u128)top << 64) | (uint64_t)std::ldexp(hi - (long double)top, 64);
+}
+
+// Turns per position of every rotated pair in 64-bit fixed point (omega <= 1
+// radian, so below 1/6): a geometric series, its ratio and products held as
+// 128-bit fractions, since a position of 2^31 would multiply the rounding of a
+// double into 2^-24 turns, and a pow per frequency costs more than the launch.
 void fill_turns(const h3_rope_config& c, uint64_t* turns) {
   typedef long double real;
-  const real kTwoPi = 6.283185307179586476925286766559005768L;
+  const real kInvTwoPi = 0.15915494309189533576888376337251436203L;
   const int F = c.n_freqs;
-  for (int a = 0; a < c.n_axes; ++a)
+  bool done[2] = {false, false};
+  int at[2] = {0, 0};
+  for (int a = 0; a < c.n_axes; ++a) {
+    const int scaled = c.scaling != H3_ROPE_SCALE_NONE && ((c.scaled_axes >> a) & 1);
+    if (done[scaled]) {   // the axes of one kind share their frequencies
+      std::memcpy(turns + a * F, turns + at[scaled] * F, (size_t)F * sizeof(uint64_t));
+      continue;
+    }
+    done[scaled] = true;
+    at[scaled] = a;
+    const real s = c.factor;
+    real first = kInvTwoPi, base = c.theta;
+    if (scaled && c.scaling == H3_ROPE_SCALE_LINEAR) first /= s;
+    if (scaled && c.scaling == H3_ROPE_SCALE_NTK) base *= std::pow(s, (real)F / (F - 1));
+    const u128 ratio = F > 1 ? fraction(std::pow(base, (real)-1 / F)) : 0;
+    u128 w = fraction(first);
     for (int f = 0; f < F; ++f) {
-      const real e = -(real)f / F, s = c.factor;
-      real w = std::pow((real)c.theta, e);
-      if (c.scaling != H3_ROPE_SCALE_NONE && ((c.scaled_axes >> a) & 1)) {
-        if (c.scaling == H3_ROPE_SCALE_LINEAR) {
-          w /= s;
-        } else if (c.scaling == H3_ROPE_SCALE_NTK) {
-          w = std::pow((real)c.theta * std::pow(s, (real)F / (F - 1)), e);
-        } else {
-          real g = ((real)c.trained_length * w / kTwoPi - c.alpha) / ((real)c.beta - c.alpha);
-          g = g < 0 ? 0 : (g > 1 ? 1 : g);
-          w = g * w + (1 - g) * w / s;
+      u128 t = w;
+      if (scaled && c.scaling == H3_ROPE_SCALE_YARN) {
+        // turns over the trained length, and by them the share kept
+        const double n = (double)c.trained_length * std::ldexp((double)(uint64_t)(w >> 64), -64);
+        if (n <= c.alpha) {
+          t = s > 1 ? mul_hi(w, fraction(1 / s)) : w;
+        } else if (n < c.beta) {
+          const real nn = (real)c.trained_length * std::ldexp((real)(uint64_t)(w >> 64), -64);
+          const real g = (nn - c.alpha) / ((real)c.beta - c.alpha);
+          const real keep = g + (1 - g) / s;
+          if (keep < 1) t = mul_hi(w, fraction(keep));
         }
       }
-      turns[a * F + f] = (uint64_t)std::ldexp(w / kTwoPi, 64);
+      turns[a * F + f] = (uint64_t)(t >> 64);
+      w = mul_hi(w, ratio);
     }
+  }
 }
 
 h3_status check_norm(const h3_norm_config* c, int32_t n_rows, int32_t n_heads) {
@@ -1303,7 +1335,7 @@ h3_status check_norm(const h3_norm_config* c, int32_t n_rows, int32_t n_heads) {
 }
 int norm_part_width(int width) { return (width + 7) & ~7; }
 size_t norm_bwd_ws_bytes(const h3_norm_config& c, int64_t rows, int64_t heads) {
-  return al256((size_t)norm_bwd_ctas(rows * heads, c.width) * 2 * norm_part_width(c.width) * 4);
+  return al256((size_t)norm_bwd_ctas(rows * heads, c.width, c.dtype == H3_FP32) * 2 * norm_part_width(c.width) * 4);
 }
 NormArgs norm_args(const h3_norm_config& c, int32_t n_rows, int32_t n_heads) {
   NormArgs a{};
@@ -1502,7 +1534,7 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   a.x_elems = view_elems(n_rows, n_heads, cfg->width, a.x_row, a.x_head);
   a.dy_elems = view_elems(n_rows, n_heads, cfg->width, a.dy_row, a.dy_head);
   a.dx_elems = view_elems(n_rows, n_heads, cfg->width, a.dx_row, a.dx_head);
-  a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width) * 2 * a.part_width : 0;
+  a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width, a.fp32) * 2 * a.part_width : 0;
   return cuda_st(launch_norm_bwd(a, dgain, dbias, stream));
 }
 

@@ -300,6 +300,7 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
 struct NormArgs {
   long long units;            // rows x heads
   int heads, width;
+  int tpr;                    // threads per row, set by the launchers
   int layer, fp32, param_fp32;
   float eps;
   const void *x, *dy;
@@ -313,16 +314,16 @@ struct NormArgs {
   uint32_t* err;
 };
 constexpr int kNormMaxWidth = 8192;
-int norm_bwd_ctas(long long units, int width);   // CTAs of the backward kernel on this GPU
-cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormArgs& a, float* dgain, float* dbias, cudaStream_t st);
+int norm_bwd_ctas(long long units, int width, bool fp32);   // CTAs of the backward kernel on this GPU
+cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st);
+cudaError_t launch_norm_bwd(NormArgs a, float* dgain, float* dbias, cudaStream_t st);
 
 constexpr int kRopeMaxPairs = 128;    // rotated pairs of a head (axes x frequencies)
 constexpr int kRopeMaxWidth = 256;    // channels of a head
 struct RopePosArgs {
   int rows, q_heads, k_heads, width;
   int axes, freqs, half, fp32, in_place;
-  int heads_per_cta;          // set by the launcher
+  int heads_per_cta, units;   // set by the launcher: heads of one CTA, units of a head
   float magnitude, sin_scale; // sin_scale: -magnitude for the gradient
   const int32_t* pos;         // [rows][axes]
   const void *q_in, *k_in;

@@ -13,180 +13,257 @@
 // sums of squares would lose a row whose mean is large).  Every reduction has
 // a fixed order, so results repeat bit for bit.
 //
-// Channels are handled in chunks of 8: thread t of a row's TPR threads owns
-// chunks t, t + TPR, ...; only the last chunk of a row may be partial.
+// Channels are handled in chunks of 8: thread t of a row's `tpr` threads owns
+// chunks t, t + tpr, ...; only the last chunk of a row may be partial.  Rows of
+// at most 1024 channels belong to a group of up to 32 threads, which reduces by
+// shuffles alone, several groups to a CTA; wider rows to a whole CTA.
 #include "h3_device.cuh"
 #include "h3_internal.h"
 
+#include <mutex>
 #include <type_traits>
+#include <vector>
 
 namespace h3 {
 
 namespace {
-constexpr int NORM_FWD_BATCH_THREADS = 256;
+constexpr int NORM_GROUP_THREADS = 256;   // CTA of rows of at most 1024 channels
+constexpr int NORM_GROUP_CHUNKS = 128;    // the widest such row
+constexpr int NORM_MAX_WARPS = 8;
 
-// 8 values at p, of which the first `valid` exist (the others read as 0).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int valid, float (&v)[8]) {
-  if (valid >= 8) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight channels as they lie in memory.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_part(const __nv_bfloat16* p, int valid) {
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[2 * e] = bf16_lo(w[e]);
-      v[2 * e + 1] = bf16_hi(w[e]);
+      const uint32_t lo = 2 * e < valid ? reinterpret_cast<const uint16_t*>(p)[2 * e] : 0u;
+      const uint32_t hi = 2 * e + 1 < valid ? reinterpret_cast<const uint16_t*>(p)[2 * e + 1] : 0u;
+      w[e] = lo | (hi << 16);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < valid ? __bfloat162float(p[e]) : 0.0f;
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-__device__ __forceinline__ void load8(const float* p, int valid, float (&v)[8]) {
-  if (valid >= 8) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < valid ? p[e] : 0.0f;
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    v[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+    v[2] = make_float2(bf16_lo(r.z), bf16_hi(r.z));
+    v[3] = make_float2(bf16_lo(r.w), bf16_hi(r.w));
   }
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int valid, const float (&v)[8]) {
+};
+template <>
+struct Chunk<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void load_part(const float* p, int valid) {
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = e < valid ? p[e] : 0.0f;
+    a = make_float4(w[0], w[1], w[2], w[3]);
+    b = make_float4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+  }
+};
+// the first `valid` of eight results, each rounded once
+__device__ __forceinline__ void put8(__nv_bfloat16* p, int valid, const float2 (&v)[4]) {
   if (valid >= 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                              pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < valid) p[e] = __float2bfloat16_rn(v[e]);
+      if (e < valid) p[e] = __float2bfloat16_rn((e & 1) ? v[e >> 1].y : v[e >> 1].x);
   }
 }
-__device__ __forceinline__ void store8(float* p, int valid, const float (&v)[8]) {
+__device__ __forceinline__ void put8(float* p, int valid, const float2 (&v)[4]) {
   if (valid >= 8) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < valid) p[e] = v[e];
+      if (e < valid) p[e] = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
   }
 }
-// gain or bias (either type; null reads as `none`)
-__device__ __forceinline__ void load_param8(const void* p, int is_fp32, int at, int valid, float none, float (&v)[8]) {
+// 8 channels of gain or bias (either type; null reads as `none`)
+__device__ __forceinline__ void param8(const void* p, int is_fp32, int at, int valid, float none, float2 (&v)[4]) {
   if (p == nullptr) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = none;
+    for (int e = 0; e < 4; ++e) v[e] = make_float2(none, none);
   } else if (is_fp32) {
-    load8(static_cast<const float*>(p) + at, valid, v);
+    Chunk<float> c;
+    if (valid >= 8) c.load(static_cast<const float*>(p) + at);
+    else c.load_part(static_cast<const float*>(p) + at, valid);
+    c.get(v);
   } else {
-    load8(static_cast<const __nv_bfloat16*>(p) + at, valid, v);
+    Chunk<__nv_bfloat16> c;
+    if (valid >= 8) c.load(static_cast<const __nv_bfloat16*>(p) + at);
+    else c.load_part(static_cast<const __nv_bfloat16*>(p) + at, valid);
+    c.get(v);
+  }
+}
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void zero_past(float2 (&v)[4], int valid) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (2 * e >= valid) v[e].x = 0.0f;
+    if (2 * e + 1 >= valid) v[e].y = 0.0f;
   }
 }
 
-// Sum over the row's TPR threads, the same value in all of them: a butterfly
-// inside a warp, then the warps' sums in order.  slot: the group's scratch,
-// not read since the last __syncthreads before the previous use of the other
-// slot (callers alternate two).
-template <int TPR, int NV>
-__device__ __forceinline__ void row_sum(float (&s)[NV], float* slot) {
-  constexpr int W = TPR < 32 ? TPR : 32;
+// NV sums over a row's threads, the same value in all of them: a butterfly
+// inside the group (or warp), then the CTA's warps in order.  slot: scratch of
+// NORM_MAX_WARPS * NV floats; two calls in a row need different ones.
+template <bool BLOCK, int NV>
+__device__ __forceinline__ void row_sum(float (&s)[NV], int tpr, float* slot) {
+  if (BLOCK) {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < NV; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-  if (TPR > 32) {
-    constexpr int NW = TPR / 32;
-    const int warp = threadIdx.x >> 5;
+      for (int k = 0; k < NV; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    const int warp = threadIdx.x >> 5, nw = tpr >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int k = 0; k < NV; ++k) slot[warp * NV + k] = s[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float t = 0.0f;
+    for (int k = 0; k < NV; ++k) s[k] = slot[k];
 #pragma unroll
-      for (int w = 0; w < NW; ++w) t += slot[w * NV + k];
-      s[k] = t;
-    }
+    for (int w = 1; w < NORM_MAX_WARPS; ++w)
+      if (w < nw)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) s[k] += slot[w * NV + k];
+  } else {
+    for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
   }
 }
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Forward: TPR threads per row, NC chunks per thread, the row read once into
-// registers and written once.
+// Forward: R rows per thread group at a time, NC chunks of each row per
+// thread, kept in registers as read; every row is read and written once.
+// Bound by memory.  Few threads with many chunks each keep more rows, and so
+// more bytes, in flight on an SM than many threads with few.
 // ---------------------------------------------------------------------------
-template <typename T, int TPR, int NC, bool LAYER>
-__global__ void __launch_bounds__(TPR < NORM_FWD_BATCH_THREADS && TPR <= 32 ? NORM_FWD_BATCH_THREADS : TPR)
-    norm_fwd_kernel(const NormArgs a) {
+template <typename T, int NC, int R, bool LAYER, bool BLOCK>
+__global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const NormArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int RPB = TPR <= 32 ? NORM_FWD_BATCH_THREADS / TPR : 1;    // rows per block
-  __shared__ float red[2][32];
-  const int t = threadIdx.x % TPR;
-  const long long unit = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool have = unit < a.units;
-  const long long u = have ? unit : 0;
-  const int64_t i = u / a.heads, h = u % a.heads;
-  const T* x = static_cast<const T*>(a.x) + i * a.x_row + h * a.x_head;
-  T* y = static_cast<T*>(a.y) + i * a.y_row + h * a.y_head;
+  __shared__ float red[2][NORM_MAX_WARPS * R];
+  const int tpr = a.tpr;
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & (tpr - 1);
+  const int g = BLOCK ? 0 : threadIdx.x / tpr;
+  const int groups = BLOCK ? 1 : NORM_GROUP_THREADS / tpr;
   const int width = a.width;
-  float v[NC][8];
-  float s[1] = {0.0f};
+  const float inv_width = 1.0f / (float)width;
+  Chunk<T> raw[R][NC];
+  T* y[R];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int at = (t + c * TPR) * 8;
-    const int valid = min(width - at, 8);
-    if (have && valid > 0 && in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, x + at, valid, a.err, 50)) {
-      load8(x + at, valid, v[c]);
-    } else {
+  for (int k = 0; k < R; ++k) {
+    const long long u = ((long long)blockIdx.x * R + k) * groups + g;
+    y[k] = nullptr;
+    if (u < a.units) {
+      const int64_t i = a.heads == 1 ? u : u / a.heads, h = a.heads == 1 ? 0 : u - i * a.heads;
+      const T* x = static_cast<const T*>(a.x) + i * a.x_row + h * a.x_head;
+      y[k] = static_cast<T*>(a.y) + i * a.y_row + h * a.y_head;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = 0.0f;
+      for (int c = 0; c < NC; ++c) {
+        const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
+        if (valid <= 0 || !in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, x + at, valid, a.err, 50)) continue;
+        if (valid == 8) raw[k][c].load(x + at);
+        else raw[k][c].load_part(x + at, valid);
+      }
     }
   }
-  const float inv_width = 1.0f / (float)width;
+  float mean[R], s[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    mean[k] = 0.0f;
+    if (LAYER) {
+      float2 acc = splat(0.0f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (y[k] == nullptr || (t + c * tpr) * 8 >= width) continue;
+        float2 v[4];
+        raw[k][c].get(v);
+        acc = __fadd2_rn(acc, __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3])));
+      }
+      s[k] = acc.x + acc.y;
+    }
+  }
   if (LAYER) {
+    row_sum<BLOCK>(s, tpr, red[0]);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int k = 0; k < R; ++k) mean[k] = s[k] * inv_width;
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[c][e];
-    row_sum<TPR>(s, red[0]);
-    const float mean = s[0] * inv_width;
+  for (int k = 0; k < R; ++k) {
+    float2 acc = splat(0.0f);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int valid = width - (t + c * TPR) * 8;
+      const int at = (t + c * tpr) * 8;
+      if (y[k] == nullptr || at >= width) continue;
+      float2 v[4];
+      raw[k][c].get(v);
+      if (LAYER) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = e < valid ? v[c][e] - mean : 0.0f;
+        for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], splat(-mean[k]));
+        if (width - at < 8) zero_past(v, width - at);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = __ffma2_rn(v[e], v[e], acc);
     }
-    s[0] = 0.0f;
+    s[k] = acc.x + acc.y;
   }
+  row_sum<BLOCK>(s, tpr, red[1]);
+  float r[R];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[0] = __fmaf_rn(v[c][e], v[c][e], s[0]);
-  row_sum<TPR>(s, red[1]);
-  const float r = 1.0f / sqrtf(s[0] * inv_width + a.eps);
-  if (!have) return;
+  for (int k = 0; k < R; ++k) r[k] = 1.0f / sqrtf(s[k] * inv_width + a.eps);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int at = (t + c * TPR) * 8;
-    const int valid = min(width - at, 8);
+    const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
     if (valid <= 0) continue;
-    float g[8], b[8];
-    load_param8(a.gain, a.param_fp32, at, valid, 1.0f, g);
-    load_param8(a.bias, a.param_fp32, at, valid, 0.0f, b);
+    float2 gn[4], bs[4];
+    param8(a.gain, a.param_fp32, at, valid, 1.0f, gn);
+    param8(a.bias, a.param_fp32, at, valid, 0.0f, bs);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = __fmaf_rn(v[c][e] * r, g[e], b[e]);
-    if (in_bounds<T>(static_cast<const T*>(a.y), a.y_elems, y + at, valid, a.err, 51)) store8(y + at, valid, g);
+    for (int k = 0; k < R; ++k) {
+      if (y[k] == nullptr) continue;
+      float2 v[4];
+      raw[k][c].get(v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (LAYER) v[e] = __fadd2_rn(v[e], splat(-mean[k]));
+        v[e] = __ffma2_rn(__fmul2_rn(v[e], splat(r[k])), gn[e], bs[e]);
+      }
+      if (in_bounds<T>(static_cast<const T*>(a.y), a.y_elems, y[k] + at, valid, a.err, 51)) put8(y[k] + at, valid, v);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Persistent CTAs; each row's x and dy are copied asynchronously
-// into a ring of NORM_STAGES stages (each thread copies and later reads its
-// own chunks, so a stage needs no barrier), the gain is kept in shared memory
-// as fp32, and every thread accumulates dgain and dbias of its own channels
-// in registers over all the CTA's rows.  The CTA's sums go to the workspace
-// and norm_param_kernel adds them in CTA order.
+// Backward.  Persistent CTAs take R rows per thread group and step.  The x and
+// dy of a step are copied asynchronously into a ring of two stages one step
+// ahead (each thread copies and later reads its own chunks, so a stage needs
+// no barrier); the gain is kept in shared memory as fp32; every thread
+// accumulates dgain (and, with BIAS, dbias) of its own channels in registers
+// over all the CTA's rows.  The CTAs' sums go to the workspace, where
+// norm_param_kernel adds them in CTA order.  R rows at a time share the
+// reductions' latency and keep more bytes in flight.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int NORM_STAGES = 2;
@@ -211,187 +288,247 @@ __device__ __forceinline__ void copy8(T* dst, const T* src, int valid) {
 }
 }  // namespace
 
-template <typename T, int TPR, int NC, bool LAYER>
-__global__ void __launch_bounds__(TPR <= 32 ? 256 : TPR) norm_bwd_kernel(const NormArgs a) {
-  constexpr int NT = TPR <= 32 ? 256 : TPR;
-  constexpr int RPB = NT / TPR;                   // rows a CTA works on at once
-  constexpr int ROW = NC * TPR * 8;               // channels of a row, padded
+template <typename T, int NC, int R, bool LAYER, bool BIAS, bool BLOCK>
+__global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  __shared__ float red[2][2 * 32];
-  T* ring = reinterpret_cast<T*>(norm_smem);      // [stage][x|dy][RPB][ROW]
-  float* sgain = reinterpret_cast<float*>(norm_smem + (size_t)NORM_STAGES * 2 * RPB * ROW * sizeof(T));
+  __shared__ float red[2][NORM_MAX_WARPS * 2 * R];
+  const int tpr = a.tpr;
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & (tpr - 1);
+  const int g = BLOCK ? 0 : threadIdx.x / tpr;
+  const int groups = BLOCK ? 1 : NORM_GROUP_THREADS / tpr;
+  const int row = NC * tpr * 8;                   // channels of a row, padded
+  T* ring = reinterpret_cast<T*>(norm_smem);      // [stage][R][x|dy][group][row]
+  float* sgain = reinterpret_cast<float*>(norm_smem + (size_t)NORM_STAGES * R * 2 * groups * row * sizeof(T));
   griddep_launch_dependents();
   griddep_wait();
-  const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
   const int width = a.width;
   const float inv_width = 1.0f / (float)width;
+  const long long step = (long long)gridDim.x * groups * R;
 
-  auto row_at = [&](long long u, int64_t row, int64_t head) { return (u / a.heads) * row + (u % a.heads) * head; };
-  const long long step = (long long)gridDim.x * RPB;
-  auto fetch = [&](long long u, int st) {
-    if (u < a.units) {
-      const T* x = static_cast<const T*>(a.x) + row_at(u, a.x_row, a.x_head);
-      const T* dy = static_cast<const T*>(a.dy) + row_at(u, a.dy_row, a.dy_head);
-      T* to = ring + (size_t)(st * 2 * RPB + g) * ROW;
+  auto at_stage = [&](int st, int k, int which) {
+    return ring + (size_t)(((st * R + k) * 2 + which) * groups + g) * row;
+  };
+  auto at_row = [&](long long u, int64_t row_stride, int64_t head_stride) {
+    const int64_t i = a.heads == 1 ? u : (a.units <= 0xffffffffLL ? (uint32_t)u / (uint32_t)a.heads : u / a.heads);
+    return i * row_stride + (u - i * a.heads) * head_stride;
+  };
+  // rows of a step: base + g + k * groups
+  auto fetch = [&](long long base, int st) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * TPR) * 8;
-        const int valid = min(width - at, 8);
-        if (valid <= 0) continue;
-        if (in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, x + at, valid, a.err, 52)) copy8(to + at, x + at, valid);
-        if (in_bounds<T>(static_cast<const T*>(a.dy), a.dy_elems, dy + at, valid, a.err, 53))
-          copy8(to + RPB * ROW + at, dy + at, valid);
+    for (int k = 0; k < R; ++k) {
+      const long long u = base + g + k * groups;
+      if (u < a.units) {
+        const T* x = static_cast<const T*>(a.x) + at_row(u, a.x_row, a.x_head);
+        const T* dy = static_cast<const T*>(a.dy) + at_row(u, a.dy_row, a.dy_head);
+        T* to_x = at_stage(st, k, 0);
+        T* to_dy = at_stage(st, k, 1);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
+          if (valid <= 0) continue;
+          if (in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, x + at, valid, a.err, 52))
+            copy8(to_x + at, x + at, valid);
+          if (in_bounds<T>(static_cast<const T*>(a.dy), a.dy_elems, dy + at, valid, a.err, 53))
+            copy8(to_dy + at, dy + at, valid);
+        }
       }
     }
     cp_async_commit();
   };
 
-  long long u = (long long)blockIdx.x * RPB + g;
-  for (int st = 0; st < NORM_STAGES - 1; ++st) fetch(u + st * step, st);
-  for (int at = threadIdx.x * 8; at < ROW; at += NT * 8) {
-    float v[8];
-    const int valid = min(width - at, 8);
-    load_param8(valid > 0 ? a.gain : nullptr, a.param_fp32, at, valid, 1.0f, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < valid ? v[e] : 0.0f;
-    store8(sgain + at, 8, v);
+  long long base = (long long)blockIdx.x * groups * R;
+  fetch(base, 0);
+  for (int at = threadIdx.x * 8; at < row; at += blockDim.x * 8) {
+    float2 v[4];
+    param8(at < width ? a.gain : nullptr, a.param_fp32, at, width - at, 1.0f, v);
+    zero_past(v, width - at);
+    put8(sgain + at, 8, v);
   }
   __syncthreads();
 
-  float ag[NC][8], ab[NC][8];
+  float2 ag[NC][4], ab[BIAS ? NC : 1][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ag[c][e] = ab[c][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      ag[c][e] = splat(0.0f);
+      if (BIAS) ab[c][e] = splat(0.0f);
+    }
 
-  // every group of the CTA runs the same number of steps (the row sums of
-  // TPR > 32 hold a block barrier; narrower groups only shuffle)
-  const long long first = (long long)blockIdx.x * RPB;
-  int st = 0, parity = 0;   // the RMS norm's one sum per row alternates the scratch slots
-  for (long long base = first; base < a.units; base += step, u += step) {
-    const bool have = u < a.units;
-    fetch(u + (NORM_STAGES - 1) * step, (st + NORM_STAGES - 1) % NORM_STAGES);
-    cp_async_wait<NORM_STAGES - 1>();
-    const T* xs = ring + (size_t)(st * 2 * RPB + g) * ROW;
-    const T* ds = xs + RPB * ROW;
-    float mean = 0.0f, mean_w = 0.0f;
-    float s[2] = {0.0f, 0.0f};
+  // every group of the CTA runs the same number of steps: wide rows meet at
+  // the reductions' barrier, and half-warp groups at their warp's shuffles
+  int st = 0, parity = 0;
+  for (; base < a.units; base += step) {
+    fetch(base + step, st ^ 1);
+    cp_async_wait<1>();
+    float mean[R], mean_w[R], s[2 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) mean[k] = mean_w[k] = 0.0f;
     if (LAYER) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * TPR) * 8;
-        if (!have || at >= width) continue;
-        float x[8], dy[8], gn[8];
-        load8(xs + at, 8, x);
-        load8(ds + at, 8, dy);
-        load8(sgain + at, 8, gn);
+      for (int k = 0; k < R; ++k) {
+        float2 sx = splat(0.0f), sw = splat(0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[0] += x[e];
-          s[1] = __fmaf_rn(dy[e], gn[e], s[1]);
+        for (int c = 0; c < NC; ++c) {
+          const int at = (t + c * tpr) * 8;
+          if (at >= width || base + g + k * groups >= a.units) continue;
+          Chunk<T> x, d;
+          Chunk<float> gc;
+          x.load(at_stage(st, k, 0) + at);
+          d.load(at_stage(st, k, 1) + at);
+          gc.load(sgain + at);
+          float2 xv[4], dv[4], gv[4];
+          x.get(xv);
+          d.get(dv);
+          gc.get(gv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sx = __fadd2_rn(sx, xv[e]);
+            sw = __ffma2_rn(dv[e], gv[e], sw);
+          }
+        }
+        s[2 * k] = sx.x + sx.y;
+        s[2 * k + 1] = sw.x + sw.y;
+      }
+      row_sum<BLOCK>(s, tpr, red[0]);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        mean[k] = s[2 * k] * inv_width;
+        mean_w[k] = s[2 * k + 1] * inv_width;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float2 sc = splat(0.0f), sw = splat(0.0f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int at = (t + c * tpr) * 8;
+        if (at >= width || base + g + k * groups >= a.units) continue;
+        Chunk<T> x, d;
+        Chunk<float> gc;
+        x.load(at_stage(st, k, 0) + at);
+        d.load(at_stage(st, k, 1) + at);
+        gc.load(sgain + at);
+        float2 xv[4], dv[4], gv[4];
+        x.get(xv);
+        d.get(dv);
+        gc.get(gv);
+        if (LAYER) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xv[e] = __fadd2_rn(xv[e], splat(-mean[k]));
+          if (width - at < 8) zero_past(xv, width - at);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc = __ffma2_rn(xv[e], xv[e], sc);
+          sw = __ffma2_rn(__fmul2_rn(dv[e], gv[e]), xv[e], sw);
         }
       }
-      row_sum<TPR>(s, red[0]);
-      mean = s[0] * inv_width;
-      mean_w = s[1] * inv_width;
-      s[0] = s[1] = 0.0f;
+      s[2 * k] = sc.x + sc.y;
+      s[2 * k + 1] = sw.x + sw.y;
     }
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int at = (t + c * TPR) * 8;
-      if (!have || at >= width) continue;
-      float x[8], dy[8], gn[8];
-      load8(xs + at, 8, x);
-      load8(ds + at, 8, dy);
-      load8(sgain + at, 8, gn);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float cx = !LAYER ? x[e] : (at + e < width ? x[e] - mean : 0.0f);
-        s[0] = __fmaf_rn(cx, cx, s[0]);
-        s[1] = __fmaf_rn(dy[e] * gn[e], cx, s[1]);
-      }
-    }
-    row_sum<TPR>(s, red[LAYER ? 1 : parity]);
+    // (the RMS norm's one sum per step alternates the scratch slots)
+    row_sum<BLOCK>(s, tpr, red[LAYER ? 1 : parity]);
     parity ^= 1;
-    const float r = 1.0f / sqrtf(s[0] * inv_width + a.eps);
-    const float k = s[1] * r * inv_width;          // mean(w xhat)
-    if (have) {
-      T* dx = static_cast<T*>(a.dx) + row_at(u, a.dx_row, a.dx_head);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long u = base + g + k * groups;
+      if (u >= a.units) continue;
+      const float r = 1.0f / sqrtf(s[2 * k] * inv_width + a.eps);
+      const float m = s[2 * k + 1] * r * inv_width;          // mean(w xhat)
+      T* dx = static_cast<T*>(a.dx) + at_row(u, a.dx_row, a.dx_head);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * TPR) * 8;
-        const int valid = min(width - at, 8);
+        const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
         if (valid <= 0) continue;
-        float x[8], dy[8], gn[8], out[8];
-        load8(xs + at, 8, x);
-        load8(ds + at, 8, dy);
-        load8(sgain + at, 8, gn);
+        Chunk<T> x, d;
+        Chunk<float> gc;
+        x.load(at_stage(st, k, 0) + at);
+        d.load(at_stage(st, k, 1) + at);
+        gc.load(sgain + at);
+        float2 xv[4], dv[4], gv[4];
+        x.get(xv);
+        d.get(dv);
+        gc.get(gv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xhat = (x[e] - mean) * r;
-          out[e] = (__fmaf_rn(dy[e], gn[e], -mean_w) - xhat * k) * r;
-          ag[c][e] = __fmaf_rn(dy[e], xhat, ag[c][e]);
-          ab[c][e] += dy[e];
+        for (int e = 0; e < 4; ++e) {
+          float2 xhat = xv[e];
+          if (LAYER) xhat = __fadd2_rn(xhat, splat(-mean[k]));
+          xhat = __fmul2_rn(xhat, splat(r));
+          ag[c][e] = __ffma2_rn(dv[e], xhat, ag[c][e]);
+          if (BIAS) ab[c][e] = __fadd2_rn(ab[c][e], dv[e]);
+          float2 w = LAYER ? __ffma2_rn(dv[e], gv[e], splat(-mean_w[k])) : __fmul2_rn(dv[e], gv[e]);
+          xv[e] = __fmul2_rn(__ffma2_rn(xhat, splat(-m), w), splat(r));
         }
-        if (in_bounds<T>(static_cast<const T*>(a.dx), a.dx_elems, dx + at, valid, a.err, 54))
-          store8(dx + at, valid, out);
+        if (in_bounds<T>(static_cast<const T*>(a.dx), a.dx_elems, dx + at, valid, a.err, 54)) put8(dx + at, valid, xv);
       }
     }
-    st = (st + 1) % NORM_STAGES;
+    st ^= 1;
   }
   cp_async_wait<0>();
 
   if (a.part == nullptr) return;
-  // the CTA's sums: group 0's channels, the other groups added in order
-  __syncthreads();
+  // the CTA's sums: each group's channels, the groups added in order
+  const int n_which = BIAS ? 2 : 1;
+  float* part = a.part + (size_t)blockIdx.x * n_which * a.part_width;
   float* comb = reinterpret_cast<float*>(norm_smem);
-  float* part = a.part + (size_t)blockIdx.x * 2 * a.part_width;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (RPB > 1) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) store8(comb + (size_t)g * ROW + (t + c * TPR) * 8, 8, which == 0 ? ag[c] : ab[c]);
-      __syncthreads();
-      for (int at = threadIdx.x; at < width; at += NT) {
-        float v = 0.0f;
-        for (int k = 0; k < RPB; ++k) v += comb[(size_t)k * ROW + at];
-        if (in_bounds<float>(a.part, a.part_elems, part + which * a.part_width + at, 1, a.err, 55))
-          part[which * a.part_width + at] = v;
-      }
-      __syncthreads();
-    } else {
+  for (int which = 0; which < n_which; ++which) {
+    if (BLOCK) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * TPR) * 8;
-        if (at < width && in_bounds<float>(a.part, a.part_elems, part + which * a.part_width + at, 8, a.err, 55))
-          store8(part + which * a.part_width + at, 8, which == 0 ? ag[c] : ab[c]);
+        const int at = (t + c * tpr) * 8;
+        float* p = part + which * a.part_width + at;
+        if (at < width && in_bounds<float>(a.part, a.part_elems, p, 8, a.err, 55))
+          put8(p, 8, which == 0 ? ag[c] : ab[BIAS ? c : 0]);
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        put8(comb + (size_t)g * row + (t + c * tpr) * 8, 8, which == 0 ? ag[c] : ab[BIAS ? c : 0]);
+      __syncthreads();
+      for (int at = threadIdx.x; at < width; at += NORM_GROUP_THREADS) {
+        float v = 0.0f;
+        for (int k = 0; k < groups; ++k) v += comb[(size_t)k * row + at];
+        float* p = part + which * a.part_width + at;
+        if (in_bounds<float>(a.part, a.part_elems, p, 1, a.err, 55)) *p = v;
       }
     }
   }
 }
 
-// dgain and dbias: the CTAs' sums added in a fixed order (eight interleaved
-// runs over the CTAs, then the eight in order).  blockIdx.y: 0 gain, 1 bias.
-__global__ void __launch_bounds__(256) norm_param_kernel(const float* part, int n_parts, int part_width, int width,
-                                                         float* dgain, float* dbias) {
+// dgain and dbias: the CTAs' sums added in a fixed order (32 interleaved runs
+// over the CTAs, then the 32 in order).  A CTA handles 32 channels of one of
+// the two (blockIdx.y: 0 gain, 1 bias).
+__global__ void __launch_bounds__(256) norm_param_kernel(const float* part, int n_parts, int n_which, int part_width,
+                                                         int width, float* dgain, float* dbias) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float red[8][32];
+  __shared__ float4 red[32][8];
   float* out = blockIdx.y == 0 ? dgain : dbias;
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), seg = threadIdx.x >> 5;
-  float s = 0.0f;
-  if (out != nullptr && col < width) {
+  if (out == nullptr) return;
+  const int seg = threadIdx.x >> 3, q = threadIdx.x & 7;
+  const int col = blockIdx.x * 32 + q * 4;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < width) {   // part_width is a multiple of 8: whole vectors
     const float* p = part + (size_t)blockIdx.y * part_width + col;
 #pragma unroll 8
-    for (int k = seg; k < n_parts; k += 8) s += p[(size_t)k * 2 * part_width];
+    for (int k = seg; k < n_parts; k += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (size_t)k * n_which * part_width);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
   }
-  red[seg][threadIdx.x & 31] = s;
+  red[seg][q] = s;
   __syncthreads();
-  if (seg == 0 && out != nullptr && col < width) {
+  if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < (unsigned)width) {
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += red[k][threadIdx.x];
-    out[col] = v;
+    for (int k = 0; k < 32; ++k) v += reinterpret_cast<const float*>(red[k])[threadIdx.x];
+    out[blockIdx.x * 32 + threadIdx.x] = v;
   }
 }
 
@@ -399,85 +536,157 @@ __global__ void __launch_bounds__(256) norm_param_kernel(const float* part, int 
 // launchers
 // ---------------------------------------------------------------------------
 namespace {
-// The thread layout of a width: TPR threads per row, NC chunks of 8 channels
-// per thread.
-template <typename F>
-cudaError_t norm_layout(int width, F&& f) {
+constexpr int kNormSmemMax = 227 * 1024;
+
+// Thread layout of a width: chunks per thread nc, threads per row tpr (a power
+// of two up to 32 for rows of at most 1024 channels, whole warps beyond).
+struct NormLayout {
+  int nc, tpr;
+  bool block;
+};
+NormLayout layout_of(int width, int wide_nc) {
   const int n = (width + 7) / 8;
-#define H3_NORM_CASE(tpr, nc) return f(std::integral_constant<int, tpr>{}, std::integral_constant<int, nc>{})
-  if (n <= 16) H3_NORM_CASE(16, 1);
-  if (n <= 32) H3_NORM_CASE(32, 1);
-  if (n <= 64) H3_NORM_CASE(32, 2);
-  if (n <= 128) H3_NORM_CASE(32, 4);
-  if (n <= 256) H3_NORM_CASE(128, 2);
-  if (n <= 384) H3_NORM_CASE(128, 3);
-  if (n <= 512) H3_NORM_CASE(128, 4);
-  if (n <= 768) H3_NORM_CASE(256, 3);
-  H3_NORM_CASE(256, 4);
-#undef H3_NORM_CASE
+  NormLayout l;
+  l.block = n > NORM_GROUP_CHUNKS;
+  if (l.block) {
+    l.nc = wide_nc;
+    l.tpr = (n + 32 * l.nc - 1) / (32 * l.nc) * 32;
+  } else {
+    l.nc = n <= 32 ? 1 : (n <= 64 ? 2 : 4);
+    l.tpr = 4;
+    while (l.tpr * l.nc < n) l.tpr *= 2;
+  }
+  return l;
 }
-int norm_rows_at_once(int width) {
-  int r = 1;
-  norm_layout(width, [&](auto tpr, auto) {
-    r = tpr() <= 32 ? 256 / tpr() : 1;
-    return cudaSuccess;
-  });
-  return r;
+// Forward, wide rows: 8 chunks per thread.  Backward: 3 (the accumulators are
+// 16 registers a chunk), 4 where 8 warps do not reach with 3.
+NormLayout fwd_layout(int width) { return layout_of(width, 8); }
+NormLayout bwd_layout(int width) { return layout_of(width, width > 8 * 3 * 32 * NORM_MAX_WARPS ? 4 : 3); }
+
+// Rows per group and step of the backward kernel, and its shared memory.
+struct NormBwdPlan {
+  NormLayout l;
+  int rows, threads, groups;
+  size_t smem;
+  int ctas;
+};
+NormBwdPlan bwd_plan(long long units, int width, bool fp32) {
+  NormBwdPlan p;
+  p.l = bwd_layout(width);
+  p.threads = p.l.block ? p.l.tpr : NORM_GROUP_THREADS;
+  p.groups = p.threads / p.l.tpr;
+  const size_t row = (size_t)p.l.nc * p.l.tpr * 8;
+  auto smem = [&](int r) { return (size_t)NORM_STAGES * r * 2 * p.groups * row * (fp32 ? 4 : 2) + row * 4; };
+  p.rows = p.l.nc == 1 ? 4 : 2;
+  if (smem(p.rows) > kNormSmemMax) p.rows = 1;
+  p.smem = smem(p.rows);
+  if (!p.l.block && p.smem < (size_t)p.groups * row * 4) p.smem = (size_t)p.groups * row * 4;
+  // at most what fits by shared memory and four: the workspace is sized for
+  // these, the launch takes as many as the kernel's registers let be resident
+  const int per_sm = (int)(kNormSmemMax / (p.smem + 1024));
+  const long long most = (long long)(per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm)) * num_sms();
+  const long long steps = (units + p.groups * p.rows - 1) / (p.groups * p.rows);
+  p.ctas = (int)(steps < most ? steps : most);
+  return p;
+}
+// CTAs of a kernel that fit on one SM; asked once per kernel and device.
+int resident_ctas(const void* kernel, int threads, size_t smem) {
+  struct Entry {
+    const void* kernel;
+    int device, threads;
+    size_t smem;
+    int ctas;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Entry& e : known)
+    if (e.kernel == kernel && e.device == dev && e.threads == threads && e.smem == smem) return e.ctas;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) return 1;
+  known.push_back({kernel, dev, threads, smem, n});
+  return n;
 }
 
-template <typename T>
-cudaError_t launch_norm_fwd_t(const NormArgs& a, cudaStream_t st) {
-  return norm_layout(a.width, [&](auto tpr, auto nc) {
-    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    constexpr int RPB = TPR <= 32 ? NORM_FWD_BATCH_THREADS / TPR : 1;
-    const long long blocks = (a.units + RPB - 1) / RPB;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(TPR <= 32 ? NORM_FWD_BATCH_THREADS : TPR);
-    return a.layer ? launch_kernel(norm_fwd_kernel<T, TPR, NC, true>, grid, block, 0, st, a)
-                   : launch_kernel(norm_fwd_kernel<T, TPR, NC, false>, grid, block, 0, st, a);
-  });
+template <typename F>
+cudaError_t with_flag(bool b, F&& f) {
+  return b ? f(std::true_type{}) : f(std::false_type{});
 }
 
-template <typename T>
-cudaError_t launch_norm_bwd_t(const NormArgs& a, cudaStream_t st) {
-  return norm_layout(a.width, [&](auto tpr, auto nc) {
-    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    constexpr int NT = TPR <= 32 ? 256 : TPR, RPB = NT / TPR, ROW = NC * TPR * 8;
-    constexpr size_t ring = (size_t)NORM_STAGES * 2 * RPB * ROW * sizeof(T) + (size_t)ROW * 4;
-    constexpr size_t comb = RPB > 1 ? (size_t)RPB * ROW * 4 : 0;
-    constexpr size_t smem = ring > comb ? ring : comb;
-    auto kernel = a.layer ? norm_bwd_kernel<T, TPR, NC, true> : norm_bwd_kernel<T, TPR, NC, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, dim3((unsigned)norm_bwd_ctas(a.units, a.width)), dim3(NT), smem, st, a);
+template <typename T, int NC, int R, bool BLOCK>
+cudaError_t launch_fwd(const NormArgs& a, int threads, cudaStream_t st) {
+  const long long per = (long long)R * (BLOCK ? 1 : threads / a.tpr);
+  const long long blocks = (a.units + per - 1) / per;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return with_flag(a.layer != 0, [&](auto layer) {
+    return launch_kernel(norm_fwd_kernel<T, NC, R, decltype(layer)::value, BLOCK>, dim3((unsigned)blocks),
+                         dim3((unsigned)threads), 0, st, a);
   });
+}
+template <typename T>
+cudaError_t launch_fwd_t(NormArgs& a, cudaStream_t st) {
+  const NormLayout l = fwd_layout(a.width);
+  a.tpr = l.tpr;
+  if (l.block) return launch_fwd<T, 8, 1, true>(a, l.tpr, st);
+  if (l.nc == 1) return launch_fwd<T, 1, 4, false>(a, NORM_GROUP_THREADS, st);
+  if (l.nc == 2) return launch_fwd<T, 2, 2, false>(a, NORM_GROUP_THREADS, st);
+  return launch_fwd<T, 4, 1, false>(a, NORM_GROUP_THREADS, st);
+}
+
+template <typename T, int NC, int R, bool BLOCK>
+cudaError_t launch_bwd(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_t st) {
+  return with_flag(a.layer != 0, [&](auto layer) {
+    return with_flag(bias, [&](auto with_bias) {
+      auto kernel = norm_bwd_kernel<T, NC, R, decltype(layer)::value, decltype(with_bias)::value, BLOCK>;
+      if (p.smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        if (e != cudaSuccess) return e;
+      }
+      const long long fit =
+          (long long)resident_ctas(reinterpret_cast<const void*>(kernel), p.threads, p.smem) * num_sms();
+      if (p.ctas > fit) p.ctas = (int)fit;
+      return launch_kernel(kernel, dim3((unsigned)p.ctas), dim3((unsigned)p.threads), p.smem, st, a);
+    });
+  });
+}
+template <typename T>
+cudaError_t launch_bwd_t(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_t st) {
+  if (p.l.block) {
+    if (p.l.nc == 3) return p.rows == 2 ? launch_bwd<T, 3, 2, true>(a, p, bias, st) : launch_bwd<T, 3, 1, true>(a, p, bias, st);
+    return p.rows == 2 ? launch_bwd<T, 4, 2, true>(a, p, bias, st) : launch_bwd<T, 4, 1, true>(a, p, bias, st);
+  }
+  if (p.l.nc == 1) return launch_bwd<T, 1, 4, false>(a, p, bias, st);
+  if (p.l.nc == 2) return launch_bwd<T, 2, 2, false>(a, p, bias, st);
+  return p.rows == 2 ? launch_bwd<T, 4, 2, false>(a, p, bias, st) : launch_bwd<T, 4, 1, false>(a, p, bias, st);
 }
 }  // namespace
 
-int norm_bwd_ctas(long long units, int width) {
-  const long long most = 2LL * num_sms(), blocks = (units + norm_rows_at_once(width) - 1) / norm_rows_at_once(width);
-  return (int)(blocks < most ? blocks : most);
-}
+int norm_bwd_ctas(long long units, int width, bool fp32) { return bwd_plan(units, width, fp32).ctas; }
 
-cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
-  cudaError_t e = a.fp32 ? launch_norm_fwd_t<float>(a, st) : launch_norm_fwd_t<__nv_bfloat16>(a, st);
+cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st) {
+  cudaError_t e = a.fp32 ? launch_fwd_t<float>(a, st) : launch_fwd_t<__nv_bfloat16>(a, st);
   if (e != cudaSuccess) return e;
-  set_kernel_info("norm_fwd_kernel %s %s rows=%lld width=%d", a.layer ? "layer" : "rms", a.fp32 ? "fp32" : "bf16",
-                  a.units, a.width);
+  set_kernel_info("norm_fwd_kernel %s %s rows=%lld width=%d threads/row=%d", a.layer ? "layer" : "rms",
+                  a.fp32 ? "fp32" : "bf16", a.units, a.width, a.tpr);
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a, float* dgain, float* dbias, cudaStream_t st) {
-  cudaError_t e = a.fp32 ? launch_norm_bwd_t<float>(a, st) : launch_norm_bwd_t<__nv_bfloat16>(a, st);
+cudaError_t launch_norm_bwd(NormArgs a, float* dgain, float* dbias, cudaStream_t st) {
+  NormBwdPlan p = bwd_plan(a.units, a.width, a.fp32);
+  a.tpr = p.l.tpr;
+  const bool bias = dbias != nullptr;
+  cudaError_t e = a.fp32 ? launch_bwd_t<float>(a, p, bias, st) : launch_bwd_t<__nv_bfloat16>(a, p, bias, st);
   if (e != cudaSuccess) return e;
-  const int ctas = norm_bwd_ctas(a.units, a.width);
   if (dgain || dbias) {
-    e = launch_kernel(norm_param_kernel, dim3((unsigned)((a.width + 31) / 32), dbias ? 2 : 1), dim3(256), 0, st,
-                      (const float*)a.part, ctas, a.part_width, a.width, dgain, dbias);
+    e = launch_kernel(norm_param_kernel, dim3((unsigned)((a.width + 31) / 32), bias ? 2 : 1), dim3(256), 0, st,
+                      (const float*)a.part, p.ctas, bias ? 2 : 1, a.part_width, a.width, dgain, dbias);
     if (e != cudaSuccess) return e;
   }
-  set_kernel_info("norm_bwd_kernel %s %s rows=%lld width=%d ctas=%d stages=%d", a.layer ? "layer" : "rms",
-                  a.fp32 ? "fp32" : "bf16", a.units, a.width, ctas, NORM_STAGES);
+  set_kernel_info("norm_bwd_kernel %s %s rows=%lld width=%d threads/row=%d rows/step=%d ctas=%d",
+                  a.layer ? "layer" : "rms", a.fp32 ? "fp32" : "bf16", a.units, a.width, a.tpr, p.rows * p.groups,
+                  p.ctas);
   return cudaGetLastError();
 }
 

@@ -12,9 +12,11 @@
 // fraction, in half turns.
 //
 // Bound by memory: q and k are read and written once.  A CTA handles one
-// packed row (of few rows: a range of its heads); it computes the row's A F
-// sines and cosines once into shared memory, and each thread keeps those of
-// its own 16-byte unit of a head in registers while it walks over the heads.
+// packed row (of few rows: a range of its heads).  A thread owns a pair of
+// 16-byte vectors of a head (the first channels and the second ones of its
+// pairs, or two vectors of whole pairs, or two of passed-through channels) and
+// walks over the heads; it asks for the vectors of RO_BATCH heads before the
+// row's sines and cosines are computed (once per CTA, into shared memory).
 #include "h3_device.cuh"
 #include "h3_internal.h"
 
@@ -24,49 +26,35 @@ namespace {
 constexpr int RO_THREADS = 256;
 constexpr int RO_BATCH = 4;      // heads whose loads a thread issues before their use
 
+// 16 bytes of channels, as they lie in memory and as fp32.
 template <typename T>
-struct Vec16 {
-  static constexpr int N = 16 / (int)sizeof(T);
-  float v[N];
-  __device__ __forceinline__ void load(const T* p) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ void ro_unpack(const uint4& r, float (&v)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
     if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = bf16_lo(w[e]);
-        v[2 * e + 1] = bf16_hi(w[e]);
-      }
+      v[2 * e] = bf16_lo(w[e]);
+      v[2 * e + 1] = bf16_hi(w[e]);
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+      v[e] = __uint_as_float(w[e]);
     }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-  }
-};
+}
+template <typename T>
+__device__ __forceinline__ uint4 ro_pack(const float (&v)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  else
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
 __device__ __forceinline__ float ro_get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float ro_get(const float* p) { return *p; }
 __device__ __forceinline__ void ro_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void ro_put(float* p, float v) { *p = v; }
-}  // namespace
 
-// VEC: 16-byte units (half layout: a unit of first channels with its unit of
-// second ones; interleaved: one unit holding whole pairs); otherwise one pair
-// or one passed-through channel at a time.
-template <typename T, bool HALF, bool VEC>
-__global__ void __launch_bounds__(RO_THREADS) rope_kernel(const RopePosArgs a) {
-  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
-  griddep_launch_dependents();
-  griddep_wait();
-  constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
-  const int64_t row = blockIdx.x;
+// sines and cosines of the row, times the magnitude
+__device__ __forceinline__ void ro_angles(const RopePosArgs& a, int64_t row, float* cs, float* sn) {
   const int P = a.axes * a.freqs;
   for (int p = threadIdx.x; p < P; p += RO_THREADS) {
     const int32_t* pp = a.pos + row * a.axes + p / a.freqs;
@@ -77,112 +65,175 @@ __global__ void __launch_bounds__(RO_THREADS) rope_kernel(const RopePosArgs a) {
     cs[p] = c * a.magnitude;
     sn[p] = s * a.sin_scale;
   }
-  __syncthreads();
+}
 
-  // units of a head: rotated ones first, then the passed-through channels
-  // (in place: none)
-  const int per_rot = HALF ? V : (VEC ? V / 2 : 1);            // pairs per rotated unit
-  const int n_rot = P / per_rot;
-  const int pass = a.in_place ? 0 : a.width - 2 * P;
-  const int upl = n_rot + (pass + V - 1) / V;
-  const int at_once = RO_THREADS / upl;                         // heads the CTA handles at once
+template <typename T>
+struct RoRow {   // the row's q and k heads, numbered through
+  const T *q_in, *k_in;
+  T *q_out, *k_out;
+  __device__ __forceinline__ RoRow(const RopePosArgs& a, int64_t row) {
+    q_in = static_cast<const T*>(a.q_in) + row * a.in_row;
+    k_in = static_cast<const T*>(a.k_in) + row * a.in_row - a.q_heads * a.in_head;
+    q_out = static_cast<T*>(a.q_out) + row * a.out_row;
+    k_out = static_cast<T*>(a.k_out) + row * a.out_row - a.q_heads * a.out_head;
+  }
+  __device__ __forceinline__ const T* src(const RopePosArgs& a, int h) const {
+    return (h < a.q_heads ? q_in : k_in) + h * a.in_head;
+  }
+  __device__ __forceinline__ T* dst(const RopePosArgs& a, int h) const {
+    return (h < a.q_heads ? q_out : k_out) + h * a.out_head;
+  }
+};
+template <typename T>
+__device__ __forceinline__ bool ro_in_ok(const RopePosArgs& a, int h, const T* p, int n) {
+  return h < a.q_heads ? in_bounds<T>(static_cast<const T*>(a.q_in), a.q_in_elems, p, n, a.err, 61)
+                       : in_bounds<T>(static_cast<const T*>(a.k_in), a.k_in_elems, p, n, a.err, 62);
+}
+template <typename T>
+__device__ __forceinline__ bool ro_out_ok(const RopePosArgs& a, int h, const T* p, int n) {
+  return h < a.q_heads ? in_bounds<T>(static_cast<const T*>(a.q_out), a.q_out_elems, p, n, a.err, 63)
+                       : in_bounds<T>(static_cast<const T*>(a.k_out), a.k_out_elems, p, n, a.err, 64);
+}
+}  // namespace
+
+// Heads whose rotated channels are whole 16-byte vectors.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(RO_THREADS) rope_kernel(const RopePosArgs a) {
+  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int V = 16 / (int)sizeof(T);
+  const int64_t row = blockIdx.x;
+  const RoRow<T> rr(a, row);
+  const int P = a.axes * a.freqs;
+  const int rot_vecs = 2 * P / V;
+  const int n_rot = (rot_vecs + 1) / 2;                       // units of rotated channels
+  const int upl = a.units;                                    // all units of a head
+  const int at_once = RO_THREADS / upl;                       // heads the CTA handles at once
   const int u = threadIdx.x % upl, hg = threadIdx.x / upl;
+  const int h_lo = (int)blockIdx.y * a.heads_per_cta;
+  const int h_hi = hg < at_once ? min(h_lo + a.heads_per_cta, a.q_heads + a.k_heads) : 0;
+  // the unit's two vectors: channel offsets and channels (0: no vector)
+  int at0, at1, n0 = V, n1 = V;
+  if (u < n_rot) {
+    at0 = HALF ? u * V : 2 * u * V;
+    at1 = HALF ? P + u * V : at0 + V;
+    if (!HALF && 2 * u + 1 >= rot_vecs) n1 = 0;
+  } else {
+    at0 = 2 * P + 2 * (u - n_rot) * V;
+    at1 = at0 + V;
+    n0 = min(V, a.width - at0);
+    n1 = max(0, min(V, a.width - at1));
+  }
+  bool angles = false;
+  float c[V], s[V];
+  int h0 = h_lo + hg;
+  do {
+    uint4 x[RO_BATCH], y[RO_BATCH];
+#pragma unroll
+    for (int b = 0; b < RO_BATCH; ++b) {
+      const int h = h0 + b * at_once;
+      if (h < h_hi) {
+        const T* p = rr.src(a, h);
+        if (n0 == V && ro_in_ok(a, h, p + at0, V)) x[b] = *reinterpret_cast<const uint4*>(p + at0);
+        if (n1 == V && ro_in_ok(a, h, p + at1, V)) y[b] = *reinterpret_cast<const uint4*>(p + at1);
+      }
+    }
+    if (!angles) {   // (every thread comes here once, in its first pass)
+      ro_angles(a, row, cs, sn);
+      __syncthreads();
+      angles = true;
+      if (u < n_rot) {
+        // half: vector 0 holds the first channels of V pairs, vector 1 the
+        // second ones; interleaved: each vector holds V / 2 pairs
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const bool have = e < V / 2 || HALF || n1 == V;
+          c[e] = have ? cs[u * V + e] : 0.0f;
+          s[e] = have ? sn[u * V + e] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < RO_BATCH; ++b) {
+      const int h = h0 + b * at_once;
+      if (h >= h_hi) break;
+      T* p = rr.dst(a, h);
+      if (u < n_rot) {
+        float v[V], w[V];
+        ro_unpack<T>(x[b], v);
+        ro_unpack<T>(y[b], w);
+        if (HALF) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float x0 = v[e], x1 = w[e];
+            v[e] = __fmaf_rn(x0, c[e], -(x1 * s[e]));
+            w[e] = __fmaf_rn(x0, s[e], x1 * c[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            const float x0 = v[2 * e], x1 = v[2 * e + 1], y0 = w[2 * e], y1 = w[2 * e + 1];
+            v[2 * e] = __fmaf_rn(x0, c[e], -(x1 * s[e]));
+            v[2 * e + 1] = __fmaf_rn(x0, s[e], x1 * c[e]);
+            w[2 * e] = __fmaf_rn(y0, c[V / 2 + e], -(y1 * s[V / 2 + e]));
+            w[2 * e + 1] = __fmaf_rn(y0, s[V / 2 + e], y1 * c[V / 2 + e]);
+          }
+        }
+        x[b] = ro_pack<T>(v);
+        y[b] = ro_pack<T>(w);
+      }
+      if (n0 == V && ro_out_ok(a, h, p + at0, V)) *reinterpret_cast<uint4*>(p + at0) = x[b];
+      if (n1 == V && ro_out_ok(a, h, p + at1, V)) *reinterpret_cast<uint4*>(p + at1) = y[b];
+      // the last passed-through channels of a width that is no whole vector
+      const int tail = n0 < V ? n0 : (n1 < V ? n1 : 0);
+      if (tail > 0 && u >= n_rot) {
+        const int at = n0 < V ? at0 : at1;
+        const T* q = rr.src(a, h) + at;
+        if (ro_in_ok(a, h, q, tail) && ro_out_ok(a, h, p + at, tail))
+          for (int e = 0; e < tail; ++e) p[at + e] = q[e];
+      }
+    }
+    h0 += RO_BATCH * at_once;
+  } while (h0 < h_hi);
+}
+
+// Any other head: one pair, or one passed-through channel, at a time.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(RO_THREADS) rope_pairs_kernel(const RopePosArgs a) {
+  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t row = blockIdx.x;
+  const RoRow<T> rr(a, row);
+  ro_angles(a, row, cs, sn);
+  __syncthreads();
+  const int P = a.axes * a.freqs;
+  const int at_once = RO_THREADS / a.units;
+  const int u = threadIdx.x % a.units, hg = threadIdx.x / a.units;
   if (hg >= at_once) return;
   const int h_lo = (int)blockIdx.y * a.heads_per_cta;
   const int h_hi = min(h_lo + a.heads_per_cta, a.q_heads + a.k_heads);
-
-  auto src = [&](int h) {
-    return (h < a.q_heads ? static_cast<const T*>(a.q_in) + (int64_t)h * a.in_head
-                          : static_cast<const T*>(a.k_in) + (int64_t)(h - a.q_heads) * a.in_head) +
-           row * a.in_row;
-  };
-  auto dst = [&](int h) {
-    return (h < a.q_heads ? static_cast<T*>(a.q_out) + (int64_t)h * a.out_head
-                          : static_cast<T*>(a.k_out) + (int64_t)(h - a.q_heads) * a.out_head) +
-           row * a.out_row;
-  };
-  auto in_ok = [&](int h, const T* p, int n) {
-    return h < a.q_heads ? in_bounds<T>(static_cast<const T*>(a.q_in), a.q_in_elems, p, n, a.err, 61)
-                         : in_bounds<T>(static_cast<const T*>(a.k_in), a.k_in_elems, p, n, a.err, 62);
-  };
-  auto out_ok = [&](int h, const T* p, int n) {
-    return h < a.q_heads ? in_bounds<T>(static_cast<const T*>(a.q_out), a.q_out_elems, p, n, a.err, 63)
-                         : in_bounds<T>(static_cast<const T*>(a.k_out), a.k_out_elems, p, n, a.err, 64);
-  };
-
-  if (u >= n_rot) {
-    // passed-through channels
-    const int at = 2 * P + (u - n_rot) * V;
-    const int n = min(V, a.width - at);
+  if (u >= P) {
+    const int at = 2 * P + u - P;
     for (int h = h_lo + hg; h < h_hi; h += at_once) {
-      const T* s = src(h) + at;
-      T* d = dst(h) + at;
-      if (!in_ok(h, s, n) || !out_ok(h, d, n)) continue;
-      if (VEC && n == V) {
-        *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
-      } else {
-        for (int e = 0; e < n; ++e) d[e] = s[e];
-      }
+      const T* p = rr.src(a, h) + at;
+      T* d = rr.dst(a, h) + at;
+      if (ro_in_ok(a, h, p, 1) && ro_out_ok(a, h, d, 1)) *d = *p;
     }
     return;
   }
-
-  if constexpr (VEC) {
-    constexpr int NP = HALF ? V : V / 2;
-    float c[NP], s[NP];
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      c[e] = cs[u * NP + e];
-      s[e] = sn[u * NP + e];
-    }
-    const int at0 = u * V, at1 = HALF ? P + u * V : 0;
-    for (int h0 = h_lo + hg; h0 < h_hi; h0 += RO_BATCH * at_once) {
-      Vec16<T> x[RO_BATCH], y[HALF ? RO_BATCH : 1];
-#pragma unroll
-      for (int b = 0; b < RO_BATCH; ++b) {
-        const int h = h0 + b * at_once;
-        if (h < h_hi) {
-          const T* p = src(h);
-          if (in_ok(h, p + at0, V)) x[b].load(p + at0);
-          if (HALF && in_ok(h, p + at1, V)) y[b].load(p + at1);
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < RO_BATCH; ++b) {
-        const int h = h0 + b * at_once;
-        if (h >= h_hi) break;
-        T* p = dst(h);
-        if constexpr (HALF) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float x0 = x[b].v[e], x1 = y[b].v[e];
-            x[b].v[e] = __fmaf_rn(x0, c[e], -(x1 * s[e]));
-            y[b].v[e] = __fmaf_rn(x0, s[e], x1 * c[e]);
-          }
-          if (out_ok(h, p + at0, V)) x[b].store(p + at0);
-          if (out_ok(h, p + at1, V)) y[b].store(p + at1);
-        } else {
-#pragma unroll
-          for (int e = 0; e < NP; ++e) {
-            const float x0 = x[b].v[2 * e], x1 = x[b].v[2 * e + 1];
-            x[b].v[2 * e] = __fmaf_rn(x0, c[e], -(x1 * s[e]));
-            x[b].v[2 * e + 1] = __fmaf_rn(x0, s[e], x1 * c[e]);
-          }
-          if (out_ok(h, p + at0, V)) x[b].store(p + at0);
-        }
-      }
-    }
-  } else {
-    const float c = cs[u], s = sn[u];
-    const int at0 = HALF ? u : 2 * u, at1 = HALF ? P + u : 2 * u + 1;
-    for (int h = h_lo + hg; h < h_hi; h += at_once) {
-      const T* p = src(h);
-      T* d = dst(h);
-      if (!in_ok(h, p + at0, 1) || !in_ok(h, p + at1, 1) || !out_ok(h, d + at0, 1) || !out_ok(h, d + at1, 1)) continue;
-      const float x0 = ro_get(p + at0), x1 = ro_get(p + at1);
-      ro_put(d + at0, __fmaf_rn(x0, c, -(x1 * s)));
-      ro_put(d + at1, __fmaf_rn(x0, s, x1 * c));
-    }
+  const float c = cs[u], s = sn[u];
+  const int at0 = HALF ? u : 2 * u, at1 = HALF ? P + u : 2 * u + 1;
+  for (int h = h_lo + hg; h < h_hi; h += at_once) {
+    const T* p = rr.src(a, h);
+    T* d = rr.dst(a, h);
+    if (!ro_in_ok(a, h, p + at0, 1) || !ro_in_ok(a, h, p + at1, 1) || !ro_out_ok(a, h, d + at0, 1) ||
+        !ro_out_ok(a, h, d + at1, 1))
+      continue;
+    const float x0 = ro_get(p + at0), x1 = ro_get(p + at1);
+    ro_put(d + at0, __fmaf_rn(x0, c, -(x1 * s)));
+    ro_put(d + at1, __fmaf_rn(x0, s, x1 * c));
   }
 }
 
@@ -191,12 +242,12 @@ template <typename T>
 cudaError_t launch_rope_t(RopePosArgs& a, cudaStream_t st, bool* vec) {
   constexpr int V = 16 / (int)sizeof(T);
   const int P = a.axes * a.freqs;
-  // whole 16-byte units: the half layout needs its second channels aligned
-  // too, the interleaved one whole units of pairs
+  // whole 16-byte vectors: the half layout needs its second channels aligned
+  // too, the interleaved one whole vectors of pairs
   *vec = a.half ? P % V == 0 : 2 * P % V == 0;
-  const int units = *vec ? (a.half ? P / V : 2 * P / V) : P;
   const int pass = a.in_place ? 0 : a.width - 2 * P;
-  const int at_once = RO_THREADS / (units + (*vec ? (pass + V - 1) / V : pass));
+  a.units = *vec ? (2 * P / V + 1) / 2 + (pass + 2 * V - 1) / (2 * V) : P + pass;
+  const int at_once = RO_THREADS / a.units;
   const int heads = a.q_heads + a.k_heads;
   // of few rows, several CTAs per row: at least two per SM in all, each with
   // at least one pass over its threads
@@ -205,8 +256,8 @@ cudaError_t launch_rope_t(RopePosArgs& a, cudaStream_t st, bool* vec) {
   if (split > most) split = most;
   a.heads_per_cta = (int)((heads + split - 1) / split);
   const dim3 grid((unsigned)a.rows, (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta));
-  auto kernel = a.half ? (*vec ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
-                       : (*vec ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+  auto kernel = *vec ? (a.half ? rope_kernel<T, true> : rope_kernel<T, false>)
+                     : (a.half ? rope_pairs_kernel<T, true> : rope_pairs_kernel<T, false>);
   return launch_kernel(kernel, grid, dim3(RO_THREADS), 0, st, a);
 }
 }  // namespace
