@@ -25,7 +25,13 @@
 //   warps 4-11   softmax: warpgroup w takes columns [64 w, 64 w + 64), one
 //                row per thread: P from S into bf16 over the thread's own S
 //                columns, then dS from dP and the P still in registers.
-// TMEM: S [0,128), dP [128,256), A1 [256,384), A2 [384,512).
+// Each warp hands P and dS over in two halves of its columns, so that the
+// products that read them begin while the second half is computed.
+// TMEM: S [0,128), dP [128,256), A1 [256,384); on the key side A2 [384,512), P
+// over S and dS over dP; on the query side Q [384,448) as S's left operand
+// (64 KB less operand traffic from shared memory per step, which is what
+// bounds the products: 128 bytes a cycle) and dS [448,512), so that the next S
+// and dP can be computed as soon as the softmax holds this step's.
 #include "h3_device.cuh"
 #include "h3_internal.h"
 
@@ -34,26 +40,60 @@
 namespace h3 {
 
 namespace {
-constexpr int AB_THREADS = 384;
-constexpr int AB_STAGES = 2;
+constexpr int AB_WARPS = 16;                 // softmax warps: 4 per 32 columns of a tile
+constexpr int AB_THREADS = 32 * (4 + AB_WARPS);
+constexpr int AB_ST1 = 3, AB_ST2 = 2;        // stages of the G1 and G2 rings
 constexpr int AB_TILE = 128 * 128 * 2;       // 32 KB: two 64-channel boxes of 16 KB
 constexpr int AB_BOX = 128 * 64 * 2;
 constexpr int AB_ROWVALS = 2 * 128 * 4;      // a tile's log-sum-exp (base 2) and D
-constexpr int AB_SMEM = 1024 + AB_TILE * (2 + 2 * AB_STAGES) + AB_STAGES * AB_ROWVALS + 256;
+constexpr uint32_t TM_S = 0, TM_DP = 128, TM_A1 = 256, TM_A2 = 384, TM_Q = 384, TM_DS = 448;   // TMEM columns
+constexpr int AB_SMEM = AB_TILE * (2 + AB_ST1 + AB_ST2) + 2 * AB_ROWVALS + 256;
 
 __device__ __forceinline__ float ab_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void ab_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// The MMA warp runs its loop converged, so that descriptors and addresses are
+// computed in uniform registers, and one lane (`one` != 0) issues.  (With one
+// lane's branch around the loop every operand of every MMA was moved over from
+// vector registers; the products then took 800 cycles instead of 512.)
+__device__ __forceinline__ void ab_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
+}
+__device__ __forceinline__ void ab_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void ab_commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t ab_elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(one));
+  return one;
 }
 __device__ __forceinline__ void ab_tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -68,6 +108,11 @@ __device__ __forceinline__ void ab_drain(uint64_t* bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer() - t0 > kWaitLimitNs) return;
   }
+}
+// A whole warp's wait: one outcome for all lanes, so that a wait that runs out
+// leaves no lane behind.
+__device__ __forceinline__ bool ab_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, c));
 }
 __device__ __forceinline__ void ab_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -128,8 +173,8 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
 namespace {
 struct AbSmem {
   uint8_t *f1, *f2, *g1, *g2, *rowvals;
-  uint64_t *f1_full, *f2_full, *g1_full, *g1_empty, *g2_full, *g2_empty;
-  uint64_t *s_full, *p_full, *dp_full, *ds_full, *acc_full, *drain;
+  uint64_t *f1_full, *f2_full, *g1_full, *g1_empty, *g2_full, *g2_empty, *rv_full, *rv_empty;
+  uint64_t *s_full, *s_empty, *p_full, *dp_full, *dp_empty, *ds_full, *ds_empty, *f_full, *acc_full, *drain;
 };
 
 // Rows [row0, row0 + 32) of one warp, NC columns of an accumulator, scaled and
@@ -148,7 +193,7 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int u = c * 4 + g;
-      *reinterpret_cast<uint4*>(stg + lane * (U * 16) + ((u ^ (lane & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(stg + lane * (U * 16) + ((u ^ (lane & (U < 8 ? U - 1 : 7))) << 4)) =
           make_uint4(pack_bf16x2(__uint_as_float(o[g * 8 + 0]) * scale, __uint_as_float(o[g * 8 + 1]) * scale),
                      pack_bf16x2(__uint_as_float(o[g * 8 + 2]) * scale, __uint_as_float(o[g * 8 + 3]) * scale),
                      pack_bf16x2(__uint_as_float(o[g * 8 + 4]) * scale, __uint_as_float(o[g * 8 + 5]) * scale),
@@ -161,7 +206,7 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
     const int r = it * (32 / U) + lane / U, u = lane % U;
     __nv_bfloat16* p = out + (int64_t)(row0 + r) * row_stride + u * 8;
     if (row0 + r < S && in_bounds<__nv_bfloat16>(base, elems, p, 8, err, 44))
-      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(stg + r * (U * 16) + ((u ^ (r & 7)) << 4));
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(stg + r * (U * 16) + ((u ^ (r & (U < 8 ? U - 1 : 7))) << 4));
   }
 }
 
@@ -185,106 +230,130 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       mbar_arrive_expect_tx(sm.f1_full, AB_TILE);
       load(sm.f1, tmF1, sm.f1_full, tile);
       for (int j = 0; j < n && ok; ++j) {
-        const int st = j % AB_STAGES;
-        const uint32_t ph = (uint32_t)(j / AB_STAGES) & 1u;
-        if (!mbar_wait(&sm.g1_empty[st], ph ^ 1u, ctl)) { ok = false; break; }
-        mbar_arrive_expect_tx(&sm.g1_full[st], AB_TILE + (KEYS ? AB_ROWVALS : 0));
-        load(sm.g1 + st * AB_TILE, tmG1, &sm.g1_full[st], j);
-        if (KEYS)
-          ab_bulk_load(sm.rowvals + st * AB_ROWVALS, a.rowvals + ((size_t)head * n + j) * 256, AB_ROWVALS,
-                       &sm.g1_full[st]);
+        const int s1 = j % AB_ST1, s2 = j % AB_ST2;
+        if (!mbar_wait(&sm.g1_empty[s1], ((uint32_t)(j / AB_ST1) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sm.g1_full[s1], AB_TILE);
+        load(sm.g1 + s1 * AB_TILE, tmG1, &sm.g1_full[s1], j);
         ++i1;
         if (j == 0) {
           mbar_arrive_expect_tx(sm.f2_full, AB_TILE);
           load(sm.f2, tmF2, sm.f2_full, tile);
         }
-        if (!mbar_wait(&sm.g2_empty[st], ph ^ 1u, ctl)) { ok = false; break; }
-        mbar_arrive_expect_tx(&sm.g2_full[st], AB_TILE);
-        load(sm.g2 + st * AB_TILE, tmG2, &sm.g2_full[st], j);
+        if (!mbar_wait(&sm.g2_empty[s2], ((uint32_t)(j / AB_ST2) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sm.g2_full[s2], AB_TILE);
+        load(sm.g2 + s2 * AB_TILE, tmG2, &sm.g2_full[s2], j);
         ++i2;
       }
       if (!ok) {  // let issued loads land before the CTA exits
         ab_drain(sm.f1_full, 0);
         if (i1 > 0) ab_drain(sm.f2_full, 0);
-        for (int j = (i1 > AB_STAGES ? i1 - AB_STAGES : 0); j < i1; ++j)
-          ab_drain(&sm.g1_full[j % AB_STAGES], (uint32_t)(j / AB_STAGES) & 1u);
-        for (int j = (i2 > AB_STAGES ? i2 - AB_STAGES : 0); j < i2; ++j)
-          ab_drain(&sm.g2_full[j % AB_STAGES], (uint32_t)(j / AB_STAGES) & 1u);
+        for (int j = (i1 > AB_ST1 ? i1 - AB_ST1 : 0); j < i1; ++j)
+          ab_drain(&sm.g1_full[j % AB_ST1], (uint32_t)(j / AB_ST1) & 1u);
+        for (int j = (i2 > AB_ST2 ? i2 - AB_ST2 : 0); j < i2; ++j)
+          ab_drain(&sm.g2_full[j % AB_ST2], (uint32_t)(j / AB_ST2) & 1u);
       }
+    }
+    __syncwarp();
+  } else if (KEYS && warp == 2) {
+    // ------------------------------------------------------------ producer of the query rows' values
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        if (!mbar_wait(&sm.rv_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sm.rv_full[j & 1], AB_ROWVALS);
+        ab_bulk_load(sm.rowvals + (j & 1) * AB_ROWVALS, a.rowvals + ((size_t)head * n + j) * 256, AB_ROWVALS,
+                     &sm.rv_full[j & 1]);
+        ++i;
+      }
+      if (!ok)
+        for (int j = (i > 2 ? i - 2 : 0); j < i; ++j) ab_drain(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_a = idesc_bf16(128, 128, false, true);   // G1, G2 MN-major
-      const uint32_t f1 = smem_u32(sm.f1), f2 = smem_u32(sm.f2), g1 = smem_u32(sm.g1), g2 = smem_u32(sm.g2);
-      // columns [0,128) or [128,256) = F G^T
-      auto issue_ss = [&](uint32_t d, uint32_t f, uint32_t g) {
+    constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idesc_a = idesc_bf16(128, 128, false, true);   // G1, G2 MN-major
+    constexpr uint64_t kTile = AB_TILE >> 4, kBox = AB_BOX >> 4;      // descriptor address steps
+    const uint32_t one = ab_elect();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+    const uint64_t f1 = sdesc_kmajor(smem_u32(sm.f1)), f2 = sdesc_kmajor(smem_u32(sm.f2));
+    const uint64_t g1k = sdesc_kmajor(smem_u32(sm.g1)), g2k = sdesc_kmajor(smem_u32(sm.g2));
+    const uint64_t g1m = sdesc_sw128(smem_u32(sm.g1), AB_BOX, 1024), g2m = sdesc_sw128(smem_u32(sm.g2), AB_BOX, 1024);
+    auto issue_ss = [&](uint32_t d, uint64_t f, uint64_t g) {   // F G^T
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * AB_BOX + (k & 3) * 32);
-          mma_bf16_ss(tmem_base + d, sdesc_kmajor(f + off), sdesc_kmajor(g + off), idesc_s, k != 0 ? 1u : 0u);
-        }
-      };
-      // accumulator += A G, A bf16 in TMEM: each warpgroup's 64 columns are
-      // 32 packed ones at the start of its own half
-      auto issue_ts = [&](uint32_t d, uint32_t s, uint32_t g, bool first) {
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t off = (uint64_t)(k >> 2) * kBox + (uint64_t)(k & 3) * 2;
+        ab_mma_ss(tm + d, f + off, g + off, idesc_s, k != 0 ? 1u : 0u, one);
+      }
+    };
+    auto issue_q = [&](uint32_t d, uint64_t g) {                // Q in TMEM times G^T
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t b = sdesc_sw128(g + (uint32_t)(k * 2048), AB_BOX, 1024);
-          ab_mma_ts(tmem_base + d, tmem_base + s + (uint32_t)((k >> 2) * 64 + (k & 3) * 8), b, idesc_a,
-                    first && k == 0 ? 0u : 1u);
-        }
-      };
-      bool ok = mbar_wait(sm.f1_full, 0, ctl) && mbar_wait(&sm.g1_full[0], 0, ctl);
-      if (ok) {
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t off = (uint64_t)(k >> 2) * kBox + (uint64_t)(k & 3) * 2;
+        ab_mma_ts(tm + d, tm + TM_Q + (uint32_t)(k * 8), g + off, idesc_s, k != 0 ? 1u : 0u, one);
+      }
+    };
+    // accumulator += A G, A bf16 in TMEM: the 32 columns of a warpgroup in 16
+    // packed ones, the next warpgroup's 16 + gap columns further
+    auto issue_ts = [&](uint32_t d, uint32_t s, uint32_t gap, uint64_t g, uint32_t accumulate) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        ab_mma_ts(tm + d, tm + s + (uint32_t)((k >> 1) * (16 + gap) + (k & 1) * 8), g + (uint64_t)(k * 128), idesc_a,
+                  k == 0 ? accumulate : 1u, one);
+    };
+    // S and dP of the next tile: stages and phases of the rings go round here
+    uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;   // the next tile's stage and phase in each ring
+    auto issue_s = [&]() -> bool {
+      if (!ab_wait(&sm.g1_full[s1], p1, ctl)) return false;
+      tc_fence_after();
+      if (KEYS) issue_ss(TM_S, f1, g1k + s1 * kTile);
+      else issue_q(TM_S, g1k + s1 * kTile);
+      ab_commit(sm.s_full, one);
+      if (++s1 == AB_ST1) { s1 = 0; p1 ^= 1u; }
+      return true;
+    };
+    auto issue_dp = [&]() -> bool {
+      if (!ab_wait(&sm.g2_full[s2], p2, ctl)) return false;
+      tc_fence_after();
+      issue_ss(TM_DP, f2, g2k + s2 * kTile);
+      if (!KEYS) ab_commit(&sm.g2_empty[s2], one);
+      ab_commit(sm.dp_full, one);
+      if (++s2 == AB_ST2) { s2 = 0; p2 ^= 1u; }
+      return true;
+    };
+    bool ok = ab_wait(KEYS ? sm.f1_full : sm.f_full, 0, ctl);
+    if (ok) ok = issue_s() && ab_wait(sm.f2_full, 0, ctl) && issue_dp();
+    uint32_t c1 = 0, c2 = 0;                   // this tile's stages
+    for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      const uint32_t ph = (uint32_t)j & 1u, accumulate = j != 0 ? 1u : 0u;
+      if (KEYS) {
+        // A2 += P G2, then the next S over P
+        if (!ab_wait(sm.p_full, ph, ctl)) { ok = false; break; }
         tc_fence_after();
-        issue_ss(0, f1, g1);
-        mma_commit(sm.s_full);
-        ok = mbar_wait(sm.f2_full, 0, ctl) && mbar_wait(&sm.g2_full[0], 0, ctl);
+        issue_ts(TM_A2, TM_S, 16u, g2m + c2 * kTile, accumulate);
+        ab_commit(&sm.g2_empty[c2], one);
+        if (more && !issue_s()) { ok = false; break; }
+      } else if (more) {
+        // S (and dP) of the next tile as soon as the softmax holds this one's
+        if (!ab_wait(sm.s_empty, ph, ctl) || !issue_s()) { ok = false; break; }
+        if (!ab_wait(sm.dp_empty, ph, ctl) || !issue_dp()) { ok = false; break; }
       }
-      if (ok) {
-        tc_fence_after();
-        issue_ss(128, f2, g2);
-        if (!KEYS) mma_commit(&sm.g2_empty[0]);
-        mma_commit(sm.dp_full);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const bool more = j + 1 < n;
-        const int st = j % AB_STAGES, nx = (j + 1) % AB_STAGES;
-        const uint32_t nph = (uint32_t)((j + 1) / AB_STAGES) & 1u;
-        // the softmax has read S (and on the key side written P over it)
-        if (!mbar_wait(sm.p_full, (uint32_t)j & 1u, ctl)) { ok = false; break; }
-        if (KEYS) {
-          tc_fence_after();
-          issue_ts(384, 0, g2 + st * AB_TILE, j == 0);
-          mma_commit(&sm.g2_empty[st]);
-        }
-        if (more) {
-          if (!mbar_wait(&sm.g1_full[nx], nph, ctl)) { ok = false; break; }
-          tc_fence_after();
-          issue_ss(0, f1, g1 + nx * AB_TILE);
-          mma_commit(sm.s_full);
-        }
-        if (!mbar_wait(sm.ds_full, (uint32_t)j & 1u, ctl)) { ok = false; break; }
-        tc_fence_after();
-        issue_ts(256, 128, g1 + st * AB_TILE, j == 0);
-        mma_commit(&sm.g1_empty[st]);
-        if (more) {
-          if (!mbar_wait(&sm.g2_full[nx], nph, ctl)) { ok = false; break; }
-          tc_fence_after();
-          issue_ss(128, f2, g2 + nx * AB_TILE);
-          if (!KEYS) mma_commit(&sm.g2_empty[nx]);
-          mma_commit(sm.dp_full);
-        } else {
-          mma_commit(sm.acc_full);
-        }
-      }
-      if (!ok) {
-        mma_commit(sm.drain);
-        ab_drain(sm.drain, 0);
-      }
+      if (!ab_wait(sm.ds_full, ph, ctl)) { ok = false; break; }
+      tc_fence_after();
+      if (KEYS) issue_ts(TM_A1, TM_DP, 16u, g1m + c1 * kTile, accumulate);
+      else issue_ts(TM_A1, TM_DS, 0u, g1m + c1 * kTile, accumulate);
+      ab_commit(&sm.g1_empty[c1], one);
+      if (!KEYS) ab_commit(sm.ds_empty, one);
+      if (KEYS && more && !issue_dp()) { ok = false; break; }
+      if (!more) ab_commit(sm.acc_full, one);
+      if (++c1 == AB_ST1) c1 = 0;
+      if (++c2 == AB_ST2) c2 = 0;
+    }
+    if (!ok) {
+      ab_commit(sm.drain, one);
+      if (one) ab_drain(sm.drain, 0);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -292,110 +361,140 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
     const int wg = (warp - 4) >> 2;
     const int qq = warp & 3;
     const int row = qq * 32 + lane;
-    const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), (uint32_t)(wg * 64));
-    const uint32_t dp_base = s_base + 128u;
-    const float sl2 = a.scale_log2;
+    const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_S + (uint32_t)(wg * 32));
+    const uint32_t dp_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_DP + (uint32_t)(wg * 32));
+    // where the packed dS goes: over the thread's own dP on the key side
+    const uint32_t ds_base =
+        KEYS ? dp_base : tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_DS + (uint32_t)(wg * 16));
+    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     float my_l2 = 0.0f, my_d = 0.0f;
+    bool ok = true;
     if (!KEYS) {
       const float* rv = a.rowvals + ((size_t)head * n + tile) * 256 + row;
       if (in_bounds<float>(a.rowvals, a.rowval_elems, rv, 129, a.err, 45)) {
         my_l2 = rv[0];
         my_d = rv[128];
       }
-    }
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int st = j % AB_STAGES;
-      const float* rv = reinterpret_cast<const float*>(sm.rowvals + st * AB_ROWVALS) + wg * 64;
-      if (KEYS && !mbar_wait(&sm.g1_full[st], (uint32_t)(j / AB_STAGES) & 1u, ctl)) { ok = false; break; }
-      if (!mbar_wait(sm.s_full, (uint32_t)j & 1u, ctl)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t p[2][32];
-      tmem_ld32(s_base, p[0]);
-      tmem_ld32(s_base + 32u, p[1]);
-      tmem_ld_wait(p[0]);
-      tmem_ld_wait(p[1]);
-      const float2 sl2x2 = make_float2(sl2, sl2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      // Q from its tile into TMEM, where it is the left operand of every S:
+      // warpgroup w takes channels [32 w, 32 w + 32) of the row
+      ok = ab_wait(sm.f1_full, 0, ctl);
+      if (ok) {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float4 l = KEYS ? *reinterpret_cast<const float4*>(rv + h * 32 + c * 2)
-                                : make_float4(my_l2, my_l2, my_l2, my_l2);
-          const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(p[h][2 * c]), __uint_as_float(p[h][2 * c + 1])),
-                                       sl2x2, make_float2(-l.x, -l.y));
-          const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(p[h][2 * c + 2]), __uint_as_float(p[h][2 * c + 3])),
-                                       sl2x2, make_float2(-l.z, -l.w));
-          const float e0 = ab_ex2(z0.x), e1 = ab_ex2(z0.y), e2 = ab_ex2(z1.x), e3 = ab_ex2(z1.y);
-          p[h][2 * c] = __float_as_uint(e0);
-          p[h][2 * c + 1] = __float_as_uint(e1);
-          p[h][2 * c + 2] = __float_as_uint(e2);
-          p[h][2 * c + 3] = __float_as_uint(e3);
-          pk[c] = pack_bf16x2(e0, e1);
-          pk[c + 1] = pack_bf16x2(e2, e3);
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              sm.f1 + (wg >> 1) * AB_BOX + sw128_offset((uint32_t)row, (uint32_t)((wg & 1) * 4 + c)));
+          pk[4 * c] = v.x;
+          pk[4 * c + 1] = v.y;
+          pk[4 * c + 2] = v.z;
+          pk[4 * c + 3] = v.w;
         }
-        if (KEYS) ab_tmem_st16(s_base + (uint32_t)(h * 16), pk);
+        ab_tmem_st16(tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_Q + (uint32_t)(wg * 16)), pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.f_full);
       }
-      if (KEYS) tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm.p_full);
-      if (!KEYS && j == n - 1) {
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      const uint32_t ph = (uint32_t)j & 1u;
+      const float* rv = reinterpret_cast<const float*>(sm.rowvals + (j & 1) * AB_ROWVALS) + wg * 32;
+      if (KEYS && !ab_wait(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl)) { ok = false; break; }
+      if (!ab_wait(sm.s_full, ph, ctl)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t p[32], pk[16];
+      tmem_ld32(s_base, p);
+      tmem_ld_wait(p);
+      if (!KEYS) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.s_empty);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 l =
+            KEYS ? *reinterpret_cast<const float4*>(rv + c) : make_float4(my_l2, my_l2, my_l2, my_l2);
+        const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])), sl2,
+                                     make_float2(-l.x, -l.y));
+        const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])), sl2,
+                                     make_float2(-l.z, -l.w));
+        const float e0 = ab_ex2(z0.x), e1 = ab_ex2(z0.y), e2 = ab_ex2(z1.x), e3 = ab_ex2(z1.y);
+        p[c] = __float_as_uint(e0);
+        p[c + 1] = __float_as_uint(e1);
+        p[c + 2] = __float_as_uint(e2);
+        p[c + 3] = __float_as_uint(e3);
+        pk[c >> 1] = pack_bf16x2(e0, e1);
+        pk[(c >> 1) + 1] = pack_bf16x2(e2, e3);
+      }
+      if (KEYS) {
+        ab_tmem_st16(s_base, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.p_full);
+      } else if (j == n - 1) {
         // keys past the end: their K rows are zero, but exp(-lse) times 0
         // must not become NaN where lse is far below 0
-        const int valid = a.S - j * 128 - wg * 64;
+        const int valid = a.S - j * 128 - wg * 32;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (h * 32 + c >= valid) p[h][c] = 0u;
+        for (int c = 0; c < 32; ++c)
+          if (c >= valid) p[c] = 0u;
       }
-      if (!mbar_wait(sm.dp_full, (uint32_t)j & 1u, ctl)) { ok = false; break; }
+      if (!ab_wait(sm.dp_full, ph, ctl)) { ok = false; break; }
       tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t d[32], pk[16];
-        tmem_ld32(dp_base + (uint32_t)(h * 32), d);
-        tmem_ld_wait(d);
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float4 dd = KEYS ? *reinterpret_cast<const float4*>(rv + 128 + h * 32 + c * 2)
-                                 : make_float4(my_d, my_d, my_d, my_d);
-          const float2 t0 = __fadd2_rn(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])),
-                                       make_float2(-dd.x, -dd.y));
-          const float2 t1 = __fadd2_rn(make_float2(__uint_as_float(d[2 * c + 2]), __uint_as_float(d[2 * c + 3])),
-                                       make_float2(-dd.z, -dd.w));
-          const float2 u0 = __fmul2_rn(t0, make_float2(__uint_as_float(p[h][2 * c]), __uint_as_float(p[h][2 * c + 1])));
-          const float2 u1 =
-              __fmul2_rn(t1, make_float2(__uint_as_float(p[h][2 * c + 2]), __uint_as_float(p[h][2 * c + 3])));
-          pk[c] = pack_bf16x2(u0.x, u0.y);
-          pk[c + 1] = pack_bf16x2(u1.x, u1.y);
-        }
-        ab_tmem_st16(dp_base + (uint32_t)(h * 16), pk);
+      uint32_t d[32];
+      tmem_ld32(dp_base, d);
+      tmem_ld_wait(d);
+      if (!KEYS) {   // the next dP may follow
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.dp_empty);
       }
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 dd =
+            KEYS ? *reinterpret_cast<const float4*>(rv + 128 + c) : make_float4(my_d, my_d, my_d, my_d);
+        const float2 t0 = __fadd2_rn(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])),
+                                     make_float2(-dd.x, -dd.y));
+        const float2 t1 = __fadd2_rn(make_float2(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])),
+                                     make_float2(-dd.z, -dd.w));
+        const float2 u0 = __fmul2_rn(t0, make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])));
+        const float2 u1 = __fmul2_rn(t1, make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])));
+        pk[c >> 1] = pack_bf16x2(u0.x, u0.y);
+        pk[(c >> 1) + 1] = pack_bf16x2(u1.x, u1.y);
+      }
+      if (!KEYS) {   // the previous dS has been read
+        if (!ab_wait(sm.ds_empty, ph ^ 1u, ctl)) { ok = false; break; }
+        tc_fence_after();
+      }
+      ab_tmem_st16(ds_base, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sm.ds_full);
+      if (lane == 0) {
+        mbar_arrive(sm.ds_full);
+        if (KEYS) mbar_arrive(&sm.rv_empty[j & 1]);
+      }
     }
-    if (ok && mbar_wait(sm.acc_full, 0, ctl)) {
+    if (ok && ab_wait(sm.acc_full, 0, ctl)) {
       tc_fence_after();
       // the accumulators leave through the G rings, idle now (acc_full covers
       // every MMA, and every load has been consumed by one)
-      uint8_t* stg = sm.g1 + (warp - 4) * 8192;
+      uint8_t* stg = sm.g1 + (warp - 4) * 4096;
       const int row0 = tile * 128 + qq * 32;
-      const uint32_t acc = tmem_addr(tmem_base, (uint32_t)(qq * 32), 256);
+      const uint32_t acc = tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_A1);
+      const int64_t at_head = head * a.d_head_stride;
       if (KEYS) {
-        if (wg == 0)
-          ab_store<128>(acc + 128u, 1.0f, stg, lane, row0, a.S, a.dv + head * a.d_head_stride, a.d_row_stride, a.dv,
-                        a.d_elems, a.err);
+        const int half = (wg & 1) * 64;
+        if (wg < 2)
+          ab_store<64>(acc + (TM_A2 - TM_A1) + (uint32_t)half, 1.0f, stg, lane, row0, a.S, a.dv + at_head + half,
+                       a.d_row_stride, a.dv, a.d_elems, a.err);
         else
-          ab_store<128>(acc, a.scale, stg, lane, row0, a.S, a.dk + head * a.d_head_stride, a.d_row_stride, a.dk,
-                        a.d_elems, a.err);
+          ab_store<64>(acc + (uint32_t)half, a.scale, stg, lane, row0, a.S, a.dk + at_head + half, a.d_row_stride,
+                       a.dk, a.d_elems, a.err);
       } else {
-        ab_store<64>(acc + (uint32_t)(wg * 64), a.scale, stg, lane, row0, a.S,
-                     a.dq + head * a.d_head_stride + wg * 64, a.d_row_stride, a.dq, a.d_elems, a.err);
+        ab_store<32>(acc + (uint32_t)(wg * 32), a.scale, stg, lane, row0, a.S, a.dq + at_head + wg * 32,
+                     a.d_row_stride, a.dq, a.d_elems, a.err);
       }
     }
   }
@@ -408,26 +507,33 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                          const AttnBwdArgs args) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // no static shared memory: the dynamic part starts at a multiple of 1024,
+  // as the swizzled tiles need
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   AbSmem sm;
-  sm.f1 = smem;
+  sm.f1 = smem_raw;
   sm.f2 = sm.f1 + AB_TILE;
   sm.g1 = sm.f2 + AB_TILE;
-  sm.g2 = sm.g1 + AB_STAGES * AB_TILE;
-  sm.rowvals = sm.g2 + AB_STAGES * AB_TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm.rowvals + AB_STAGES * AB_ROWVALS);
+  sm.g2 = sm.g1 + AB_ST1 * AB_TILE;
+  sm.rowvals = sm.g2 + AB_ST2 * AB_TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm.rowvals + 2 * AB_ROWVALS);
   sm.f1_full = bars;
   sm.f2_full = bars + 1;
   sm.g1_full = bars + 2;
-  sm.g1_empty = sm.g1_full + AB_STAGES;
-  sm.g2_full = sm.g1_empty + AB_STAGES;
-  sm.g2_empty = sm.g2_full + AB_STAGES;
-  sm.s_full = sm.g2_empty + AB_STAGES;
-  sm.p_full = sm.s_full + 1;
+  sm.g1_empty = sm.g1_full + AB_ST1;
+  sm.g2_full = sm.g1_empty + AB_ST1;
+  sm.g2_empty = sm.g2_full + AB_ST2;
+  sm.rv_full = sm.g2_empty + AB_ST2;
+  sm.rv_empty = sm.rv_full + 2;
+  sm.s_full = sm.rv_empty + 2;
+  sm.s_empty = sm.s_full + 1;
+  sm.p_full = sm.s_empty + 1;
   sm.dp_full = sm.p_full + 1;
-  sm.ds_full = sm.dp_full + 1;
-  sm.acc_full = sm.ds_full + 1;
+  sm.dp_empty = sm.dp_full + 1;
+  sm.ds_full = sm.dp_empty + 1;
+  sm.ds_empty = sm.ds_full + 1;
+  sm.f_full = sm.ds_empty + 1;
+  sm.acc_full = sm.f_full + 1;
   sm.drain = sm.acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -437,16 +543,26 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(sm.f1_full, 1);
     mbar_init(sm.f2_full, 1);
-    for (int s = 0; s < AB_STAGES; ++s) {
+    for (int s = 0; s < AB_ST1; ++s) {
       mbar_init(&sm.g1_full[s], 1);
       mbar_init(&sm.g1_empty[s], 1);
+    }
+    for (int s = 0; s < AB_ST2; ++s) {
       mbar_init(&sm.g2_full[s], 1);
       mbar_init(&sm.g2_empty[s], 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.rv_full[s], 1);
+      mbar_init(&sm.rv_empty[s], AB_WARPS);
+    }
     mbar_init(sm.s_full, 1);
-    mbar_init(sm.p_full, 8);
+    mbar_init(sm.s_empty, AB_WARPS);
+    mbar_init(sm.p_full, AB_WARPS);
     mbar_init(sm.dp_full, 1);
-    mbar_init(sm.ds_full, 8);
+    mbar_init(sm.dp_empty, AB_WARPS);
+    mbar_init(sm.ds_full, AB_WARPS);
+    mbar_init(sm.ds_empty, 1);
+    mbar_init(sm.f_full, AB_WARPS);
     mbar_init(sm.acc_full, 1);
     mbar_init(sm.drain, 1);
     *abort_flag = timeout_recorded(args.err) ? 1 : 0;   // sticky timeout of an earlier launch
@@ -494,9 +610,9 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   if (e != cudaSuccess) return e;
   e = launch_kernel(attention_bwd_kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
   if (e != cudaSuccess) return e;
-  set_kernel_info("attention_bwd_kernel tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d acc=f32 "
-                  "tmem=S,dP,A1,A2 P,dS-in-TMEM grid=%ux%ux2",
-                  AB_STAGES, grid.x, grid.y);
+  set_kernel_info("attention_bwd_kernel tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d,%d acc=f32 "
+                  "P,dS-in-TMEM grid=%ux%ux2",
+                  AB_ST1, AB_ST2, grid.x, grid.y);
   return cudaGetLastError();
 }
 
