@@ -1272,20 +1272,41 @@ u128 mul_hi(u128 a, u128 b) {
   const u128 mid = (ll >> 64) + (uint64_t)lh + (uint64_t)hl;
   return hh + (lh >> 64) + (hl >> 64) + (mid >> 64);
 }
-u128 fraction(long double x) {   // 0 <= x < 1
-  const long double hi = std::ldexp(x, 64);
-  const uint64_t top = (uint64_t)hi;
-  return ((u128)top << 64) | (uint64_t)std::ldexp(hi - (long double)top, 64);
+u128 fraction(double x) {   // 0 <= x < 1, exactly
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(x, &e), 53);   // x = m 2^(e - 53)
+  const int shift = 128 - 53 + e;
+  return shift >= 0 ? (u128)m << shift : (shift > -64 ? (u128)(m >> -shift) : 0);
+}
+u128 inverse(float b) {     // 1 / b for b >= 1
+  int e;
+  const uint32_t m = (uint32_t)std::ldexp(std::frexp(b, &e), 24);   // b = m 2^(e - 24), 2^23 <= m < 2^24
+  const u128 q = ~(u128)0 / m;                                      // 2^128 / m
+  return e <= 24 ? (e <= 1 && m == (1u << 23) ? ~(u128)0 : q << (24 - e)) : q >> (e - 24);
+}
+// b^(-1/n) for b >= 1: a double's root and one Newton step on its n-th power.
+u128 inverse_root(float b, int n) {
+  const double r0 = std::pow((double)b, -1.0 / n);
+  if (!(r0 < 1.0)) return ~(u128)0;
+  const u128 r = fraction(r0);
+  if (!(b < 1.0995116e12f)) return r;   // 2^40: beyond, the power has too few digits for the step
+  u128 power = ~(u128)0, square = r;
+  for (int k = n; k > 0; k >>= 1) {
+    if (k & 1) power = mul_hi(power, square);
+    square = mul_hi(square, square);
+  }
+  const double off = (double)(__int128)(inverse(b) - power) / ((double)power * n);
+  return r + (u128)(__int128)std::ldexp(r0 * off, 128);
 }
 
 // Turns per position of every rotated pair in 64-bit fixed point (omega <= 1
-// radian, so below 1/6): a geometric series, its ratio and products held as
-// 128-bit fractions, since a position of 2^31 would multiply the rounding of a
-// double into 2^-24 turns, and a pow per frequency costs more than the launch.
+// radian, so below 1/6): a geometric series in 128-bit fractions, since a
+// position of 2^31 would multiply the rounding of a double into 2^-24 turns,
+// and a long double pow per frequency costs more than the launch.
 void fill_turns(const h3_rope_config& c, uint64_t* turns) {
-  typedef long double real;
-  const real kInvTwoPi = 0.15915494309189533576888376337251436203L;
+  const u128 kInvTwoPi = ((u128)0x28BE60DB9391054Aull << 64) | 0x7F09D5F47D4D3770ull;
   const int F = c.n_freqs;
+  const double s = c.factor, inv_s = 1.0 / s, per_turn = 1.0 / ((double)c.beta - c.alpha);
   bool done[2] = {false, false};
   int at[2] = {0, 0};
   for (int a = 0; a < c.n_axes; ++a) {
@@ -1296,25 +1317,19 @@ void fill_turns(const h3_rope_config& c, uint64_t* turns) {
     }
     done[scaled] = true;
     at[scaled] = a;
-    const real s = c.factor;
-    real first = kInvTwoPi, base = c.theta;
-    if (scaled && c.scaling == H3_ROPE_SCALE_LINEAR) first /= s;
-    if (scaled && c.scaling == H3_ROPE_SCALE_NTK) base *= std::pow(s, (real)F / (F - 1));
-    const u128 ratio = F > 1 ? fraction(std::pow(base, (real)-1 / F)) : 0;
-    u128 w = fraction(first);
+    const int scaling = scaled ? c.scaling : H3_ROPE_SCALE_NONE;
+    u128 ratio = F > 1 ? inverse_root(c.theta, F) : 0;
+    if (scaling == H3_ROPE_SCALE_NTK) ratio = mul_hi(ratio, inverse_root(c.factor, F - 1));
+    u128 w = kInvTwoPi;
+    if (scaling == H3_ROPE_SCALE_LINEAR) w = mul_hi(w, inverse(c.factor));
     for (int f = 0; f < F; ++f) {
       u128 t = w;
-      if (scaled && c.scaling == H3_ROPE_SCALE_YARN) {
+      if (scaling == H3_ROPE_SCALE_YARN) {
         // turns over the trained length, and by them the share kept
         const double n = (double)c.trained_length * std::ldexp((double)(uint64_t)(w >> 64), -64);
-        if (n <= c.alpha) {
-          t = s > 1 ? mul_hi(w, fraction(1 / s)) : w;
-        } else if (n < c.beta) {
-          const real nn = (real)c.trained_length * std::ldexp((real)(uint64_t)(w >> 64), -64);
-          const real g = (nn - c.alpha) / ((real)c.beta - c.alpha);
-          const real keep = g + (1 - g) / s;
-          if (keep < 1) t = mul_hi(w, fraction(keep));
-        }
+        const double g = n <= c.alpha ? 0.0 : (n >= c.beta ? 1.0 : (n - c.alpha) * per_turn);
+        const double keep = g + (1.0 - g) * inv_s;
+        if (keep < 1.0) t = mul_hi(w, fraction(keep));
       }
       turns[a * F + f] = (uint64_t)(t >> 64);
       w = mul_hi(w, ratio);

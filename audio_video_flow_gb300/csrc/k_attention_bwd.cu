@@ -58,24 +58,40 @@ __device__ __forceinline__ float ab_ex2(float x) {
 // computed in uniform registers, and one lane (`one` != 0) issues.  (With one
 // lane's branch around the loop every operand of every MMA was moved over from
 // vector registers; the products then took 800 cycles instead of 512.)
-__device__ __forceinline__ void ab_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate, uint32_t one) {
+// Four K steps of 16.  Operand steps are immediate: SA, SB in descriptor units
+// of 16 bytes (shared memory) or TMEM columns.
+template <int SA, int SB>
+__device__ __forceinline__ void ab_mma4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\t"
+      "add.s64 a2, a1, %6;\n\tadd.s64 b2, b1, %7;\n\t"
+      "add.s64 a3, a2, %6;\n\tadd.s64 b3, b2, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one), "n"(SA), "n"(SB)
       : "memory");
 }
-__device__ __forceinline__ void ab_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate, uint32_t one) {
+template <int SA, int SB>
+__device__ __forceinline__ void ab_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      "add.s32 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\t"
+      "add.s32 a2, a1, %6;\n\tadd.s64 b2, b1, %7;\n\t"
+      "add.s32 a3, a2, %6;\n\tadd.s64 b3, b2, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one), "n"(SA), "n"(SB)
       : "memory");
 }
 __device__ __forceinline__ void ab_commit(uint64_t* bar, uint32_t one) {
@@ -102,6 +118,17 @@ __device__ __forceinline__ void ab_tmem_st16(uint32_t taddr, const uint32_t (&r)
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// Eight packed columns to TMEM, then this warp's arrival at the barrier that the
+// MMA warp waits on.
+__device__ __forceinline__ void ab_hand_over(uint32_t taddr, const uint32_t* r, uint64_t* bar, int lane) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ void ab_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -280,27 +307,22 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
     const uint64_t f1 = sdesc_kmajor(smem_u32(sm.f1)), f2 = sdesc_kmajor(smem_u32(sm.f2));
     const uint64_t g1k = sdesc_kmajor(smem_u32(sm.g1)), g2k = sdesc_kmajor(smem_u32(sm.g2));
     const uint64_t g1m = sdesc_sw128(smem_u32(sm.g1), AB_BOX, 1024), g2m = sdesc_sw128(smem_u32(sm.g2), AB_BOX, 1024);
-    auto issue_ss = [&](uint32_t d, uint64_t f, uint64_t g) {   // F G^T
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint64_t off = (uint64_t)(k >> 2) * kBox + (uint64_t)(k & 3) * 2;
-        ab_mma_ss(tm + d, f + off, g + off, idesc_s, k != 0 ? 1u : 0u, one);
-      }
+    auto issue_ss = [&](uint32_t d, uint64_t f, uint64_t g) {   // F G^T: two 64-channel boxes
+      ab_mma4_ss<2, 2>(tm + d, f, g, idesc_s, 0u, one);
+      ab_mma4_ss<2, 2>(tm + d, f + kBox, g + kBox, idesc_s, 1u, one);
     };
     auto issue_q = [&](uint32_t d, uint64_t g) {                // Q in TMEM times G^T
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint64_t off = (uint64_t)(k >> 2) * kBox + (uint64_t)(k & 3) * 2;
-        ab_mma_ts(tm + d, tm + TM_Q + (uint32_t)(k * 8), g + off, idesc_s, k != 0 ? 1u : 0u, one);
-      }
+      ab_mma4_ts<8, 2>(tm + d, tm + TM_Q, g, idesc_s, 0u, one);
+      ab_mma4_ts<8, 2>(tm + d, tm + TM_Q + 32u, g + kBox, idesc_s, 1u, one);
     };
-    // accumulator += A G, A bf16 in TMEM: the 32 columns of a warpgroup in 16
-    // packed ones, the next warpgroup's 16 + gap columns further
-    auto issue_ts = [&](uint32_t d, uint32_t s, uint32_t gap, uint64_t g, uint32_t accumulate) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        ab_mma_ts(tm + d, tm + s + (uint32_t)((k >> 1) * (16 + gap) + (k & 1) * 8), g + (uint64_t)(k * 128), idesc_a,
-                  k == 0 ? accumulate : 1u, one);
+    // accumulator += A G, A bf16 in TMEM.  Key side, half h: the first or
+    // second 16 of each warpgroup's 32 columns, 8 packed ones at 32 w + 8 h.
+    auto issue_half = [&](uint32_t d, uint32_t s, uint64_t g, int h, uint32_t accumulate) {
+      ab_mma4_ts<32, 256>(tm + d, tm + s + (uint32_t)(8 * h), g + (uint64_t)(128 * h), idesc_a, accumulate, one);
+    };
+    auto issue_ds = [&](uint64_t g, uint32_t accumulate) {      // query side: 64 packed columns in a row
+      ab_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS, g, idesc_a, accumulate, one);
+      ab_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS + 32u, g + 512u, idesc_a, 1u, one);
     };
     // S and dP of the next tile: stages and phases of the rings go round here
     uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;   // the next tile's stage and phase in each ring
@@ -329,10 +351,14 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       const bool more = j + 1 < n;
       const uint32_t ph = (uint32_t)j & 1u, accumulate = j != 0 ? 1u : 0u;
       if (KEYS) {
-        // A2 += P G2, then the next S over P
-        if (!ab_wait(sm.p_full, ph, ctl)) { ok = false; break; }
+        // A2 += P G2 in the halves that the softmax hands over, then the next
+        // S over P
+        if (!ab_wait(&sm.p_full[0], ph, ctl)) { ok = false; break; }
         tc_fence_after();
-        issue_ts(TM_A2, TM_S, 16u, g2m + c2 * kTile, accumulate);
+        issue_half(TM_A2, TM_S, g2m + c2 * kTile, 0, accumulate);
+        if (!ab_wait(&sm.p_full[1], ph, ctl)) { ok = false; break; }
+        tc_fence_after();
+        issue_half(TM_A2, TM_S, g2m + c2 * kTile, 1, 1u);
         ab_commit(&sm.g2_empty[c2], one);
         if (more && !issue_s()) { ok = false; break; }
       } else if (more) {
@@ -340,10 +366,16 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
         if (!ab_wait(sm.s_empty, ph, ctl) || !issue_s()) { ok = false; break; }
         if (!ab_wait(sm.dp_empty, ph, ctl) || !issue_dp()) { ok = false; break; }
       }
-      if (!ab_wait(sm.ds_full, ph, ctl)) { ok = false; break; }
+      if (!ab_wait(&sm.ds_full[0], ph, ctl)) { ok = false; break; }
       tc_fence_after();
-      if (KEYS) issue_ts(TM_A1, TM_DP, 16u, g1m + c1 * kTile, accumulate);
-      else issue_ts(TM_A1, TM_DS, 0u, g1m + c1 * kTile, accumulate);
+      if (KEYS) {
+        issue_half(TM_A1, TM_DP, g1m + c1 * kTile, 0, accumulate);
+        if (!ab_wait(&sm.ds_full[1], ph, ctl)) { ok = false; break; }
+        tc_fence_after();
+        issue_half(TM_A1, TM_DP, g1m + c1 * kTile, 1, 1u);
+      } else {
+        issue_ds(g1m + c1 * kTile, accumulate);
+      }
       ab_commit(&sm.g1_empty[c1], one);
       if (!KEYS) ab_commit(sm.ds_empty, one);
       if (KEYS && more && !issue_dp()) { ok = false; break; }
@@ -411,28 +443,28 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
         if (lane == 0) mbar_arrive(sm.s_empty);
       }
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 l =
-            KEYS ? *reinterpret_cast<const float4*>(rv + c) : make_float4(my_l2, my_l2, my_l2, my_l2);
-        const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])), sl2,
-                                     make_float2(-l.x, -l.y));
-        const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])), sl2,
-                                     make_float2(-l.z, -l.w));
-        const float e0 = ab_ex2(z0.x), e1 = ab_ex2(z0.y), e2 = ab_ex2(z1.x), e3 = ab_ex2(z1.y);
-        p[c] = __float_as_uint(e0);
-        p[c + 1] = __float_as_uint(e1);
-        p[c + 2] = __float_as_uint(e2);
-        p[c + 3] = __float_as_uint(e3);
-        pk[c >> 1] = pack_bf16x2(e0, e1);
-        pk[(c >> 1) + 1] = pack_bf16x2(e2, e3);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+          const float4 l =
+              KEYS ? *reinterpret_cast<const float4*>(rv + c) : make_float4(my_l2, my_l2, my_l2, my_l2);
+          const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])), sl2,
+                                       make_float2(-l.x, -l.y));
+          const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])), sl2,
+                                       make_float2(-l.z, -l.w));
+          const float e0 = ab_ex2(z0.x), e1 = ab_ex2(z0.y), e2 = ab_ex2(z1.x), e3 = ab_ex2(z1.y);
+          p[c] = __float_as_uint(e0);
+          p[c + 1] = __float_as_uint(e1);
+          p[c + 2] = __float_as_uint(e2);
+          p[c + 3] = __float_as_uint(e3);
+          if (KEYS) {
+            pk[c >> 1] = pack_bf16x2(e0, e1);
+            pk[(c >> 1) + 1] = pack_bf16x2(e2, e3);
+          }
+        }
+        if (KEYS) ab_hand_over(s_base + (uint32_t)(8 * h), &pk[8 * h], &sm.p_full[h], lane);
       }
-      if (KEYS) {
-        ab_tmem_st16(s_base, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm.p_full);
-      } else if (j == n - 1) {
+      if (!KEYS && j == n - 1) {
         // keys past the end: their K rows are zero, but exp(-lse) times 0
         // must not become NaN where lse is far below 0
         const int valid = a.S - j * 128 - wg * 32;
@@ -451,29 +483,32 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
         if (lane == 0) mbar_arrive(sm.dp_empty);
       }
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 dd =
-            KEYS ? *reinterpret_cast<const float4*>(rv + 128 + c) : make_float4(my_d, my_d, my_d, my_d);
-        const float2 t0 = __fadd2_rn(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])),
-                                     make_float2(-dd.x, -dd.y));
-        const float2 t1 = __fadd2_rn(make_float2(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])),
-                                     make_float2(-dd.z, -dd.w));
-        const float2 u0 = __fmul2_rn(t0, make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])));
-        const float2 u1 = __fmul2_rn(t1, make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])));
-        pk[c >> 1] = pack_bf16x2(u0.x, u0.y);
-        pk[(c >> 1) + 1] = pack_bf16x2(u1.x, u1.y);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+          const float4 dd =
+              KEYS ? *reinterpret_cast<const float4*>(rv + 128 + c) : make_float4(my_d, my_d, my_d, my_d);
+          const float2 t0 = __fadd2_rn(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])),
+                                       make_float2(-dd.x, -dd.y));
+          const float2 t1 = __fadd2_rn(make_float2(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])),
+                                       make_float2(-dd.z, -dd.w));
+          const float2 u0 = __fmul2_rn(t0, make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])));
+          const float2 u1 = __fmul2_rn(t1, make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])));
+          pk[c >> 1] = pack_bf16x2(u0.x, u0.y);
+          pk[(c >> 1) + 1] = pack_bf16x2(u1.x, u1.y);
+        }
+        if (KEYS) ab_hand_over(ds_base + (uint32_t)(8 * h), &pk[8 * h], &sm.ds_full[h], lane);
       }
-      if (!KEYS) {   // the previous dS has been read
+      if (KEYS) {
+        if (lane == 0) mbar_arrive(&sm.rv_empty[j & 1]);
+      } else {   // once the previous dS has been read
         if (!ab_wait(sm.ds_empty, ph ^ 1u, ctl)) { ok = false; break; }
         tc_fence_after();
-      }
-      ab_tmem_st16(ds_base, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(sm.ds_full);
-        if (KEYS) mbar_arrive(&sm.rv_empty[j & 1]);
+        ab_tmem_st16(ds_base, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ds_full[0]);
       }
     }
     if (ok && ab_wait(sm.acc_full, 0, ctl)) {
@@ -527,11 +562,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   sm.rv_empty = sm.rv_full + 2;
   sm.s_full = sm.rv_empty + 2;
   sm.s_empty = sm.s_full + 1;
-  sm.p_full = sm.s_empty + 1;
-  sm.dp_full = sm.p_full + 1;
+  sm.p_full = sm.s_empty + 1;     // [2]
+  sm.dp_full = sm.p_full + 2;
   sm.dp_empty = sm.dp_full + 1;
-  sm.ds_full = sm.dp_empty + 1;
-  sm.ds_empty = sm.ds_full + 1;
+  sm.ds_full = sm.dp_empty + 1;   // [2]
+  sm.ds_empty = sm.ds_full + 2;
   sm.f_full = sm.ds_empty + 1;
   sm.acc_full = sm.f_full + 1;
   sm.drain = sm.acc_full + 1;
@@ -557,10 +592,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     }
     mbar_init(sm.s_full, 1);
     mbar_init(sm.s_empty, AB_WARPS);
-    mbar_init(sm.p_full, AB_WARPS);
     mbar_init(sm.dp_full, 1);
     mbar_init(sm.dp_empty, AB_WARPS);
-    mbar_init(sm.ds_full, AB_WARPS);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sm.p_full[h], AB_WARPS);
+      mbar_init(&sm.ds_full[h], AB_WARPS);
+    }
     mbar_init(sm.ds_empty, 1);
     mbar_init(sm.f_full, AB_WARPS);
     mbar_init(sm.acc_full, 1);

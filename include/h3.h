@@ -381,8 +381,8 @@ typedef enum { H3_BF16 = 0, H3_FP32 = 1 } h3_dtype;
  *   H3_ROPE_SCALE_YARN    by parts: with r = trained_length * omega / (2 pi) turns
  *                         over the trained length and g = (r - alpha) / (beta - alpha)
  *                         clipped to [0, 1]:  g omega + (1 - g) omega / factor
- * Angles are exact to 2^-31 of a turn for every 32-bit position, negative ones
- * included.  Limits: head_dim even, 2 .. 256; n_axes 1 .. 4;
+ * pos is any 32-bit number, negative ones included, and the angles are within
+ * 2^-28 of a turn throughout.  Limits: head_dim even, 2 .. 256; n_axes 1 .. 4;
  * 1 <= n_axes * n_freqs <= 128, 2 * n_axes * n_freqs <= head_dim
  * (H3_ERR_UNSUPPORTED); theta > 1, factor >= 1, trained_length >= 1,
  * 0 <= alpha < beta, magnitude finite and > 0, scaled_axes inside the axes
