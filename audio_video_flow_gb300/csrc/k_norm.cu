@@ -124,7 +124,7 @@ __device__ __forceinline__ void zero_past(float2 (&v)[4], int valid) {
 }
 
 // NV sums over a row's threads, the same value in all of them: a butterfly
-// inside the group (or warp), then the CTA's warps in order.  slot: scratch of
+// inside the group (or warp), then one over the CTA's warps.  slot: scratch of
 // NORM_MAX_WARPS * NV floats; two calls in a row need different ones.
 template <bool BLOCK, int NV>
 __device__ __forceinline__ void row_sum(float (&s)[NV], int tpr, float* slot) {
@@ -133,18 +133,18 @@ __device__ __forceinline__ void row_sum(float (&s)[NV], int tpr, float* slot) {
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
       for (int k = 0; k < NV; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-    const int warp = threadIdx.x >> 5, nw = tpr >> 5;
-    if ((threadIdx.x & 31) == 0)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
 #pragma unroll
       for (int k = 0; k < NV; ++k) slot[warp * NV + k] = s[k];
     __syncthreads();
+    // lane l takes warp (l mod 8)'s sums, 0 past the last warp
 #pragma unroll
-    for (int k = 0; k < NV; ++k) s[k] = slot[k];
+    for (int k = 0; k < NV; ++k) s[k] = (lane & 7) * 32 < tpr ? slot[(lane & 7) * NV + k] : 0.0f;
 #pragma unroll
-    for (int w = 1; w < NORM_MAX_WARPS; ++w)
-      if (w < nw)
+    for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
-        for (int k = 0; k < NV; ++k) s[k] += slot[w * NV + k];
+      for (int k = 0; k < NV; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
   } else {
     for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const Norm
   row_sum<BLOCK>(s, tpr, red[1]);
   float r[R];
 #pragma unroll
-  for (int k = 0; k < R; ++k) r[k] = 1.0f / sqrtf(s[k] * inv_width + a.eps);
+  for (int k = 0; k < R; ++k) r[k] = rsqrtf(s[k] * inv_width + a.eps);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
@@ -257,17 +257,16 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const Norm
 
 // ---------------------------------------------------------------------------
 // Backward.  Persistent CTAs take R rows per thread group and step.  The x and
-// dy of a step are copied asynchronously into a ring of two stages one step
-// ahead (each thread copies and later reads its own chunks, so a stage needs
-// no barrier); the gain is kept in shared memory as fp32; every thread
+// dy of a step are copied asynchronously into a ring of ST stages ahead of
+// their use (each thread copies and later reads its own chunks, so a stage
+// needs no barrier) and then held in registers as fp32: unpacking them again
+// for each of the two or three passes costs more instructions than the
+// arithmetic.  The gain is kept in shared memory as fp32; every thread
 // accumulates dgain (and, with BIAS, dbias) of its own channels in registers
 // over all the CTA's rows.  The CTAs' sums go to the workspace, where
-// norm_param_kernel adds them in CTA order.  R rows at a time share the
-// reductions' latency and keep more bytes in flight.
+// norm_param_kernel adds them in CTA order.
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int NORM_STAGES = 2;
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
@@ -288,8 +287,8 @@ __device__ __forceinline__ void copy8(T* dst, const T* src, int valid) {
 }
 }  // namespace
 
-template <typename T, int NC, int R, bool LAYER, bool BIAS, bool BLOCK>
-__global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const NormArgs a) {
+template <typename T, int NC, int R, int ST, bool LAYER, bool BIAS, bool BLOCK>
+__global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
   __shared__ float red[2][NORM_MAX_WARPS * 2 * R];
   const int tpr = a.tpr;
@@ -297,47 +296,69 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const Norm
   const int g = BLOCK ? 0 : threadIdx.x / tpr;
   const int groups = BLOCK ? 1 : NORM_GROUP_THREADS / tpr;
   const int row = NC * tpr * 8;                   // channels of a row, padded
-  T* ring = reinterpret_cast<T*>(norm_smem);      // [stage][R][x|dy][group][row]
-  float* sgain = reinterpret_cast<float*>(norm_smem + (size_t)NORM_STAGES * R * 2 * groups * row * sizeof(T));
+  // ring: [stage][R][x|dy][group][row]
+  T* ring = reinterpret_cast<T*>(norm_smem) + (size_t)g * row + t * 8;
+  const int which_step = groups * row, stage_step = R * 2 * which_step;
+  float* sgain = reinterpret_cast<float*>(norm_smem + (size_t)ST * stage_step * sizeof(T));
   griddep_launch_dependents();
   griddep_wait();
   const int width = a.width;
   const float inv_width = 1.0f / (float)width;
   const long long step = (long long)gridDim.x * groups * R;
+  // only a thread's last chunk may be partial or missing: layout_of() leaves
+  // no more than that to a width
+  const int last = max(0, min(width - (t + (NC - 1) * tpr) * 8, 8));
+  auto valid = [&](int c) { return c < NC - 1 ? 8 : last; };
 
-  auto at_stage = [&](int st, int k, int which) {
-    return ring + (size_t)(((st * R + k) * 2 + which) * groups + g) * row;
-  };
-  auto at_row = [&](long long u, int64_t row_stride, int64_t head_stride) {
-    const int64_t i = a.heads == 1 ? u : (a.units <= 0xffffffffLL ? (uint32_t)u / (uint32_t)a.heads : u / a.heads);
-    return i * row_stride + (u - i * a.heads) * head_stride;
-  };
-  // rows of a step: base + g + k * groups
-  auto fetch = [&](long long base, int st) {
+  // The rows of a step are base + g + k groups, k < R.  Pointers to x and dy of
+  // the next step to fetch and to dx of the current one advance by a step's
+  // packed rows and heads, and by one more row where the heads wrap round.
+  const int64_t di = step / a.heads;
+  const int dh = (int)(step - di * a.heads);
+  const int64_t adv_x = di * a.x_row + dh * a.x_head, wrap_x = a.x_row - a.heads * a.x_head;
+  const int64_t adv_dy = di * a.dy_row + dh * a.dy_head, wrap_dy = a.dy_row - a.heads * a.dy_head;
+  const int64_t adv_dx = di * a.dx_row + dh * a.dx_head, wrap_dx = a.dx_row - a.heads * a.dx_head;
+  long long base = (long long)blockIdx.x * groups * R;
+  const T *px[R], *pdy[R];
+  T* pdx[R];
+  int nh[R], ch[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const long long u = base + g + k * groups;
+    const int64_t i = u / a.heads;
+    nh[k] = ch[k] = (int)(u - i * a.heads);
+    px[k] = static_cast<const T*>(a.x) + i * a.x_row + nh[k] * a.x_head + t * 8;
+    pdy[k] = static_cast<const T*>(a.dy) + i * a.dy_row + nh[k] * a.dy_head + t * 8;
+    pdx[k] = static_cast<T*>(a.dx) + i * a.dx_row + nh[k] * a.dx_head + t * 8;
+  }
+  // rows of the CTA's step that begins at `from` (uniform), as an int
+  auto rows_left = [&](long long from) { return (int)min(max(a.units - from, 0LL), (long long)(1 << 30)); };
+  auto fetch = [&](long long from, T* to) {
+    const int left = rows_left(from);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const long long u = base + g + k * groups;
-      if (u < a.units) {
-        const T* x = static_cast<const T*>(a.x) + at_row(u, a.x_row, a.x_head);
-        const T* dy = static_cast<const T*>(a.dy) + at_row(u, a.dy_row, a.dy_head);
-        T* to_x = at_stage(st, k, 0);
-        T* to_dy = at_stage(st, k, 1);
+      if (g + k * groups < left) {
+        T* to_x = to + k * 2 * which_step;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
-          if (valid <= 0) continue;
-          if (in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, x + at, valid, a.err, 52))
-            copy8(to_x + at, x + at, valid);
-          if (in_bounds<T>(static_cast<const T*>(a.dy), a.dy_elems, dy + at, valid, a.err, 53))
-            copy8(to_dy + at, dy + at, valid);
+          const int at = c * tpr * 8;
+          if (valid(c) <= 0) continue;
+          if (in_bounds<T>(static_cast<const T*>(a.x), a.x_elems, px[k] + at, valid(c), a.err, 52))
+            copy8(to_x + at, px[k] + at, valid(c));
+          if (in_bounds<T>(static_cast<const T*>(a.dy), a.dy_elems, pdy[k] + at, valid(c), a.err, 53))
+            copy8(to_x + which_step + at, pdy[k] + at, valid(c));
         }
+        nh[k] += dh;
+        const bool wrap = nh[k] >= a.heads;
+        if (wrap) nh[k] -= a.heads;
+        px[k] += adv_x + (wrap ? wrap_x : 0);
+        pdy[k] += adv_dy + (wrap ? wrap_dy : 0);
       }
     }
     cp_async_commit();
   };
-
-  long long base = (long long)blockIdx.x * groups * R;
-  fetch(base, 0);
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) fetch(base + s * step, ring + s * stage_step);
   for (int at = threadIdx.x * 8; at < row; at += blockDim.x * 8) {
     float2 v[4];
     param8(at < width ? a.gain : nullptr, a.param_fp32, at, width - at, 1.0f, v);
@@ -354,37 +375,54 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const Norm
       ag[c][e] = splat(0.0f);
       if (BIAS) ab[c][e] = splat(0.0f);
     }
+  auto gain8 = [&](int at, float2 (&v)[4]) {
+    Chunk<float> c;
+    c.load(sgain + at);
+    c.get(v);
+  };
 
   // every group of the CTA runs the same number of steps: wide rows meet at
   // the reductions' barrier, and half-warp groups at their warp's shuffles
-  int st = 0, parity = 0;
+  const T* from = ring;
+  T* to = ring + (ST - 1) * stage_step;
+  T* const ring_end = ring + ST * stage_step;
+  int parity = 0;
   for (; base < a.units; base += step) {
-    fetch(base + step, st ^ 1);
-    cp_async_wait<1>();
-    float mean[R], mean_w[R], s[2 * R];
+    fetch(base + (ST - 1) * step, to);
+    cp_async_wait<ST - 1>();
+    const int left = rows_left(base);
+    float2 xv[R][NC][4], dv[R][NC][4];
 #pragma unroll
-    for (int k = 0; k < R; ++k) mean[k] = mean_w[k] = 0.0f;
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (valid(c) > 0 && g + k * groups < left) {
+          const T* p = from + k * 2 * which_step + c * tpr * 8;
+          Chunk<T> x, d;
+          x.load(p);
+          d.load(p + which_step);
+          x.get(xv[k][c]);
+          d.get(dv[k][c]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xv[k][c][e] = dv[k][c][e] = splat(0.0f);
+        }
+      }
+    float mean_w[R], s[2 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) mean_w[k] = 0.0f;
     if (LAYER) {
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         float2 sx = splat(0.0f), sw = splat(0.0f);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const int at = (t + c * tpr) * 8;
-          if (at >= width || base + g + k * groups >= a.units) continue;
-          Chunk<T> x, d;
-          Chunk<float> gc;
-          x.load(at_stage(st, k, 0) + at);
-          d.load(at_stage(st, k, 1) + at);
-          gc.load(sgain + at);
-          float2 xv[4], dv[4], gv[4];
-          x.get(xv);
-          d.get(dv);
-          gc.get(gv);
+          float2 gv[4];
+          gain8((t + c * tpr) * 8, gv);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sx = __fadd2_rn(sx, xv[e]);
-            sw = __ffma2_rn(dv[e], gv[e], sw);
+            sx = __fadd2_rn(sx, xv[k][c][e]);
+            sw = __ffma2_rn(dv[k][c][e], gv[e], sw);
           }
         }
         s[2 * k] = sx.x + sx.y;
@@ -393,8 +431,14 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const Norm
       row_sum<BLOCK>(s, tpr, red[0]);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        mean[k] = s[2 * k] * inv_width;
+        const float mean = s[2 * k] * inv_width;
         mean_w[k] = s[2 * k + 1] * inv_width;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xv[k][c][e] = __fadd2_rn(xv[k][c][e], splat(-mean));
+          if (valid(c) < 8) zero_past(xv[k][c], valid(c));
+        }
       }
     }
 #pragma unroll
@@ -402,26 +446,12 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const Norm
       float2 sc = splat(0.0f), sw = splat(0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * tpr) * 8;
-        if (at >= width || base + g + k * groups >= a.units) continue;
-        Chunk<T> x, d;
-        Chunk<float> gc;
-        x.load(at_stage(st, k, 0) + at);
-        d.load(at_stage(st, k, 1) + at);
-        gc.load(sgain + at);
-        float2 xv[4], dv[4], gv[4];
-        x.get(xv);
-        d.get(dv);
-        gc.get(gv);
-        if (LAYER) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) xv[e] = __fadd2_rn(xv[e], splat(-mean[k]));
-          if (width - at < 8) zero_past(xv, width - at);
-        }
+        float2 gv[4];
+        gain8((t + c * tpr) * 8, gv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc = __ffma2_rn(xv[e], xv[e], sc);
-          sw = __ffma2_rn(__fmul2_rn(dv[e], gv[e]), xv[e], sw);
+          sc = __ffma2_rn(xv[k][c][e], xv[k][c][e], sc);
+          sw = __ffma2_rn(__fmul2_rn(dv[k][c][e], gv[e]), xv[k][c][e], sw);
         }
       }
       s[2 * k] = sc.x + sc.y;
@@ -432,38 +462,35 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_bwd_kernel(const Norm
     parity ^= 1;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const long long u = base + g + k * groups;
-      if (u >= a.units) continue;
-      const float r = 1.0f / sqrtf(s[2 * k] * inv_width + a.eps);
+      const float r = rsqrtf(s[2 * k] * inv_width + a.eps);
       const float m = s[2 * k + 1] * r * inv_width;          // mean(w xhat)
-      T* dx = static_cast<T*>(a.dx) + at_row(u, a.dx_row, a.dx_head);
+      const bool have = g + k * groups < left;
+      T* dx = pdx[k];
+      ch[k] += dh;
+      const bool wrap = ch[k] >= a.heads;
+      if (wrap) ch[k] -= a.heads;
+      pdx[k] += adv_dx + (wrap ? wrap_dx : 0);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int at = (t + c * tpr) * 8, valid = min(width - at, 8);
-        if (valid <= 0) continue;
-        Chunk<T> x, d;
-        Chunk<float> gc;
-        x.load(at_stage(st, k, 0) + at);
-        d.load(at_stage(st, k, 1) + at);
-        gc.load(sgain + at);
-        float2 xv[4], dv[4], gv[4];
-        x.get(xv);
-        d.get(dv);
-        gc.get(gv);
+        float2 gv[4];
+        gain8((t + c * tpr) * 8, gv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float2 xhat = xv[e];
-          if (LAYER) xhat = __fadd2_rn(xhat, splat(-mean[k]));
-          xhat = __fmul2_rn(xhat, splat(r));
-          ag[c][e] = __ffma2_rn(dv[e], xhat, ag[c][e]);
-          if (BIAS) ab[c][e] = __fadd2_rn(ab[c][e], dv[e]);
-          float2 w = LAYER ? __ffma2_rn(dv[e], gv[e], splat(-mean_w[k])) : __fmul2_rn(dv[e], gv[e]);
-          xv[e] = __fmul2_rn(__ffma2_rn(xhat, splat(-m), w), splat(r));
+          const float2 d = dv[k][c][e];
+          const float2 xhat = __fmul2_rn(xv[k][c][e], splat(r));
+          ag[c][e] = __ffma2_rn(d, xhat, ag[c][e]);
+          if (BIAS) ab[c][e] = __fadd2_rn(ab[c][e], d);
+          const float2 w = LAYER ? __ffma2_rn(d, gv[e], splat(-mean_w[k])) : __fmul2_rn(d, gv[e]);
+          gv[e] = __fmul2_rn(__ffma2_rn(xhat, splat(-m), w), splat(r));
         }
-        if (in_bounds<T>(static_cast<const T*>(a.dx), a.dx_elems, dx + at, valid, a.err, 54)) put8(dx + at, valid, xv);
+        dx += c == 0 ? 0 : tpr * 8;
+        if (have && valid(c) > 0 &&
+            in_bounds<T>(static_cast<const T*>(a.dx), a.dx_elems, dx, valid(c), a.err, 54))
+          put8(dx, valid(c), gv);
       }
     }
-    st ^= 1;
+    from = from + stage_step == ring_end ? ring : from + stage_step;
+    to = to + stage_step == ring_end ? ring : to + stage_step;
   }
   cp_async_wait<0>();
 
@@ -544,26 +571,41 @@ struct NormLayout {
   int nc, tpr;
   bool block;
 };
-NormLayout layout_of(int width, int wide_nc) {
-  const int n = (width + 7) / 8;
+// Every thread's chunks but the last exist: (nc - 1) tpr chunks are no more than
+// the row's n.
+NormLayout group_layout(int n) {
   NormLayout l;
-  l.block = n > NORM_GROUP_CHUNKS;
-  if (l.block) {
-    l.nc = wide_nc;
-    l.tpr = (n + 32 * l.nc - 1) / (32 * l.nc) * 32;
-  } else {
-    l.nc = n <= 32 ? 1 : (n <= 64 ? 2 : 4);
-    l.tpr = 4;
-    while (l.tpr * l.nc < n) l.tpr *= 2;
-  }
+  l.block = false;
+  l.nc = n <= 32 ? 1 : (n <= 64 ? 2 : 4);
+  l.tpr = 4;
+  while (l.tpr * l.nc < n) l.tpr *= 2;
   return l;
 }
-// Forward, wide rows: 8 chunks per thread.  Backward: 3 (the accumulators are
-// 16 registers a chunk), 4 where 8 warps do not reach with 3.
-NormLayout fwd_layout(int width) { return layout_of(width, 8); }
-NormLayout bwd_layout(int width) { return layout_of(width, width > 8 * 3 * 32 * NORM_MAX_WARPS ? 4 : 3); }
+NormLayout block_layout(int n, int nc) {
+  NormLayout l;
+  l.block = true;
+  l.nc = nc;
+  l.tpr = (n + 32 * nc - 1) / (32 * nc) * 32;
+  return l;
+}
+// Forward, wide rows: 8 chunks per thread (here any chunk may be missing).
+NormLayout fwd_layout(int width) {
+  const int n = (width + 7) / 8;
+  return n > NORM_GROUP_CHUNKS ? block_layout(n, 8) : group_layout(n);
+}
+// Backward: as many chunks as 8 warps need, at most 3 while they reach (the
+// accumulators are 16 registers a chunk).
+NormLayout bwd_layout(int width) {
+  const int n = (width + 7) / 8;
+  if (n <= 64) return group_layout(n);
+  return block_layout(n, n <= 32 * NORM_MAX_WARPS ? 1 : (n <= 3 * 32 * NORM_MAX_WARPS ? 3 : 4));
+}
 
-// Rows per group and step of the backward kernel, and its shared memory.
+// Rows per group and step and ring stages of the backward kernel: with narrow
+// rows two per step, so that their reductions overlap; stages as far as two
+// CTAs of the widest rows fit on an SM.
+constexpr int norm_bwd_rows(int nc) { return nc == 1 ? 2 : 1; }
+constexpr int norm_bwd_stages(bool fp32) { return fp32 ? 2 : 4; }
 struct NormBwdPlan {
   NormLayout l;
   int rows, threads, groups;
@@ -575,11 +617,9 @@ NormBwdPlan bwd_plan(long long units, int width, bool fp32) {
   p.l = bwd_layout(width);
   p.threads = p.l.block ? p.l.tpr : NORM_GROUP_THREADS;
   p.groups = p.threads / p.l.tpr;
+  p.rows = norm_bwd_rows(p.l.nc);
   const size_t row = (size_t)p.l.nc * p.l.tpr * 8;
-  auto smem = [&](int r) { return (size_t)NORM_STAGES * r * 2 * p.groups * row * (fp32 ? 4 : 2) + row * 4; };
-  p.rows = p.l.nc == 1 ? 4 : 2;
-  if (smem(p.rows) > kNormSmemMax) p.rows = 1;
-  p.smem = smem(p.rows);
+  p.smem = (size_t)norm_bwd_stages(fp32) * p.rows * 2 * p.groups * row * (fp32 ? 4 : 2) + row * 4;
   if (!p.l.block && p.smem < (size_t)p.groups * row * 4) p.smem = (size_t)p.groups * row * 4;
   // at most what fits by shared memory and four: the workspace is sized for
   // these, the launch takes as many as the kernel's registers let be resident
@@ -635,11 +675,12 @@ cudaError_t launch_fwd_t(NormArgs& a, cudaStream_t st) {
   return launch_fwd<T, 4, 1, false>(a, NORM_GROUP_THREADS, st);
 }
 
-template <typename T, int NC, int R, bool BLOCK>
+template <typename T, int NC, bool BLOCK>
 cudaError_t launch_bwd(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_t st) {
+  constexpr int R = norm_bwd_rows(NC), ST = norm_bwd_stages(sizeof(T) == 4);
   return with_flag(a.layer != 0, [&](auto layer) {
     return with_flag(bias, [&](auto with_bias) {
-      auto kernel = norm_bwd_kernel<T, NC, R, decltype(layer)::value, decltype(with_bias)::value, BLOCK>;
+      auto kernel = norm_bwd_kernel<T, NC, R, ST, decltype(layer)::value, decltype(with_bias)::value, BLOCK>;
       if (p.smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
@@ -653,13 +694,9 @@ cudaError_t launch_bwd(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_
 }
 template <typename T>
 cudaError_t launch_bwd_t(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_t st) {
-  if (p.l.block) {
-    if (p.l.nc == 3) return p.rows == 2 ? launch_bwd<T, 3, 2, true>(a, p, bias, st) : launch_bwd<T, 3, 1, true>(a, p, bias, st);
-    return p.rows == 2 ? launch_bwd<T, 4, 2, true>(a, p, bias, st) : launch_bwd<T, 4, 1, true>(a, p, bias, st);
-  }
-  if (p.l.nc == 1) return launch_bwd<T, 1, 4, false>(a, p, bias, st);
-  if (p.l.nc == 2) return launch_bwd<T, 2, 2, false>(a, p, bias, st);
-  return p.rows == 2 ? launch_bwd<T, 4, 2, false>(a, p, bias, st) : launch_bwd<T, 4, 1, false>(a, p, bias, st);
+  if (!p.l.block) return p.l.nc == 1 ? launch_bwd<T, 1, false>(a, p, bias, st) : launch_bwd<T, 2, false>(a, p, bias, st);
+  if (p.l.nc == 1) return launch_bwd<T, 1, true>(a, p, bias, st);
+  return p.l.nc == 3 ? launch_bwd<T, 3, true>(a, p, bias, st) : launch_bwd<T, 4, true>(a, p, bias, st);
 }
 }  // namespace
 
