@@ -1350,7 +1350,7 @@ h3_status check_norm(const h3_norm_config* c, int32_t n_rows, int32_t n_heads) {
 }
 int norm_part_width(int width) { return (width + 7) & ~7; }
 size_t norm_bwd_ws_bytes(const h3_norm_config& c, int64_t rows, int64_t heads) {
-  return al256((size_t)norm_bwd_ctas(rows * heads, c.width, c.dtype == H3_FP32) * 2 * norm_part_width(c.width) * 4);
+  return al256((size_t)norm_bwd_ctas(rows * heads, c.width, c.dtype == H3_FP32, c.kind == H3_NORM_LAYER) * 2 * norm_part_width(c.width) * 4);
 }
 NormArgs norm_args(const h3_norm_config& c, int32_t n_rows, int32_t n_heads) {
   NormArgs a{};
@@ -1549,7 +1549,7 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   a.x_elems = view_elems(n_rows, n_heads, cfg->width, a.x_row, a.x_head);
   a.dy_elems = view_elems(n_rows, n_heads, cfg->width, a.dy_row, a.dy_head);
   a.dx_elems = view_elems(n_rows, n_heads, cfg->width, a.dx_row, a.dx_head);
-  a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width, a.fp32) * 2 * a.part_width : 0;
+  a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width, a.fp32, a.layer) * 2 * a.part_width : 0;
   return cuda_st(launch_norm_bwd(a, dgain, dbias, stream));
 }
 

@@ -314,7 +314,7 @@ struct NormArgs {
   uint32_t* err;
 };
 constexpr int kNormMaxWidth = 8192;
-int norm_bwd_ctas(long long units, int width, bool fp32);   // CTAs of the backward kernel on this GPU
+int norm_bwd_ctas(long long units, int width, bool fp32, bool layer);   // CTAs of the backward kernel on this GPU
 cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st);
 cudaError_t launch_norm_bwd(NormArgs a, float* dgain, float* dbias, cudaStream_t st);
 

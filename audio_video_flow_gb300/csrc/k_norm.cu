@@ -22,12 +22,16 @@
 
 #include <mutex>
 #include <type_traits>
+#ifndef NV_MINNC
+#define NV_MINNC 3
+#endif
 #include <vector>
 
 namespace h3 {
 
 namespace {
 constexpr int NORM_GROUP_THREADS = 256;   // CTA of rows of at most 1024 channels
+constexpr int NORM_BWD_GROUP_THREADS = 256, NORM_BWD_GROUP_CTAS = 2;   // the same of the backward kernel
 constexpr int NORM_GROUP_CHUNKS = 128;    // the widest such row
 constexpr int NORM_MAX_WARPS = 8;
 
@@ -287,14 +291,15 @@ __device__ __forceinline__ void copy8(T* dst, const T* src, int valid) {
 }
 }  // namespace
 
-template <typename T, int NC, int R, int ST, bool LAYER, bool BIAS, bool BLOCK>
-__global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_kernel(const NormArgs a) {
+template <typename T, int NC, int R, int ST, bool HOLD, bool LAYER, bool BIAS, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 32 * NORM_MAX_WARPS : NORM_BWD_GROUP_THREADS, BLOCK ? (NC == 4 ? 1 : 2) : NORM_BWD_GROUP_CTAS)
+    norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
   __shared__ float red[2][NORM_MAX_WARPS * 2 * R];
   const int tpr = a.tpr;
   const int t = BLOCK ? threadIdx.x : threadIdx.x & (tpr - 1);
   const int g = BLOCK ? 0 : threadIdx.x / tpr;
-  const int groups = BLOCK ? 1 : NORM_GROUP_THREADS / tpr;
+  const int groups = BLOCK ? 1 : NORM_BWD_GROUP_THREADS / tpr;
   const int row = NC * tpr * 8;                   // channels of a row, padded
   // ring: [stage][R][x|dy][group][row]
   T* ring = reinterpret_cast<T*>(norm_smem) + (size_t)g * row + t * 8;
@@ -391,38 +396,54 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_
     fetch(base + (ST - 1) * step, to);
     cp_async_wait<ST - 1>();
     const int left = rows_left(base);
-    float2 xv[R][NC][4], dv[R][NC][4];
+    // x and dy of a row's chunk: unpacked once (HOLD), or again for each pass
+    float2 xv[HOLD ? R : 1][HOLD ? NC : 1][4], dv[HOLD ? R : 1][HOLD ? NC : 1][4];
+    auto unpack = [&](int k, int c, float2 (&x)[4], float2 (&d)[4]) {
+      if (valid(c) > 0 && g + k * groups < left) {
+        const T* p = from + k * 2 * which_step + c * tpr * 8;
+        Chunk<T> xc, dc;
+        xc.load(p);
+        dc.load(p + which_step);
+        xc.get(x);
+        dc.get(d);
+      } else {
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (valid(c) > 0 && g + k * groups < left) {
-          const T* p = from + k * 2 * which_step + c * tpr * 8;
-          Chunk<T> x, d;
-          x.load(p);
-          d.load(p + which_step);
-          x.get(xv[k][c]);
-          d.get(dv[k][c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) xv[k][c][e] = dv[k][c][e] = splat(0.0f);
-        }
+        for (int e = 0; e < 4; ++e) x[e] = d[e] = splat(0.0f);
       }
-    float mean_w[R], s[2 * R];
+    };
+    auto row_of = [&](int k, int c, float2 (&x)[4], float2 (&d)[4]) {
+      if (HOLD) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) mean_w[k] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          x[e] = xv[HOLD ? k : 0][HOLD ? c : 0][e];
+          d[e] = dv[HOLD ? k : 0][HOLD ? c : 0][e];
+        }
+      } else {
+        unpack(k, c, x, d);
+      }
+    };
+    if (HOLD) {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) unpack(k, c, xv[HOLD ? k : 0][HOLD ? c : 0], dv[HOLD ? k : 0][HOLD ? c : 0]);
+    }
+    float mean[R], mean_w[R], s[2 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) mean[k] = mean_w[k] = 0.0f;
     if (LAYER) {
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         float2 sx = splat(0.0f), sw = splat(0.0f);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          float2 gv[4];
+          float2 gv[4], x[4], d[4];
+          row_of(k, c, x, d);
           gain8((t + c * tpr) * 8, gv);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sx = __fadd2_rn(sx, xv[k][c][e]);
-            sw = __ffma2_rn(dv[k][c][e], gv[e], sw);
+            sx = __fadd2_rn(sx, x[e]);
+            sw = __ffma2_rn(d[e], gv[e], sw);
           }
         }
         s[2 * k] = sx.x + sx.y;
@@ -431,14 +452,8 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_
       row_sum<BLOCK>(s, tpr, red[0]);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        const float mean = s[2 * k] * inv_width;
+        mean[k] = s[2 * k] * inv_width;
         mean_w[k] = s[2 * k + 1] * inv_width;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) xv[k][c][e] = __fadd2_rn(xv[k][c][e], splat(-mean));
-          if (valid(c) < 8) zero_past(xv[k][c], valid(c));
-        }
       }
     }
 #pragma unroll
@@ -446,12 +461,22 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_
       float2 sc = splat(0.0f), sw = splat(0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        float2 gv[4];
+        float2 gv[4], x[4], d[4];
+        row_of(k, c, x, d);
         gain8((t + c * tpr) * 8, gv);
+        if (LAYER) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = __fadd2_rn(x[e], splat(-mean[k]));
+          if (valid(c) < 8) zero_past(x, valid(c));
+          if (HOLD) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xv[HOLD ? k : 0][HOLD ? c : 0][e] = x[e];
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc = __ffma2_rn(xv[k][c][e], xv[k][c][e], sc);
-          sw = __ffma2_rn(__fmul2_rn(dv[k][c][e], gv[e]), xv[k][c][e], sw);
+          sc = __ffma2_rn(x[e], x[e], sc);
+          sw = __ffma2_rn(__fmul2_rn(d[e], gv[e]), x[e], sw);
         }
       }
       s[2 * k] = sc.x + sc.y;
@@ -472,15 +497,16 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_
       pdx[k] += adv_dx + (wrap ? wrap_dx : 0);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        float2 gv[4];
+        float2 gv[4], x[4], d[4];
+        row_of(k, c, x, d);
         gain8((t + c * tpr) * 8, gv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 d = dv[k][c][e];
-          const float2 xhat = __fmul2_rn(xv[k][c][e], splat(r));
-          ag[c][e] = __ffma2_rn(d, xhat, ag[c][e]);
-          if (BIAS) ab[c][e] = __fadd2_rn(ab[c][e], d);
-          const float2 w = LAYER ? __ffma2_rn(d, gv[e], splat(-mean_w[k])) : __fmul2_rn(d, gv[e]);
+          const float2 cx = LAYER && !HOLD ? __fadd2_rn(x[e], splat(-mean[k])) : x[e];
+          const float2 xhat = __fmul2_rn(cx, splat(r));
+          ag[c][e] = __ffma2_rn(d[e], xhat, ag[c][e]);
+          if (BIAS) ab[c][e] = __fadd2_rn(ab[c][e], d[e]);
+          const float2 w = LAYER ? __ffma2_rn(d[e], gv[e], splat(-mean_w[k])) : __fmul2_rn(d[e], gv[e]);
           gv[e] = __fmul2_rn(__ffma2_rn(xhat, splat(-m), w), splat(r));
         }
         dx += c == 0 ? 0 : tpr * 8;
@@ -515,7 +541,7 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS, NC == 4 ? 1 : 2) norm_bwd_
       for (int c = 0; c < NC; ++c)
         put8(comb + (size_t)g * row + (t + c * tpr) * 8, 8, which == 0 ? ag[c] : ab[BIAS ? c : 0]);
       __syncthreads();
-      for (int at = threadIdx.x; at < width; at += NORM_GROUP_THREADS) {
+      for (int at = threadIdx.x; at < width; at += NORM_BWD_GROUP_THREADS) {
         float v = 0.0f;
         for (int k = 0; k < groups; ++k) v += comb[(size_t)k * row + at];
         float* p = part + which * a.part_width + at;
@@ -564,6 +590,7 @@ __global__ void __launch_bounds__(256) norm_param_kernel(const float* part, int 
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kNormSmemMax = 227 * 1024;
+constexpr int kNormBwdCtasPerSm = 4;
 
 // Thread layout of a width: chunks per thread nc, threads per row tpr (a power
 // of two up to 32 for rows of at most 1024 channels, whole warps beyond).
@@ -601,30 +628,35 @@ NormLayout bwd_layout(int width) {
   return block_layout(n, n <= 32 * NORM_MAX_WARPS ? 1 : (n <= 3 * 32 * NORM_MAX_WARPS ? 3 : 4));
 }
 
-// Rows per group and step and ring stages of the backward kernel: with narrow
-// rows two per step, so that their reductions overlap; stages as far as two
-// CTAs of the widest rows fit on an SM.
-constexpr int norm_bwd_rows(int nc) { return nc == 1 ? 2 : 1; }
-constexpr int norm_bwd_stages(bool fp32) { return fp32 ? 2 : 4; }
+// Rows per group and step, ring stages, and whether rows are held as fp32.
+struct NormBwdShape {
+  int rows, stages;
+  bool hold;
+};
+constexpr NormBwdShape bwd_shape(int nc, bool fp32, bool layer) {
+  if (layer && !fp32 && nc >= NV_MINNC) return {2, 2, false};
+  return {nc == 1 ? 2 : 1, fp32 ? 2 : 4, true};
+}
 struct NormBwdPlan {
   NormLayout l;
   int rows, threads, groups;
   size_t smem;
   int ctas;
 };
-NormBwdPlan bwd_plan(long long units, int width, bool fp32) {
+NormBwdPlan bwd_plan(long long units, int width, bool fp32, bool layer) {
   NormBwdPlan p;
   p.l = bwd_layout(width);
-  p.threads = p.l.block ? p.l.tpr : NORM_GROUP_THREADS;
+  p.threads = p.l.block ? p.l.tpr : NORM_BWD_GROUP_THREADS;
   p.groups = p.threads / p.l.tpr;
-  p.rows = norm_bwd_rows(p.l.nc);
+  const NormBwdShape sh = bwd_shape(p.l.nc, fp32, layer);
+  p.rows = sh.rows;
   const size_t row = (size_t)p.l.nc * p.l.tpr * 8;
-  p.smem = (size_t)norm_bwd_stages(fp32) * p.rows * 2 * p.groups * row * (fp32 ? 4 : 2) + row * 4;
+  p.smem = (size_t)sh.stages * p.rows * 2 * p.groups * row * (fp32 ? 4 : 2) + row * 4;
   if (!p.l.block && p.smem < (size_t)p.groups * row * 4) p.smem = (size_t)p.groups * row * 4;
   // at most what fits by shared memory and four: the workspace is sized for
   // these, the launch takes as many as the kernel's registers let be resident
   const int per_sm = (int)(kNormSmemMax / (p.smem + 1024));
-  const long long most = (long long)(per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm)) * num_sms();
+  const long long most = (long long)(per_sm < 1 ? 1 : (per_sm > kNormBwdCtasPerSm ? kNormBwdCtasPerSm : per_sm)) * num_sms();
   const long long steps = (units + p.groups * p.rows - 1) / (p.groups * p.rows);
   p.ctas = (int)(steps < most ? steps : most);
   return p;
@@ -677,10 +709,12 @@ cudaError_t launch_fwd_t(NormArgs& a, cudaStream_t st) {
 
 template <typename T, int NC, bool BLOCK>
 cudaError_t launch_bwd(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStream_t st) {
-  constexpr int R = norm_bwd_rows(NC), ST = norm_bwd_stages(sizeof(T) == 4);
   return with_flag(a.layer != 0, [&](auto layer) {
     return with_flag(bias, [&](auto with_bias) {
-      auto kernel = norm_bwd_kernel<T, NC, R, ST, decltype(layer)::value, decltype(with_bias)::value, BLOCK>;
+      constexpr bool LAYER = decltype(layer)::value;
+      constexpr NormBwdShape sh = bwd_shape(NC, sizeof(T) == 4, LAYER);
+      auto kernel =
+          norm_bwd_kernel<T, NC, sh.rows, sh.stages, sh.hold, LAYER, decltype(with_bias)::value, BLOCK>;
       if (p.smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
@@ -700,7 +734,9 @@ cudaError_t launch_bwd_t(const NormArgs& a, NormBwdPlan& p, bool bias, cudaStrea
 }
 }  // namespace
 
-int norm_bwd_ctas(long long units, int width, bool fp32) { return bwd_plan(units, width, fp32).ctas; }
+int norm_bwd_ctas(long long units, int width, bool fp32, bool layer) {
+  return bwd_plan(units, width, fp32, layer).ctas;
+}
 
 cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st) {
   cudaError_t e = a.fp32 ? launch_fwd_t<float>(a, st) : launch_fwd_t<__nv_bfloat16>(a, st);
@@ -711,7 +747,7 @@ cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st) {
 }
 
 cudaError_t launch_norm_bwd(NormArgs a, float* dgain, float* dbias, cudaStream_t st) {
-  NormBwdPlan p = bwd_plan(a.units, a.width, a.fp32);
+  NormBwdPlan p = bwd_plan(a.units, a.width, a.fp32, a.layer);
   a.tpr = p.l.tpr;
   const bool bias = dbias != nullptr;
   cudaError_t e = a.fp32 ? launch_bwd_t<float>(a, p, bias, st) : launch_bwd_t<__nv_bfloat16>(a, p, bias, st);
