@@ -172,7 +172,12 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
         dv[i] = *reinterpret_cast<const uint4*>(a.d_o + off);
     }
   }
-  float* out = a.rowvals + ((size_t)head * a.tiles + tile) * 256;
+  // thread `sub` < 8 of a row group also brings, and later writes, row sub * 16 + r0
+  const int mine = sub * 16 + r0, my_row = tile * 128 + mine;
+  float l2 = INFINITY, d = 0.0f;
+  if (sub < 8 && my_row < a.S &&
+      in_bounds<float>(a.lse, a.lse_elems, a.lse + (size_t)head * a.S + my_row, 1, a.err, 42))
+    l2 = a.lse[(size_t)head * a.S + my_row] * 1.44269504088896340736f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
@@ -184,16 +189,12 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (sub == 0) {
-      const int r = i * 16 + r0, row = tile * 128 + r;
-      float l2 = INFINITY;
-      if (row < a.S && in_bounds<float>(a.lse, a.lse_elems, a.lse + (size_t)head * a.S + row, 1, a.err, 42))
-        l2 = a.lse[(size_t)head * a.S + row] * 1.44269504088896340736f;
-      if (in_bounds<float>(a.rowvals, a.rowval_elems, out + r, 129, a.err, 43)) {
-        out[r] = l2;
-        out[128 + r] = s;
-      }
-    }
+    if (sub == i) d = s;
+  }
+  float* out = a.rowvals + ((size_t)head * a.tiles + tile) * 256 + mine;
+  if (sub < 8 && in_bounds<float>(a.rowvals, a.rowval_elems, out, 129, a.err, 43)) {
+    out[0] = l2;
+    out[128] = d;
   }
 }
 
@@ -212,10 +213,12 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
                                          __nv_bfloat16* out, int64_t row_stride, const __nv_bfloat16* base,
                                          size_t elems, uint32_t* err) {
   constexpr int U = NC / 8;
-#pragma unroll 1
+  uint32_t all[NC / 32][32];
+#pragma unroll
+  for (int c = 0; c < NC / 32; ++c) tmem_ld32(taddr + (uint32_t)(c * 32), all[c]);
+#pragma unroll
   for (int c = 0; c < NC / 32; ++c) {
-    uint32_t o[32];
-    tmem_ld32(taddr + (uint32_t)(c * 32), o);
+    uint32_t(&o)[32] = all[c];
     tmem_ld_wait(o);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -228,7 +231,7 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
     }
   }
   __syncwarp();
-#pragma unroll 4
+#pragma unroll
   for (int it = 0; it < U; ++it) {
     const int r = it * (32 / U) + lane / U, u = lane % U;
     __nv_bfloat16* p = out + (int64_t)(row0 + r) * row_stride + u * 8;

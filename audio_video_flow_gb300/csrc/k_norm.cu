@@ -22,10 +22,6 @@
 
 #include <mutex>
 #include <type_traits>
-#ifndef NV_MINNC
-#define NV_MINNC 3
-#endif
-#include <vector>
 
 namespace h3 {
 
@@ -263,8 +259,8 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const Norm
 // Backward.  Persistent CTAs take R rows per thread group and step.  The x and
 // dy of a step are copied asynchronously into a ring of ST stages ahead of
 // their use (each thread copies and later reads its own chunks, so a stage
-// needs no barrier) and then held in registers as fp32: unpacking them again
-// for each of the two or three passes costs more instructions than the
+// needs no barrier) and then, with HOLD, kept in registers as fp32: unpacking
+// them again for each pass costs about as many instructions as the
 // arithmetic.  The gain is kept in shared memory as fp32; every thread
 // accumulates dgain (and, with BIAS, dbias) of its own channels in registers
 // over all the CTA's rows.  The CTAs' sums go to the workspace, where
@@ -629,12 +625,15 @@ NormLayout bwd_layout(int width) {
 }
 
 // Rows per group and step, ring stages, and whether rows are held as fp32.
+// Wide bf16 layer norms take two rows at a time and unpack them for every pass:
+// their second reduction costs more than the unpacking (8192 channels: 112 us
+// against 123 held; RMS norms measure the same either way).
 struct NormBwdShape {
   int rows, stages;
   bool hold;
 };
 constexpr NormBwdShape bwd_shape(int nc, bool fp32, bool layer) {
-  if (layer && !fp32 && nc >= NV_MINNC) return {2, 2, false};
+  if (layer && !fp32 && nc >= 3) return {2, 2, false};
   return {nc == 1 ? 2 : 1, fp32 ? 2 : 4, true};
 }
 struct NormBwdPlan {
@@ -661,7 +660,8 @@ NormBwdPlan bwd_plan(long long units, int width, bool fp32, bool layer) {
   p.ctas = (int)(steps < most ? steps : most);
   return p;
 }
-// CTAs of a kernel that fit on one SM; asked once per kernel and device.
+// CTAs of a kernel that fit on one SM; asked once per kernel, device and shape
+// (when the table is full, every time).
 int resident_ctas(const void* kernel, int threads, size_t smem) {
   struct Entry {
     const void* kernel;
@@ -670,15 +670,21 @@ int resident_ctas(const void* kernel, int threads, size_t smem) {
     int ctas;
   };
   static std::mutex mu;
-  static std::vector<Entry> known;
+  static Entry known[256];
+  static int n_known = 0;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(mu);
-  for (const Entry& e : known)
+  for (int i = 0; i < n_known; ++i) {
+    const Entry& e = known[i];
     if (e.kernel == kernel && e.device == dev && e.threads == threads && e.smem == smem) return e.ctas;
+  }
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) return 1;
-  known.push_back({kernel, dev, threads, smem, n});
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  if (n_known < (int)(sizeof(known) / sizeof(known[0]))) known[n_known++] = {kernel, dev, threads, smem, n};
   return n;
 }
 
