@@ -172,12 +172,7 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
         dv[i] = *reinterpret_cast<const uint4*>(a.d_o + off);
     }
   }
-  // thread `sub` < 8 of a row group also brings, and later writes, row sub * 16 + r0
-  const int mine = sub * 16 + r0, my_row = tile * 128 + mine;
-  float l2 = INFINITY, d = 0.0f;
-  if (sub < 8 && my_row < a.S &&
-      in_bounds<float>(a.lse, a.lse_elems, a.lse + (size_t)head * a.S + my_row, 1, a.err, 42))
-    l2 = a.lse[(size_t)head * a.S + my_row] * 1.44269504088896340736f;
+  float* out = a.rowvals + ((size_t)head * a.tiles + tile) * 256;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
@@ -189,12 +184,16 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (sub == i) d = s;
-  }
-  float* out = a.rowvals + ((size_t)head * a.tiles + tile) * 256 + mine;
-  if (sub < 8 && in_bounds<float>(a.rowvals, a.rowval_elems, out, 129, a.err, 43)) {
-    out[0] = l2;
-    out[128] = d;
+    if (sub == 0) {
+      const int r = i * 16 + r0, row = tile * 128 + r;
+      float l2 = INFINITY;
+      if (row < a.S && in_bounds<float>(a.lse, a.lse_elems, a.lse + (size_t)head * a.S + row, 1, a.err, 42))
+        l2 = a.lse[(size_t)head * a.S + row] * 1.44269504088896340736f;
+      if (in_bounds<float>(a.rowvals, a.rowval_elems, out + r, 129, a.err, 43)) {
+        out[r] = l2;
+        out[128 + r] = s;
+      }
+    }
   }
 }
 
