@@ -18,20 +18,36 @@
 // the query side, a step computes
 //   S = F1 G1^T,  dP = F2 G2^T,  A1 += dS G1,  and on the key side A2 += P G2
 // (S and dP are transposed there: rows are keys, columns queries).
-//   warp 0       TMA producer: F1, F2 once, then G1 and G2 tiles (and on the
-//                key side their rows' log-sum-exp and D) into two-deep rings;
-//   warp 1       MMA issuer (one thread); G1 and G2 are read K-major for S
-//                and dP and MN-major for A1 and A2 from the same tile;
-//   warps 4-11   softmax: warpgroup w takes columns [64 w, 64 w + 64), one
-//                row per thread: P from S into bf16 over the thread's own S
-//                columns, then dS from dP and the P still in registers.
-// Each warp hands P and dS over in two halves of its columns, so that the
-// products that read them begin while the second half is computed.
+//   warp 0       TMA producer: F1, F2 once, then G1 and G2 tiles into rings of
+//                three and two stages;
+//   warp 1       MMA issuer; G1 and G2 are read K-major for S and dP and
+//                MN-major for A1 and A2 from the same tile;
+//   warp 2       on the key side, the query rows' log-sum-exp and D;
+//   warps 4-19   softmax: warpgroup w takes columns [32 w, 32 w + 32), one row
+//                per thread: P from S, then dS from dP and the P still in
+//                registers, both to TMEM as bf16, where they are left operands.
+// P and dS are rounded to bf16 for their products, as the forward kernel's P
+// is: the tensor cores' rate for wider operands is a quarter.  Each result so
+// carries the error of one such rounding (2^-8 of each term, independent ones)
+// beside that of its own; statistics, dS before the rounding and the
+// accumulators are fp32.
+// On the key side each warp hands P and dS over in two halves of its columns,
+// so that the products that read them begin while the second half is computed
+// (8192 rows x 56 heads, that side alone: 1994 -> 1946 us).
 // TMEM: S [0,128), dP [128,256), A1 [256,384); on the key side A2 [384,512), P
-// over S and dS over dP; on the query side Q [384,448) as S's left operand
-// (64 KB less operand traffic from shared memory per step, which is what
-// bounds the products: 128 bytes a cycle) and dS [448,512), so that the next S
-// and dP can be computed as soon as the softmax holds this step's.
+// over S and dS over dP; on the query side Q [384,448) as the left operand of S
+// and dS [448,512), so that the next S and dP can be computed as soon as the
+// softmax holds this step's (4096 rows x 56 heads, that side alone: 446 us;
+// without the early dP 460, with Q from shared memory 466).
+//
+// Bound by the tensor pipe: 83 % active at 4096 rows x 16 heads; 3.43 ms at 8192
+// rows x 56 heads is 1.40 PFLOP/s of the gradient's five products and 1.96 of
+// the seven computed, the rate of a large cuBLAS product.  At 15,860 rows a
+// single call takes 12.5 ms, repeated ones 14.5 at the 1.4 kW power limit.  The
+// rest is each CTA's start and end (about 4 us, 10 % at 4096 rows, half at 505).
+// Tried and slower: G tiles multicast to a pair of CTAs (3.69 ms at 8192 rows:
+// the two then wait for each other), persistent CTAs (3.6 to 3.8), 8 softmax
+// warps of 64 columns (the same).
 #include "h3_device.cuh"
 #include "h3_internal.h"
 
@@ -57,7 +73,8 @@ __device__ __forceinline__ float ab_ex2(float x) {
 // The MMA warp runs its loop converged, so that descriptors and addresses are
 // computed in uniform registers, and one lane (`one` != 0) issues.  (With one
 // lane's branch around the loop every operand of every MMA was moved over from
-// vector registers; the products then took 800 cycles instead of 512.)
+// vector registers; a product then took 800 cycles, not 512, and 8192 rows x 56
+// heads 4.5 ms, not 3.5.)
 // Four K steps of 16.  Operand steps are immediate: SA, SB in descriptor units
 // of 16 bytes (shared memory) or TMEM columns.
 template <int SA, int SB>
@@ -152,7 +169,8 @@ __device__ __forceinline__ void ab_bulk_load(void* dst, const void* src, uint32_
 // ---------------------------------------------------------------------------
 // Row values: for each head and 128-row tile, 128 log-sum-exps in base 2
 // followed by 128 sums D = sum_c dO[c] O[c] (fp32).  Rows past the end get
-// +inf and 0, so their probabilities and dS are 0.  Bound by reading o and dO.
+// +inf and 0, so their probabilities and dS are 0.  Bound by reading o and dO
+// (4 us of a call at 505 rows x 56 heads).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdArgs a) {
   griddep_launch_dependents();

@@ -157,7 +157,8 @@ __device__ __forceinline__ void row_sum(float (&s)[NV], int tpr, float* slot) {
 // Forward: R rows per thread group at a time, NC chunks of each row per
 // thread, kept in registers as read; every row is read and written once.
 // Bound by memory.  Few threads with many chunks each keep more rows, and so
-// more bytes, in flight on an SM than many threads with few.
+// more bytes, in flight on an SM than many threads with few (15,860 x 5376 bf16:
+// 56 us, 6.1 TB/s; with three chunks of 256 threads unpacked on loading 94 us).
 // ---------------------------------------------------------------------------
 template <typename T, int NC, int R, bool LAYER, bool BLOCK>
 __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const NormArgs a) {
@@ -265,6 +266,10 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const Norm
 // accumulates dgain (and, with BIAS, dbias) of its own channels in registers
 // over all the CTA's rows.  The CTAs' sums go to the workspace, where
 // norm_param_kernel adds them in CTA order.
+// Measured, with both launches: 15,860 x 5376 bf16 RMS 86 us (5.9 TB/s), layer norm with
+// bias 115 us (4.4 TB/s: its two reductions and the accumulators of both
+// parameters, 48 registers of a thread, leave 14 warps to an SM); 1824 x 56 rows
+// of 128 20 us, 15,860 x 56 of them 116 us (5.9 TB/s).
 // ---------------------------------------------------------------------------
 namespace {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
