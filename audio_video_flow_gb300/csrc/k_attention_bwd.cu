@@ -27,7 +27,7 @@
 //                per thread: P from S, then dS from dP and the P still in
 //                registers, both to TMEM as bf16, where they are left operands.
 // P and dS are rounded to bf16 for their products, as the forward kernel's P
-// is: the tensor cores' rate for wider operands is a quarter.  Each result so
+// is: tf32 operands have half the rate and twice the bytes.  Each result so
 // carries the error of one such rounding (2^-8 of each term, independent ones)
 // beside that of its own; statistics, dS before the rounding and the
 // accumulators are fp32.

@@ -28,7 +28,7 @@ namespace {
 // loads, eight CTAs: 141 us).
 constexpr int RO_THREADS = 128, RO_CTAS = 5;
 constexpr int RO_BATCH = 4;              // heads whose loads a thread issues before their use
-constexpr int RO_PAIR_THREADS = 256;     // one pair or channel per thread: at most 255 to a head
+constexpr int RO_STAGE_BYTES = 16384;    // the staged form's heads of one CTA
 
 // 16 bytes of channels, as they lie in memory and as fp32.
 template <typename T>
@@ -56,6 +56,17 @@ __device__ __forceinline__ float ro_get(const __nv_bfloat16* p) { return __bfloa
 __device__ __forceinline__ float ro_get(const float* p) { return *p; }
 __device__ __forceinline__ void ro_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void ro_put(float* p, float v) { *p = v; }
+
+// two neighbouring channels, the first at an even place
+__device__ __forceinline__ float2 ro_get2(const __nv_bfloat16* p) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(bf16_lo(v), bf16_hi(v));
+}
+__device__ __forceinline__ float2 ro_get2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void ro_put2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ void ro_put2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
 // sines and cosines of the row, times the magnitude
 __device__ __forceinline__ void ro_angles(const RopePosArgs& a, int64_t row, float* cs, float* sn) {
@@ -202,42 +213,112 @@ __global__ void __launch_bounds__(RO_THREADS, RO_CTAS) rope_kernel(const RopePos
   } while (h0 < h_hi);
 }
 
-// Any other head: one pair, or one passed-through channel, at a time.
+// Any other head: its second channels do not begin a 16-byte vector, or a
+// vector holds rotated and passed-through channels.  A CTA brings whole vectors
+// of a group of heads into shared memory, turns the pairs there, and writes
+// whole vectors back (in place, of a vector that is rotated only in part, the
+// rotated channels alone).
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(RO_PAIR_THREADS) rope_pairs_kernel(const RopePosArgs a) {
-  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+__global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosArgs a) {
+  __shared__ __align__(8) float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+  __shared__ __align__(16) T tile[RO_STAGE_BYTES / sizeof(T)];
   griddep_launch_dependents();
   griddep_wait();
+  constexpr int V = 16 / (int)sizeof(T);
   const int64_t row = blockIdx.x;
   const RoRow<T> rr(a, row);
-  ro_angles(a, row, cs, sn);
-  __syncthreads();
   const int P = a.axes * a.freqs;
-  const int at_once = RO_PAIR_THREADS / a.units;
-  const int u = threadIdx.x % a.units, hg = threadIdx.x / a.units;
-  if (hg >= at_once) return;
   const int h_lo = (int)blockIdx.y * a.heads_per_cta;
-  const int h_hi = min(h_lo + a.heads_per_cta, a.q_heads + a.k_heads);
-  if (u >= P) {
-    const int at = 2 * P + u - P;
-    for (int h = h_lo + hg; h < h_hi; h += at_once) {
-      const T* p = rr.src(a, h) + at;
-      T* d = rr.dst(a, h) + at;
-      if (ro_in_ok(a, h, p, 1) && ro_out_ok(a, h, d, 1)) *d = *p;
+  const int heads = min(a.heads_per_cta, a.q_heads + a.k_heads - h_lo);
+  const int span = a.in_place ? 2 * P : a.width;               // channels that are written
+  const int vecs = (span + V - 1) / V;                         // = a.units
+  // a thread's vectors: (head, place) advanced by RO_THREADS without divisions
+  const int adv_h = RO_THREADS / vecs, adv_v = RO_THREADS - adv_h * vecs;
+  const int first_h = threadIdx.x / vecs, first_v = threadIdx.x - first_h * vecs;
+  const int total = heads * vecs;
+  for (int u = threadIdx.x, h = first_h, v = first_v; u < total; u += RO_THREADS) {
+    const T* p = rr.src(a, h_lo + h) + v * V;
+    const int n = min(V, a.width - v * V);   // (the bytes past a partial vector's become 0)
+    if (ro_in_ok(a, h_lo + h, p, n))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + u * V)), "l"(p),
+                   "r"(n * (int)sizeof(T))
+                   : "memory");
+    h += adv_h;
+    v += adv_v;
+    if (v >= vecs) {
+      v -= vecs;
+      ++h;
     }
-    return;
   }
-  const float c = cs[u], s = sn[u];
-  const int at0 = HALF ? u : 2 * u, at1 = HALF ? P + u : 2 * u + 1;
-  for (int h = h_lo + hg; h < h_hi; h += at_once) {
-    const T* p = rr.src(a, h);
-    T* d = rr.dst(a, h);
-    if (!ro_in_ok(a, h, p + at0, 1) || !ro_in_ok(a, h, p + at1, 1) || !ro_out_ok(a, h, d + at0, 1) ||
-        !ro_out_ok(a, h, d + at1, 1))
-      continue;
-    const float x0 = ro_get(p + at0), x1 = ro_get(p + at1);
-    ro_put(d + at0, __fmaf_rn(x0, c, -(x1 * s)));
-    ro_put(d + at1, __fmaf_rn(x0, s, x1 * c));
+  ro_angles(a, row, cs, sn);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  // two pairs at a time (of an odd number, the last alone)
+  const int twos = (P + 1) / 2, stride = vecs * V;
+  const int dh = RO_THREADS / twos, dt = RO_THREADS - dh * twos;
+  int h = threadIdx.x / twos, two = threadIdx.x - h * twos;
+  while (h < heads) {
+    const int pair = 2 * two;
+    const bool both = pair + 1 < P;
+    T* x = tile + h * stride + (HALF ? pair : 2 * pair);
+    const float2 c = *reinterpret_cast<const float2*>(cs + pair), sv = *reinterpret_cast<const float2*>(sn + pair);
+    if (HALF) {
+      T* y = x + P;
+      const bool even = (P & 1) == 0;
+      float2 x0, x1;
+      if (both) {
+        x0 = ro_get2(x);
+        if (even) x1 = ro_get2(y);
+        else x1 = make_float2(ro_get(y), ro_get(y + 1));
+      } else {
+        x0 = make_float2(ro_get(x), 0.0f);
+        x1 = make_float2(ro_get(y), 0.0f);
+      }
+      const float2 r0 = make_float2(__fmaf_rn(x0.x, c.x, -(x1.x * sv.x)), __fmaf_rn(x0.y, c.y, -(x1.y * sv.y)));
+      const float2 r1 = make_float2(__fmaf_rn(x0.x, sv.x, x1.x * c.x), __fmaf_rn(x0.y, sv.y, x1.y * c.y));
+      if (both) {
+        ro_put2(x, r0);
+        if (even) {
+          ro_put2(y, r1);
+        } else {
+          ro_put(y, r1.x);
+          ro_put(y + 1, r1.y);
+        }
+      } else {
+        ro_put(x, r0.x);
+        ro_put(y, r1.x);
+      }
+    } else {
+      const float2 u = ro_get2(x);
+      ro_put2(x, make_float2(__fmaf_rn(u.x, c.x, -(u.y * sv.x)), __fmaf_rn(u.x, sv.x, u.y * c.x)));
+      if (both) {
+        const float2 w = ro_get2(x + 2);
+        ro_put2(x + 2, make_float2(__fmaf_rn(w.x, c.y, -(w.y * sv.y)), __fmaf_rn(w.x, sv.y, w.y * c.y)));
+      }
+    }
+    h += dh;
+    two += dt;
+    if (two >= twos) {
+      two -= twos;
+      ++h;
+    }
+  }
+  __syncthreads();
+  for (int u = threadIdx.x, hh = first_h, v = first_v; u < total; u += RO_THREADS) {
+    T* p = rr.dst(a, h_lo + hh) + v * V;
+    const int n = span - v * V;
+    const T* from = tile + u * V;
+    if (n >= V) {
+      if (ro_out_ok(a, h_lo + hh, p, V)) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(from);
+    } else if (ro_out_ok(a, h_lo + hh, p, n)) {
+      for (int e = 0; e < n; ++e) p[e] = from[e];
+    }
+    hh += adv_h;
+    v += adv_v;
+    if (v >= vecs) {
+      v -= vecs;
+      ++hh;
+    }
   }
 }
 
@@ -250,20 +331,21 @@ cudaError_t launch_rope_t(RopePosArgs& a, cudaStream_t st, bool* vec) {
   // too, the interleaved one whole vectors of pairs
   *vec = a.half ? P % V == 0 : 2 * P % V == 0;
   const int pass = a.in_place ? 0 : a.width - 2 * P;
-  a.units = *vec ? (2 * P / V + 1) / 2 + (pass + 2 * V - 1) / (2 * V) : P + pass;
-  const int threads = *vec ? RO_THREADS : RO_PAIR_THREADS;
-  const int at_once = threads / a.units;
+  a.units = *vec ? (2 * P / V + 1) / 2 + (pass + 2 * V - 1) / (2 * V) : (2 * P + pass + V - 1) / V;
   const int heads = a.q_heads + a.k_heads;
-  // of few rows, several CTAs per row: as many as fit on the GPU at once, each
-  // with at least one pass over its threads
+  // heads of one pass over a CTA's threads, or of its shared memory
+  const int at_once = *vec ? RO_THREADS / a.units : RO_STAGE_BYTES / 16 / a.units;
+  const long long passes = (heads + at_once - 1) / at_once;
+  // of few rows, several CTAs per row: as many as fit on the GPU at once; with
+  // vectors each has at least one pass, the staged form at most one
   long long split = ((long long)RO_CTAS * num_sms() + a.rows - 1) / a.rows;
-  const long long most = (heads + at_once - 1) / at_once;
-  if (split > most) split = most;
+  if (*vec ? split > passes : split < passes) split = passes;
+  if (split > heads) split = heads;
   a.heads_per_cta = (int)((heads + split - 1) / split);
   const dim3 grid((unsigned)a.rows, (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta));
   auto kernel = *vec ? (a.half ? rope_kernel<T, true> : rope_kernel<T, false>)
-                     : (a.half ? rope_pairs_kernel<T, true> : rope_pairs_kernel<T, false>);
-  return launch_kernel(kernel, grid, dim3(threads), 0, st, a);
+                     : (a.half ? rope_staged_kernel<T, true> : rope_staged_kernel<T, false>);
+  return launch_kernel(kernel, grid, dim3(RO_THREADS), 0, st, a);
 }
 }  // namespace
 
@@ -271,9 +353,9 @@ cudaError_t launch_rope(RopePosArgs a, cudaStream_t st) {
   bool vec = false;
   cudaError_t e = a.fp32 ? launch_rope_t<float>(a, st, &vec) : launch_rope_t<__nv_bfloat16>(a, st, &vec);
   if (e != cudaSuccess) return e;
-  set_kernel_info("rope_kernel %s %s rows=%d heads=%d pairs=%d vec=%dB heads/cta=%d", a.half ? "half" : "interleaved",
+  set_kernel_info("rope_kernel %s %s rows=%d heads=%d pairs=%d %s heads/cta=%d", a.half ? "half" : "interleaved",
                   a.fp32 ? "fp32" : "bf16", a.rows, a.q_heads + a.k_heads, a.axes * a.freqs,
-                  vec ? 16 : (a.fp32 ? 4 : 2), a.heads_per_cta);
+                  vec ? "vectors" : "staged", a.heads_per_cta);
   return cudaGetLastError();
 }
 
