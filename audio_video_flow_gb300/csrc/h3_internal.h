@@ -323,7 +323,7 @@ constexpr int kRopeMaxWidth = 256;    // channels of a head
 struct RopePosArgs {
   int rows, q_heads, k_heads, width;
   int axes, freqs, half, fp32, in_place;
-  int heads_per_cta, units;   // set by the launcher: heads of one CTA, units of a head
+  int heads_per_cta, rows_per_cta, units;   // set by the launcher: heads and rows of one CTA, units of a head
   float magnitude, sin_scale; // sin_scale: -magnitude for the gradient
   const int32_t* pos;         // [rows][axes]
   const void *q_in, *k_in;

@@ -12,7 +12,8 @@
 // fraction, in half turns.
 //
 // Bound by memory: q and k are read and written once.  A CTA handles one
-// packed row (of few rows: a range of its heads).  A thread owns a pair of
+// packed row (of few rows: a range of its heads; of many rows with few heads:
+// several rows).  A thread owns a pair of
 // 16-byte vectors of a head (the first channels and the second ones of its
 // pairs, or two vectors of whole pairs, or two of passed-through channels) and
 // walks over the heads; it asks for the vectors of RO_BATCH heads before the
@@ -29,6 +30,7 @@ namespace {
 constexpr int RO_THREADS = 128, RO_CTAS = 5;
 constexpr int RO_BATCH = 4;              // heads whose loads a thread issues before their use
 constexpr int RO_STAGE_BYTES = 16384;    // the staged form's heads of one CTA
+constexpr int RO_ANGLES = 512;           // rows x pairs of a CTA that handles several rows
 
 // 16 bytes of channels, as they lie in memory and as fp32.
 template <typename T>
@@ -68,35 +70,43 @@ __device__ __forceinline__ void ro_put2(__nv_bfloat16* p, float2 v) {
 }
 __device__ __forceinline__ void ro_put2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
-// sines and cosines of the row, times the magnitude
-__device__ __forceinline__ void ro_angles(const RopePosArgs& a, int64_t row, float* cs, float* sn) {
+// sines and cosines of `rows` rows, times the magnitude: [row][pair]
+__device__ __forceinline__ void ro_angles(const RopePosArgs& a, int64_t row, int rows, float* cs, float* sn) {
   const int P = a.axes * a.freqs;
-  for (int p = threadIdx.x; p < P; p += blockDim.x) {
-    const int32_t* pp = a.pos + row * a.axes + p / a.freqs;
+  for (int i = threadIdx.x; i < rows * P; i += blockDim.x) {
+    const int r = i / P, p = i - r * P;
+    const int32_t* pp = a.pos + (row + r) * a.axes + p / a.freqs;
     const int32_t pos = in_bounds<int32_t>(a.pos, a.pos_elems, pp, 1, a.err, 60) ? *pp : 0;
     const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[p];
     float s, c;
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns in [-1, 1)
-    cs[p] = c * a.magnitude;
-    sn[p] = s * a.sin_scale;
+    cs[i] = c * a.magnitude;
+    sn[i] = s * a.sin_scale;
   }
 }
 
-template <typename T>
-struct RoRow {   // the row's q and k heads, numbered through
+// The heads of a CTA's rows, numbered through: `n` of each row, the q heads and
+// then the k heads from number `first` on.  MULTI: several rows.
+template <typename T, bool MULTI>
+struct RoHeads {
   const T *q_in, *k_in;
   T *q_out, *k_out;
-  __device__ __forceinline__ RoRow(const RopePosArgs& a, int64_t row) {
+  int first, n;
+  __device__ __forceinline__ RoHeads(const RopePosArgs& a, int64_t row, int first_, int n_) : first(first_), n(n_) {
     q_in = static_cast<const T*>(a.q_in) + row * a.in_row;
     k_in = static_cast<const T*>(a.k_in) + row * a.in_row - a.q_heads * a.in_head;
     q_out = static_cast<T*>(a.q_out) + row * a.out_row;
     k_out = static_cast<T*>(a.k_out) + row * a.out_row - a.q_heads * a.out_head;
   }
-  __device__ __forceinline__ const T* src(const RopePosArgs& a, int h) const {
-    return (h < a.q_heads ? q_in : k_in) + h * a.in_head;
+  __device__ __forceinline__ int row_of(int i) const { return MULTI ? i / n : 0; }
+  __device__ __forceinline__ int head_of(int i) const { return first + (MULTI ? i - i / n * n : i); }
+  __device__ __forceinline__ const T* src(const RopePosArgs& a, int i) const {
+    const int h = head_of(i);
+    return (h < a.q_heads ? q_in : k_in) + h * a.in_head + row_of(i) * a.in_row;
   }
-  __device__ __forceinline__ T* dst(const RopePosArgs& a, int h) const {
-    return (h < a.q_heads ? q_out : k_out) + h * a.out_head;
+  __device__ __forceinline__ T* dst(const RopePosArgs& a, int i) const {
+    const int h = head_of(i);
+    return (h < a.q_heads ? q_out : k_out) + h * a.out_head + row_of(i) * a.out_row;
   }
 };
 template <typename T>
@@ -112,22 +122,23 @@ __device__ __forceinline__ bool ro_out_ok(const RopePosArgs& a, int h, const T* 
 }  // namespace
 
 // Heads whose rotated channels are whole 16-byte vectors.
-template <typename T, bool HALF>
+template <typename T, bool HALF, bool MULTI>
 __global__ void __launch_bounds__(RO_THREADS, RO_CTAS) rope_kernel(const RopePosArgs a) {
-  __shared__ float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+  __shared__ float cs[MULTI ? RO_ANGLES : kRopeMaxPairs], sn[MULTI ? RO_ANGLES : kRopeMaxPairs];
   griddep_launch_dependents();
   griddep_wait();
   constexpr int V = 16 / (int)sizeof(T);
-  const int64_t row = blockIdx.x;
-  const RoRow<T> rr(a, row);
+  const int64_t row = (int64_t)blockIdx.x * (MULTI ? a.rows_per_cta : 1);
+  const int rows = MULTI ? (int)min((int64_t)a.rows_per_cta, a.rows - row) : 1;
+  const int n_heads = min(a.heads_per_cta, a.q_heads + a.k_heads - (int)blockIdx.y * a.heads_per_cta);
+  const RoHeads<T, MULTI> hd(a, row, (int)blockIdx.y * a.heads_per_cta, n_heads);
   const int P = a.axes * a.freqs;
   const int rot_vecs = 2 * P / V;
   const int n_rot = (rot_vecs + 1) / 2;                       // units of rotated channels
   const int upl = a.units;                                    // all units of a head
   const int at_once = RO_THREADS / upl;                       // heads the CTA handles at once
   const int u = threadIdx.x % upl, hg = threadIdx.x / upl;
-  const int h_lo = (int)blockIdx.y * a.heads_per_cta;
-  const int h_hi = hg < at_once ? min(h_lo + a.heads_per_cta, a.q_heads + a.k_heads) : 0;
+  const int h_hi = hg < at_once ? rows * n_heads : 0;
   // the unit's two vectors: channel offsets and channels (0: no vector)
   int at0, at1, n0 = V, n1 = V;
   if (u < n_rot) {
@@ -142,39 +153,41 @@ __global__ void __launch_bounds__(RO_THREADS, RO_CTAS) rope_kernel(const RopePos
   }
   bool angles = false;
   float c[V], s[V];
-  int h0 = h_lo + hg;
+  // half: vector 0 holds the first channels of V pairs, vector 1 the second
+  // ones; interleaved: each vector holds V / 2 pairs
+  auto turn_of = [&](int r) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const bool have = e < V / 2 || HALF || n1 == V;
+      c[e] = have ? cs[r * P + u * V + e] : 0.0f;
+      s[e] = have ? sn[r * P + u * V + e] : 0.0f;
+    }
+  };
+  int h0 = hg;
   do {
     uint4 x[RO_BATCH], y[RO_BATCH];
 #pragma unroll
     for (int b = 0; b < RO_BATCH; ++b) {
       const int h = h0 + b * at_once;
       if (h < h_hi) {
-        const T* p = rr.src(a, h);
-        if (n0 == V && ro_in_ok(a, h, p + at0, V)) x[b] = *reinterpret_cast<const uint4*>(p + at0);
-        if (n1 == V && ro_in_ok(a, h, p + at1, V)) y[b] = *reinterpret_cast<const uint4*>(p + at1);
+        const T* p = hd.src(a, h);
+        if (n0 == V && ro_in_ok(a, hd.head_of(h), p + at0, V)) x[b] = *reinterpret_cast<const uint4*>(p + at0);
+        if (n1 == V && ro_in_ok(a, hd.head_of(h), p + at1, V)) y[b] = *reinterpret_cast<const uint4*>(p + at1);
       }
     }
     if (!angles) {   // (every thread comes here once, in its first pass)
-      ro_angles(a, row, cs, sn);
+      ro_angles(a, row, rows, cs, sn);
       __syncthreads();
       angles = true;
-      if (u < n_rot) {
-        // half: vector 0 holds the first channels of V pairs, vector 1 the
-        // second ones; interleaved: each vector holds V / 2 pairs
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const bool have = e < V / 2 || HALF || n1 == V;
-          c[e] = have ? cs[u * V + e] : 0.0f;
-          s[e] = have ? sn[u * V + e] : 0.0f;
-        }
-      }
+      if (!MULTI && u < n_rot) turn_of(0);
     }
 #pragma unroll
     for (int b = 0; b < RO_BATCH; ++b) {
       const int h = h0 + b * at_once;
       if (h >= h_hi) break;
-      T* p = rr.dst(a, h);
+      T* p = hd.dst(a, h);
       if (u < n_rot) {
+        if (MULTI) turn_of(hd.row_of(h));
         float v[V], w[V];
         ro_unpack<T>(x[b], v);
         ro_unpack<T>(y[b], w);
@@ -198,14 +211,15 @@ __global__ void __launch_bounds__(RO_THREADS, RO_CTAS) rope_kernel(const RopePos
         x[b] = ro_pack<T>(v);
         y[b] = ro_pack<T>(w);
       }
-      if (n0 == V && ro_out_ok(a, h, p + at0, V)) *reinterpret_cast<uint4*>(p + at0) = x[b];
-      if (n1 == V && ro_out_ok(a, h, p + at1, V)) *reinterpret_cast<uint4*>(p + at1) = y[b];
+      const int hn = hd.head_of(h);
+      if (n0 == V && ro_out_ok(a, hn, p + at0, V)) *reinterpret_cast<uint4*>(p + at0) = x[b];
+      if (n1 == V && ro_out_ok(a, hn, p + at1, V)) *reinterpret_cast<uint4*>(p + at1) = y[b];
       // the last passed-through channels of a width that is no whole vector
       const int tail = n0 < V ? n0 : (n1 < V ? n1 : 0);
       if (tail > 0 && u >= n_rot) {
         const int at = n0 < V ? at0 : at1;
-        const T* q = rr.src(a, h) + at;
-        if (ro_in_ok(a, h, q, tail) && ro_out_ok(a, h, p + at, tail))
+        const T* q = hd.src(a, h) + at;
+        if (ro_in_ok(a, hn, q, tail) && ro_out_ok(a, hn, p + at, tail))
           for (int e = 0; e < tail; ++e) p[at + e] = q[e];
       }
     }
@@ -218,18 +232,19 @@ __global__ void __launch_bounds__(RO_THREADS, RO_CTAS) rope_kernel(const RopePos
 // of a group of heads into shared memory, turns the pairs there, and writes
 // whole vectors back (in place, of a vector that is rotated only in part, the
 // rotated channels alone).
-template <typename T, bool HALF>
+template <typename T, bool HALF, bool MULTI>
 __global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosArgs a) {
-  __shared__ __align__(8) float cs[kRopeMaxPairs], sn[kRopeMaxPairs];
+  __shared__ float cs[MULTI ? RO_ANGLES : kRopeMaxPairs], sn[MULTI ? RO_ANGLES : kRopeMaxPairs];
   __shared__ __align__(16) T tile[RO_STAGE_BYTES / sizeof(T)];
   griddep_launch_dependents();
   griddep_wait();
   constexpr int V = 16 / (int)sizeof(T);
-  const int64_t row = blockIdx.x;
-  const RoRow<T> rr(a, row);
+  const int64_t row = (int64_t)blockIdx.x * (MULTI ? a.rows_per_cta : 1);
+  const int rows = MULTI ? (int)min((int64_t)a.rows_per_cta, a.rows - row) : 1;
+  const int n_heads = min(a.heads_per_cta, a.q_heads + a.k_heads - (int)blockIdx.y * a.heads_per_cta);
+  const RoHeads<T, MULTI> hd(a, row, (int)blockIdx.y * a.heads_per_cta, n_heads);
   const int P = a.axes * a.freqs;
-  const int h_lo = (int)blockIdx.y * a.heads_per_cta;
-  const int heads = min(a.heads_per_cta, a.q_heads + a.k_heads - h_lo);
+  const int heads = rows * n_heads;
   const int span = a.in_place ? 2 * P : a.width;               // channels that are written
   const int vecs = (span + V - 1) / V;                         // = a.units
   // a thread's vectors: (head, place) advanced by RO_THREADS without divisions
@@ -237,9 +252,9 @@ __global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosAr
   const int first_h = threadIdx.x / vecs, first_v = threadIdx.x - first_h * vecs;
   const int total = heads * vecs;
   for (int u = threadIdx.x, h = first_h, v = first_v; u < total; u += RO_THREADS) {
-    const T* p = rr.src(a, h_lo + h) + v * V;
+    const T* p = hd.src(a, h) + v * V;
     const int n = min(V, a.width - v * V);   // (the bytes past a partial vector's become 0)
-    if (ro_in_ok(a, h_lo + h, p, n))
+    if (ro_in_ok(a, hd.head_of(h), p, n))
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + u * V)), "l"(p),
                    "r"(n * (int)sizeof(T))
                    : "memory");
@@ -250,7 +265,7 @@ __global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosAr
       ++h;
     }
   }
-  ro_angles(a, row, cs, sn);
+  ro_angles(a, row, rows, cs, sn);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   // two pairs at a time (of an odd number, the last alone)
@@ -261,7 +276,8 @@ __global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosAr
     const int pair = 2 * two;
     const bool both = pair + 1 < P;
     T* x = tile + h * stride + (HALF ? pair : 2 * pair);
-    const float2 c = *reinterpret_cast<const float2*>(cs + pair), sv = *reinterpret_cast<const float2*>(sn + pair);
+    const int at = hd.row_of(h) * P + pair;
+    const float2 c = make_float2(cs[at], both ? cs[at + 1] : 0.0f), sv = make_float2(sn[at], both ? sn[at + 1] : 0.0f);
     if (HALF) {
       T* y = x + P;
       const bool even = (P & 1) == 0;
@@ -305,12 +321,12 @@ __global__ void __launch_bounds__(RO_THREADS) rope_staged_kernel(const RopePosAr
   }
   __syncthreads();
   for (int u = threadIdx.x, hh = first_h, v = first_v; u < total; u += RO_THREADS) {
-    T* p = rr.dst(a, h_lo + hh) + v * V;
+    T* p = hd.dst(a, hh) + v * V;
     const int n = span - v * V;
     const T* from = tile + u * V;
     if (n >= V) {
-      if (ro_out_ok(a, h_lo + hh, p, V)) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(from);
-    } else if (ro_out_ok(a, h_lo + hh, p, n)) {
+      if (ro_out_ok(a, hd.head_of(hh), p, V)) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(from);
+    } else if (ro_out_ok(a, hd.head_of(hh), p, n)) {
       for (int e = 0; e < n; ++e) p[e] = from[e];
     }
     hh += adv_h;
@@ -338,13 +354,31 @@ cudaError_t launch_rope_t(RopePosArgs& a, cudaStream_t st, bool* vec) {
   const long long passes = (heads + at_once - 1) / at_once;
   // of few rows, several CTAs per row: as many as fit on the GPU at once; with
   // vectors each has at least one pass, the staged form at most one
-  long long split = ((long long)RO_CTAS * num_sms() + a.rows - 1) / a.rows;
+  const long long room = (long long)RO_CTAS * num_sms();
+  long long split = (room + a.rows - 1) / a.rows;
   if (*vec ? split > passes : split < passes) split = passes;
   if (split > heads) split = heads;
   a.heads_per_cta = (int)((heads + split - 1) / split);
-  const dim3 grid((unsigned)a.rows, (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta));
-  auto kernel = *vec ? (a.half ? rope_kernel<T, true> : rope_kernel<T, false>)
-                     : (a.half ? rope_staged_kernel<T, true> : rope_staged_kernel<T, false>);
+  // of many rows whose units do not fill a CTA's threads, several rows per CTA:
+  // as many as fill its threads' loads or its shared memory, while every SM keeps
+  // its CTAs (15,000 rows of 2 + 1 heads of 128: 11 us)
+  a.rows_per_cta = 1;
+  if (split == 1 && heads * a.units <= RO_THREADS) {
+    long long more = (*vec ? RO_BATCH : 1) * (long long)at_once / heads;
+    if (more > RO_ANGLES / P) more = RO_ANGLES / P;
+    if (more > a.rows / room) more = a.rows / room;
+    if (more > 1) a.rows_per_cta = (int)more;
+  }
+  const bool multi = a.rows_per_cta > 1;
+  const dim3 grid((unsigned)((a.rows + (long long)a.rows_per_cta - 1) / a.rows_per_cta),
+                  (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta));
+  void (*kernel)(RopePosArgs);
+  if (*vec)
+    kernel = a.half ? (multi ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
+                    : (multi ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+  else
+    kernel = a.half ? (multi ? rope_staged_kernel<T, true, true> : rope_staged_kernel<T, true, false>)
+                    : (multi ? rope_staged_kernel<T, false, true> : rope_staged_kernel<T, false, false>);
   return launch_kernel(kernel, grid, dim3(RO_THREADS), 0, st, a);
 }
 }  // namespace
@@ -353,9 +387,9 @@ cudaError_t launch_rope(RopePosArgs a, cudaStream_t st) {
   bool vec = false;
   cudaError_t e = a.fp32 ? launch_rope_t<float>(a, st, &vec) : launch_rope_t<__nv_bfloat16>(a, st, &vec);
   if (e != cudaSuccess) return e;
-  set_kernel_info("rope_kernel %s %s rows=%d heads=%d pairs=%d %s heads/cta=%d", a.half ? "half" : "interleaved",
+  set_kernel_info("rope_kernel %s %s rows=%d heads=%d pairs=%d %s heads/cta=%d rows/cta=%d", a.half ? "half" : "interleaved",
                   a.fp32 ? "fp32" : "bf16", a.rows, a.q_heads + a.k_heads, a.axes * a.freqs,
-                  vec ? "vectors" : "staged", a.heads_per_cta);
+                  vec ? "vectors" : "staged", a.heads_per_cta, a.rows_per_cta);
   return cudaGetLastError();
 }
 

@@ -255,6 +255,76 @@ def test_rope_row_and_head_counts(S, HQ, HK):
     within(out[:, :HQ + HK], ref, bound, "counts")
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("width, axes, freqs", [(128, 3, 16), (64, 1, 32), (26, 1, 13), (100, 1, 16)])
+@pytest.mark.parametrize("S, HQ, HK", [(5003, 1, 0), (3331, 2, 1), (9001, 1, 1)])
+def test_rope_many_rows_of_few_heads(S, HQ, HK, width, axes, freqs, layout):
+    """Several rows to a CTA, the last CTA's not all there."""
+    x = rope_rows(S, HQ + HK, width, torch.bfloat16, 4)
+    pos = torch.randint(0, 4000, (S, axes), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    cfg = h3.make_rope_config(width, axes, freqs,
+                              layout=h3.H3_ROPE_HALF if layout == "half" else h3.H3_ROPE_INTERLEAVED)
+    out = torch.full((S + 7, *x.shape[1:]), 5.0, dtype=x.dtype, device="cuda")
+    h3.h3_rope(cfg, S, pos.cuda(), 0, x, out, HQ, x[:, HQ:] if HK else None, out[:, HQ:] if HK else None, HK,
+               x.stride(0), x.stride(1), out.stride(0), out.stride(1))
+    ok()
+    ref, bound = O.rope(f64(x[..., :width]), pos.numpy(), O.rope_frequencies(axes, freqs), layout)
+    within(out[:S, :, :width], ref, bound, "many rows")
+    assert (out[S:] == 5.0).all()
+
+
+def test_operators_on_head_major_tensors():
+    """[heads][rows][128] tensors: the row stride is the smaller one."""
+    S, H = 150, 3
+    q, k, v, o, d_o, lse = attention_case(S, H, 41)
+    major = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    want, _ = attention_backward((q, k, v, o, d_o, lse))
+    grads = [torch.full((H, S, 128), 7.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1) for _ in range(3)]
+    ws = torch.empty(h3.h3_attention_backward_workspace_bytes(S, H), dtype=torch.uint8, device="cuda")
+    h3.h3_attention_backward(S, H, *major, 128, S * 128, o, d_o, lse, *grads, 128, S * 128, ws)
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+    pos = torch.randint(0, 99, (S, 1), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    rope, norm = h3.make_rope_config(128, 1, 64), h3.make_norm_config(h3.H3_NORM_LAYER, 128)
+    for x in (q.contiguous(), major[0]):
+        st = (x.stride(0), x.stride(1))
+        y, z, dx = (torch.empty_like(x) for _ in range(3))
+        assert y.stride() == x.stride()
+        dg, db = (torch.empty(128, device="cuda") for _ in range(2))
+        ws = torch.empty(h3.h3_norm_backward_workspace_bytes(norm, S, H), dtype=torch.uint8, device="cuda")
+        h3.h3_rope(rope, S, pos, 0, x, y, H, None, None, 0, *st, *st)
+        h3.h3_norm_forward(norm, S, H, x, *st, None, None, z, *st)
+        h3.h3_norm_backward(norm, S, H, x, *st, None, y, *st, dx, *st, dg, db, ws)
+        got = [t.contiguous() for t in (y, z, dx, dg, db)]
+        if x is major[0]:
+            assert all(torch.equal(a, b) for a, b in zip(got, first))
+        first = got
+    ok()
+
+
+def test_rows_past_the_last_are_left():
+    """Outputs larger than the call's rows keep what lies behind them."""
+    S, H = 70, 2
+    case = attention_case(S, H, 6)
+    buf = torch.full((S + 80, H, 3, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((h3.h3_attention_backward_workspace_bytes(S, H) + 64,), 9, dtype=torch.uint8, device="cuda")
+    q, k, v, o, d_o, lse = case
+    h3.h3_attention_backward(S, H, q, k, v, q.stride(0), q.stride(1), o, d_o, lse, buf[:, :, 0], buf[:, :, 1],
+                             buf[:, :, 2], buf.stride(0), buf.stride(1), ws[:-64])
+    x, dy = norm_rows(S, 1, 300, torch.bfloat16, 1), norm_rows(S, 1, 300, torch.bfloat16, 2)
+    y, dx = (torch.full((S + 40, 1, 304), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dg, db = (torch.full((308,), 3.0, device="cuda") for _ in range(2))
+    cfg = h3.make_norm_config(h3.H3_NORM_LAYER, 300)
+    nws = h3.h3_norm_backward_workspace_bytes(cfg, S, 1)
+    ws2 = torch.full((nws + 64,), 9, dtype=torch.uint8, device="cuda")
+    h3.h3_norm_forward(cfg, S, 1, x, 304, 304, None, None, y, 304, 304)
+    h3.h3_norm_backward(cfg, S, 1, x, 304, 304, None, dy, 304, 304, dx, 304, 304, dg, db, ws2[:nws])
+    ok()
+    assert (buf[S:] == 7.0).all() and (ws[-64:] == 9).all() and (ws2[nws:] == 9).all()
+    assert (y[S:] == 5.0).all() and (dx[S:] == 5.0).all() and (y[:, :, 300:] == 5.0).all()
+    assert (dg[300:] == 3.0).all() and (db[300:] == 3.0).all()
+
+
 @pytest.mark.parametrize("scaling", ["linear", "ntk", "yarn"])
 @pytest.mark.parametrize("scaled_axes", [1, 2, 3])
 def test_rope_scalings(scaling, scaled_axes):
