@@ -22,7 +22,8 @@
 //                three and two stages;
 //   warp 1       MMA issuer; G1 and G2 are read K-major for S and dP and
 //                MN-major for A1 and A2 from the same tile;
-//   warp 2       on the key side, the query rows' log-sum-exp and D;
+//   warp 2       on the key side, the query rows' log-sum-exp and D (where few
+//                CTAs run, the softmax warps compute them instead);
 //   warps 4-19   softmax: warpgroup w takes columns [32 w, 32 w + 32), one row
 //                per thread: P from S, then dS from dP and the P still in
 //                registers, both to TMEM as bf16, where they are left operands.
@@ -164,6 +165,20 @@ __device__ __forceinline__ void ab_bulk_load(void* dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+
+// Sum over 128 channels of a product: 16 lanes with 8 channels each.
+__device__ __forceinline__ float ab_row_dot(const uint4& x, const uint4& y) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    s = __fmaf_rn(bf16_lo(xw[e]), bf16_lo(yw[e]), s);
+    s = __fmaf_rn(bf16_hi(xw[e]), bf16_hi(yw[e]), s);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -193,15 +208,7 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
   float* out = a.rowvals + ((size_t)head * a.tiles + tile) * 256;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s = __fmaf_rn(bf16_lo(ow[e]), bf16_lo(dw[e]), s);
-      s = __fmaf_rn(bf16_hi(ow[e]), bf16_hi(dw[e]), s);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float s = ab_row_dot(ov[i], dv[i]);
     if (sub == 0) {
       const int r = i * 16 + r0, row = tile * 128 + r;
       float l2 = INFINITY;
@@ -257,9 +264,43 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
   }
 }
 
+// The row values of tile t into slot `slot` of shared memory, by the softmax
+// warps themselves (the same sums as attention_bwd_rows_kernel's).
+__device__ __forceinline__ void ab_own_rows(const AttnBwdArgs& a, const AbSmem& sm, int t, int slot, int head) {
+  const int tid = threadIdx.x - 128, sub = tid & 15, r0 = tid >> 4;
+  constexpr int kStep = AB_WARPS * 2;            // rows at once
+  float* out = reinterpret_cast<float*>(sm.rowvals + slot * AB_ROWVALS);
+  uint4 ov[128 / kStep], dv[128 / kStep];
+  float l2[128 / kStep];
+#pragma unroll
+  for (int i = 0; i < 128 / kStep; ++i) {
+    const int row = t * 128 + i * kStep + r0;
+    ov[i] = dv[i] = make_uint4(0u, 0u, 0u, 0u);
+    l2[i] = INFINITY;
+    if (row < a.S) {
+      const size_t off = ((size_t)row * a.H + head) * 128 + sub * 8;
+      if (in_bounds<__nv_bfloat16>(a.o, a.o_elems, a.o + off, 8, a.err, 40))
+        ov[i] = *reinterpret_cast<const uint4*>(a.o + off);
+      if (in_bounds<__nv_bfloat16>(a.d_o, a.o_elems, a.d_o + off, 8, a.err, 41))
+        dv[i] = *reinterpret_cast<const uint4*>(a.d_o + off);
+      if (sub == 0 && in_bounds<float>(a.lse, a.lse_elems, a.lse + (size_t)head * a.S + row, 1, a.err, 42))
+        l2[i] = a.lse[(size_t)head * a.S + row] * 1.44269504088896340736f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 128 / kStep; ++i) {
+    const float s = ab_row_dot(ov[i], dv[i]);
+    if (sub == 0) {
+      out[i * kStep + r0] = l2[i];
+      out[128 + i * kStep + r0] = s;
+    }
+  }
+}
+
 // One CTA's work: KEYS = true computes dK and dV of key tile `tile`, false dQ
-// of query tile `tile`.
-template <bool KEYS>
+// of query tile `tile`.  OWN = true: at most two tiles, and the CTA computes
+// their row values itself.
+template <bool KEYS, bool OWN>
 __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorMap* tmF2, const CUtensorMap* tmG1,
                                         const CUtensorMap* tmG2, const AttnBwdArgs& a, const AbSmem& sm,
                                         uint32_t tmem_base, int tile, int head, const WaitCtl& ctl) {
@@ -301,7 +342,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       }
     }
     __syncwarp();
-  } else if (KEYS && warp == 2) {
+  } else if (KEYS && !OWN && warp == 2) {
     // ------------------------------------------------------------ producer of the query rows' values
     if (lane == 0) {
       int i = 0;
@@ -421,9 +462,16 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     float my_l2 = 0.0f, my_d = 0.0f;
     bool ok = true;
+    if (OWN) {   // every softmax warp comes here, before any wait that can run out
+      for (int t = KEYS ? 0 : tile; t < (KEYS ? n : tile + 1); ++t) ab_own_rows(a, sm, t, KEYS ? t : 0, head);
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * AB_WARPS) : "memory");
+    }
     if (!KEYS) {
       const float* rv = a.rowvals + ((size_t)head * n + tile) * 256 + row;
-      if (in_bounds<float>(a.rowvals, a.rowval_elems, rv, 129, a.err, 45)) {
+      if (OWN) {
+        my_l2 = reinterpret_cast<const float*>(sm.rowvals)[row];
+        my_d = reinterpret_cast<const float*>(sm.rowvals)[128 + row];
+      } else if (in_bounds<float>(a.rowvals, a.rowval_elems, rv, 129, a.err, 45)) {
         my_l2 = rv[0];
         my_d = rv[128];
       }
@@ -451,7 +499,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
     for (int j = 0; j < n && ok; ++j) {
       const uint32_t ph = (uint32_t)j & 1u;
       const float* rv = reinterpret_cast<const float*>(sm.rowvals + (j & 1) * AB_ROWVALS) + wg * 32;
-      if (KEYS && !ab_wait(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl)) { ok = false; break; }
+      if (KEYS && !OWN && !ab_wait(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl)) { ok = false; break; }
       if (!ab_wait(sm.s_full, ph, ctl)) { ok = false; break; }
       tc_fence_after();
       uint32_t p[32], pk[16];
@@ -558,6 +606,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
 
 // blockIdx.x: 128-row tile, blockIdx.y: head; z = 0 the key side, z = 1 the
 // query side (the longer key-side CTAs are scheduled first).
+template <bool OWN>
 __global__ void __launch_bounds__(AB_THREADS, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -595,6 +644,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int skip = 0;
   if (threadIdx.x == 0) {
     mbar_init(sm.f1_full, 1);
     mbar_init(sm.f2_full, 1);
@@ -622,7 +672,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     mbar_init(sm.f_full, AB_WARPS);
     mbar_init(sm.acc_full, 1);
     mbar_init(sm.drain, 1);
-    *abort_flag = timeout_recorded(args.err) ? 1 : 0;   // sticky timeout of an earlier launch
+    skip = timeout_recorded(args.err) ? 1 : 0;   // sticky timeout of an earlier launch
+    *abort_flag = skip;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -633,7 +684,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
-  __syncthreads();
+  if (OWN) skip = __syncthreads_or(skip);   // one answer for all warps: they meet at a barrier in ab_tile
+  else __syncthreads();
   tc_fence_after();
   griddep_wait();
   const uint32_t tmem_base = *tmem_slot;
@@ -641,11 +693,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
   // a wait of an earlier launch ran out: this launch skips its work, before
   // any copy or MMA is issued
-  if (*ctl.flag == 0) {
+  if (OWN ? skip == 0 : *ctl.flag == 0) {
     if (blockIdx.z == 0)
-      ab_tile<true>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
+      ab_tile<true, OWN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
     else
-      ab_tile<false>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
+      ab_tile<false, OWN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -661,15 +713,23 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   static_assert(tmem_footprint_exclusive(AB_SMEM), "an attention CTA must hold its SM's TMEM alone");
   if (!tmem_exclusive(AB_SMEM)) return cudaErrorNotSupported;
   const dim3 rows_grid((unsigned)a.tiles, (unsigned)a.H), grid((unsigned)a.tiles, (unsigned)a.H, 2);
-  cudaError_t e = launch_kernel(attention_bwd_rows_kernel, rows_grid, dim3(256), 0, stream, a);
+  // Up to two tiles and two CTAs per SM, every CTA computes its row values
+  // itself beside its first loads: one launch instead of two (72 rows x 4
+  // heads 9.4 -> 7.9 us, 128 x 152 18.1 -> 13.0, 256 x 56 16.6 -> 15.1).  With
+  // more CTAs that work, which each then repeats before its first step, costs
+  // more than the launch (256 x 600 136 -> 175 us, 100 x 600 59.5 -> 62.8).
+  const bool own = a.tiles <= 2 && (int64_t)a.tiles * a.H <= num_sms();
+  cudaError_t e = cudaSuccess;
+  if (!own) e = launch_kernel(attention_bwd_rows_kernel, rows_grid, dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(attention_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+  const auto kernel = own ? attention_bwd_kernel<true> : attention_bwd_kernel<false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(attention_bwd_kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
+  e = launch_kernel(kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
   if (e != cudaSuccess) return e;
   set_kernel_info("attention_bwd_kernel tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d,%d acc=f32 "
-                  "P,dS-in-TMEM grid=%ux%ux2",
-                  AB_ST1, AB_ST2, grid.x, grid.y);
+                  "P,dS-in-TMEM grid=%ux%ux2%s",
+                  AB_ST1, AB_ST2, grid.x, grid.y, own ? " own-row-values" : "");
   return cudaGetLastError();
 }
 

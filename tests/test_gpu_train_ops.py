@@ -100,6 +100,25 @@ def test_attention_backward_separate_tensors(S, H, gap):
         assert (buf[..., 128:] == 7.0).all()      # what lies between the rows is left as it was
 
 
+@pytest.mark.parametrize("S", [1, 72, 128, 200, 256])
+def test_attention_backward_few_and_many_heads_agree(S):
+    """A head's gradient is the same bits whatever heads lie beside it: few
+    heads of a short document compute their row values inside the main kernel,
+    many take them from the kernel before it."""
+    H = 160
+    case = attention_case(S, H, S + 17)
+    many, _ = attention_backward(case)
+    ok()
+    for h in (0, 3, 77, H - 2):
+        part = tuple(t[:, h:h + 2].contiguous() for t in case[:5]) + (case[5][h:h + 2].contiguous(),)
+        few, _ = attention_backward(part)
+        ok()
+        for name, x, y in zip(("dq", "dk", "dv"), few, many):
+            assert torch.equal(x, y[:, h:h + 2]), f"S={S} head {h} {name}"
+        if h == 77:
+            check_attention(part, few, f"S={S}")
+
+
 def test_attention_backward_long():
     case = attention_case(4099, 1, 5)
     grads, _ = attention_backward(case)
