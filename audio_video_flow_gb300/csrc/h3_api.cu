@@ -1239,6 +1239,12 @@ h3_status check_strides(int64_t width, int32_t heads, int64_t row_stride, int64_
   if (row_stride % unit || (heads > 1 && head_stride % unit)) return H3_ERR_ALIGN;
   return H3_OK;
 }
+// Whether an output view's elements are apart: a row's heads end before the
+// next row, or a head's rows before the next head.
+bool apart(int64_t rows, int64_t heads, int64_t width, int64_t row_stride, int64_t head_stride) {
+  return rows == 1 || heads == 1 || row_stride >= (__int128)(heads - 1) * head_stride + width ||
+         head_stride >= (__int128)(rows - 1) * row_stride + width;
+}
 
 h3_status check_rope(const h3_rope_config* c) {
   if (!c) return H3_ERR_NULL;
@@ -1385,6 +1391,7 @@ h3_status h3_attention_backward(int32_t n_rows, int32_t n_heads, const void* q, 
   if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || !al16(d_o) || !al16(dq) || !al16(dk) || !al16(dv) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return H3_ERR_ALIGN;
+  if (!apart(n_rows, n_heads, 128, d_row_stride_elems, d_head_stride_elems)) return H3_ERR_SHAPE;
   const void* const in[] = {q, k, v, o, d_o, lse, workspace};
   void* const out[] = {dq, dk, dv};
   for (int i = 0; i < 3; ++i) {
@@ -1440,6 +1447,7 @@ h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos,
   if (!al16(q_in) || !al16(q_out) || (n_k_heads > 0 && (!al16(k_in) || !al16(k_out))) ||
       (reinterpret_cast<uintptr_t>(pos) & 3u))
     return H3_ERR_ALIGN;
+  if (!apart(n_rows, heads, cfg->head_dim, out_row_stride_elems, out_head_stride_elems)) return H3_ERR_SHAPE;
   const bool in_place = q_in == q_out;
   if (n_k_heads > 0 && (in_place != (k_in == k_out) || k_out == q_out || k_out == q_in || q_out == k_in))
     return H3_ERR_SHAPE;
@@ -1489,6 +1497,7 @@ h3_status h3_norm_forward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_h
   if ((s = check_strides(cfg->width, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
   if ((s = check_strides(cfg->width, n_heads, y_row_stride_elems, y_head_stride_elems, unit)) != H3_OK) return s;
   if (!al16(x) || !al16(y) || !al16n(gain) || !al16n(bias)) return H3_ERR_ALIGN;
+  if (!apart(n_rows, n_heads, cfg->width, y_row_stride_elems, y_head_stride_elems)) return H3_ERR_SHAPE;
   if (x == y && (x_row_stride_elems != y_row_stride_elems ||
                  (n_heads > 1 && x_head_stride_elems != y_head_stride_elems)))
     return H3_ERR_SHAPE;
@@ -1527,6 +1536,7 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   if (!al16(x) || !al16(dy) || !al16(dx) || !al16n(gain) || (reinterpret_cast<uintptr_t>(dgain) & 3u) ||
       (reinterpret_cast<uintptr_t>(dbias) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return H3_ERR_ALIGN;
+  if (!apart(n_rows, n_heads, cfg->width, dx_row_stride_elems, dx_head_stride_elems)) return H3_ERR_SHAPE;
   auto same = [&](const void* p, int64_t row, int64_t head) {
     return p != dx || (row == dx_row_stride_elems && (n_heads == 1 || head == dx_head_stride_elems));
   };

@@ -349,9 +349,11 @@ h3_status h3_attention(int32_t n_rows, int32_t n_heads, const void *q, const voi
  * once to bf16.  dq, dk, dv: element (row i, head h, channel c) at
  * ptr + i*d_row_stride + h*d_head_stride + c (strides in elements, multiples
  * of 8, as the slots of a packed [S][H][3][128] tensor or three tensors of
- * their own); they must overlap neither each other nor any input
- * (H3_ERR_SHAPE where two of the pointers are equal).  Nothing else is
- * written.  The result is bitwise repeatable: no atomics.
+ * their own; rows that hold their heads or heads that hold their rows, else
+ * H3_ERR_SHAPE, as for the outputs of h3_rope and the norm calls); they must
+ * overlap neither each other nor any input (H3_ERR_SHAPE where two of the
+ * pointers are equal).  Nothing else is written.  The result is bitwise
+ * repeatable: no atomics.
  * workspace: device, 256-byte aligned, at least
  * h3_attention_backward_workspace_bytes (0 for invalid sizes); scratch of one
  * call, so calls that can overlap on the GPU need one each. */

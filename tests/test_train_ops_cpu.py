@@ -141,3 +141,12 @@ def test_binding_raises(lib):
     with pytest.raises(h3.H3Error) as e:
         h3.h3_norm_forward(_norm(width=8193), 1, 1, 0x1000, 8200, 8200, None, None, 0x9000, 8200, 8200, stream=0)
     assert e.value.status == h3.H3_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name, args, strides", [
+    ("h3_attention_backward", ATTENTION, ("drs", "dhs")), ("h3_rope", ROPE, ("ors", "ohs")),
+    ("h3_norm_forward", FORWARD, ("yrs", "yhs")), ("h3_norm_backward", BACKWARD, ("dxrs", "dxhs"))])
+@pytest.mark.parametrize("row, head", [(128, 128), (256, 128), (504, 128), (128, 1016), (512, 136)])
+def test_outputs_whose_rows_and_heads_overlap_are_refused(lib, name, args, strides, row, head):
+    """8 rows of 4 heads of 128 channels."""
+    assert _call(getattr(lib, name), args, **dict(zip(strides, (row, head)))) == h3.H3_ERR_SHAPE
