@@ -321,6 +321,42 @@ def test_operators_on_head_major_tensors():
     ok()
 
 
+def test_operators_on_rows_far_apart():
+    """Rows 2^30 elements apart: offsets past 32 bits, in elements and bytes,
+    against the same call on packed rows."""
+    S, H, far = 5, 2, 1 << 30
+    buf = torch.empty((S - 1) * far + 4096, dtype=torch.bfloat16, device="cuda")
+
+    def spread(i, fill=None):      # the i-th [S][H][128] view into buf
+        t = buf.as_strided((S, H, 128), (far, 128, 1), 256 * i)
+        t.copy_(torch.full_like(t, 7.0) if fill is None else fill)
+        return t
+
+    q, k, v, o, d_o, lse = attention_case(S, H, 11, packed=False)
+    want, _ = attention_backward((q, k, v, o, d_o, lse), packed=False)
+    grads = [spread(3 + i) for i in range(3)]
+    ws = torch.empty(h3.h3_attention_backward_workspace_bytes(S, H), dtype=torch.uint8, device="cuda")
+    h3.h3_attention_backward(S, H, spread(0, q), spread(1, k), spread(2, v), far, 128, o, d_o, lse, *grads, far, 128,
+                             ws)
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+    pos = torch.tensor([[0], [1], [2], [77], [1000]], dtype=torch.int32, device="cuda")
+    rope, norm = h3.make_rope_config(128, 1, 64), h3.make_norm_config(h3.H3_NORM_LAYER, 128)
+    got = []
+    for x, dy, y, z, dx, row in [(q, k, *(torch.empty_like(q) for _ in range(3)), H * 128),
+                                 (spread(0, q), spread(1, k), *(spread(6 + i) for i in range(3)), far)]:
+        dg, db = (torch.empty(128, device="cuda") for _ in range(2))
+        ws = torch.empty(h3.h3_norm_backward_workspace_bytes(norm, S, H), dtype=torch.uint8, device="cuda")
+        h3.h3_rope(rope, S, pos, 0, x, y, H, None, None, 0, row, 128, row, 128)
+        h3.h3_norm_forward(norm, S, H, x, row, 128, None, None, z, row, 128)
+        h3.h3_norm_backward(norm, S, H, x, row, 128, None, dy, row, 128, dx, row, 128, dg, db, ws)
+        ok()
+        got.append((y, z, dx, dg, db))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_rows_past_the_last_are_left():
     """Outputs larger than the call's rows keep what lies behind them."""
     S, H = 70, 2
