@@ -3,6 +3,7 @@
 #include "h3.h"
 #include "h3_device.cuh"
 #include "h3_internal.h"
+#include "rope_turns.h"
 
 #include <chrono>
 #include <cmath>
@@ -1270,79 +1271,6 @@ h3_status check_rope(const h3_rope_config* c) {
   return H3_OK;
 }
 
-// High half of a 128 x 128-bit product: both factors fractions of 2^128.
-typedef unsigned __int128 u128;
-u128 mul_hi(u128 a, u128 b) {
-  const uint64_t al = (uint64_t)a, ah = (uint64_t)(a >> 64), bl = (uint64_t)b, bh = (uint64_t)(b >> 64);
-  const u128 ll = (u128)al * bl, lh = (u128)al * bh, hl = (u128)ah * bl, hh = (u128)ah * bh;
-  const u128 mid = (ll >> 64) + (uint64_t)lh + (uint64_t)hl;
-  return hh + (lh >> 64) + (hl >> 64) + (mid >> 64);
-}
-u128 fraction(double x) {   // 0 <= x < 1, exactly
-  int e;
-  const uint64_t m = (uint64_t)std::ldexp(std::frexp(x, &e), 53);   // x = m 2^(e - 53)
-  const int shift = 128 - 53 + e;
-  return shift >= 0 ? (u128)m << shift : (shift > -64 ? (u128)(m >> -shift) : 0);
-}
-u128 inverse(float b) {     // 1 / b for b >= 1
-  int e;
-  const uint32_t m = (uint32_t)std::ldexp(std::frexp(b, &e), 24);   // b = m 2^(e - 24), 2^23 <= m < 2^24
-  const u128 q = ~(u128)0 / m;                                      // 2^128 / m
-  return e <= 24 ? (e <= 1 && m == (1u << 23) ? ~(u128)0 : q << (24 - e)) : q >> (e - 24);
-}
-// b^(-1/n) for b >= 1: a double's root and one Newton step on its n-th power.
-u128 inverse_root(float b, int n) {
-  const double r0 = std::pow((double)b, -1.0 / n);
-  if (!(r0 < 1.0)) return ~(u128)0;
-  const u128 r = fraction(r0);
-  if (!(b < 1.0995116e12f)) return r;   // 2^40: beyond, the power has too few digits for the step
-  u128 power = ~(u128)0, square = r;
-  for (int k = n; k > 0; k >>= 1) {
-    if (k & 1) power = mul_hi(power, square);
-    square = mul_hi(square, square);
-  }
-  const double off = (double)(__int128)(inverse(b) - power) / ((double)power * n);
-  return r + (u128)(__int128)std::ldexp(r0 * off, 128);
-}
-
-// Turns per position of every rotated pair in 64-bit fixed point (omega <= 1
-// radian, so below 1/6): a geometric series in 128-bit fractions, since a
-// position of 2^31 would multiply the rounding of a double into 2^-24 turns,
-// and a long double pow per frequency costs more than the launch.
-void fill_turns(const h3_rope_config& c, uint64_t* turns) {
-  const u128 kInvTwoPi = ((u128)0x28BE60DB9391054Aull << 64) | 0x7F09D5F47D4D3770ull;
-  const int F = c.n_freqs;
-  const double s = c.factor, inv_s = 1.0 / s, per_turn = 1.0 / ((double)c.beta - c.alpha);
-  bool done[2] = {false, false};
-  int at[2] = {0, 0};
-  for (int a = 0; a < c.n_axes; ++a) {
-    const int scaled = c.scaling != H3_ROPE_SCALE_NONE && ((c.scaled_axes >> a) & 1);
-    if (done[scaled]) {   // the axes of one kind share their frequencies
-      std::memcpy(turns + a * F, turns + at[scaled] * F, (size_t)F * sizeof(uint64_t));
-      continue;
-    }
-    done[scaled] = true;
-    at[scaled] = a;
-    const int scaling = scaled ? c.scaling : H3_ROPE_SCALE_NONE;
-    u128 ratio = F > 1 ? inverse_root(c.theta, F) : 0;
-    if (scaling == H3_ROPE_SCALE_NTK) ratio = mul_hi(ratio, inverse_root(c.factor, F - 1));
-    u128 w = kInvTwoPi;
-    if (scaling == H3_ROPE_SCALE_LINEAR) w = mul_hi(w, inverse(c.factor));
-    for (int f = 0; f < F; ++f) {
-      u128 t = w;
-      if (scaling == H3_ROPE_SCALE_YARN) {
-        // turns over the trained length, and by them the share kept
-        const double n = (double)c.trained_length * std::ldexp((double)(uint64_t)(w >> 64), -64);
-        const double g = n <= c.alpha ? 0.0 : (n >= c.beta ? 1.0 : (n - c.alpha) * per_turn);
-        const double keep = g + (1.0 - g) * inv_s;
-        if (keep < 1.0) t = mul_hi(w, fraction(keep));
-      }
-      turns[a * F + f] = (uint64_t)(t >> 64);
-      w = mul_hi(w, ratio);
-    }
-  }
-}
-
 h3_status check_norm(const h3_norm_config* c, int32_t n_rows, int32_t n_heads) {
   if (!c) return H3_ERR_NULL;
   if (c->kind != H3_NORM_RMS && c->kind != H3_NORM_LAYER) return H3_ERR_UNSUPPORTED;
@@ -1483,7 +1411,7 @@ h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos,
     a.k_out_elems = view_elems(n_rows, n_k_heads, cfg->head_dim, a.out_row, a.out_head);
   }
   a.err = device_error_word();
-  fill_turns(*cfg, a.turns);
+  rope_turns(*cfg, a.turns);
   return cuda_st(launch_rope(a, stream));
 }
 
