@@ -7,9 +7,12 @@
 //
 // Angles: omega is held as turns per position in 64-bit fixed point (2^64 = one
 // turn), so that the low 64 bits of pos * omega are the angle's fraction of a
-// turn, exact to 2^-33 turns for every 32-bit position (an fp32 product is
-// wrong by 0.06 radians at position 10^6).  The sine and cosine are of that
-// fraction, in half turns.
+// turn, within 2^-32 turns for every 32-bit position (an fp32 product is
+// wrong by 0.06 radians at position 10^6).  The sine and cosine are of what
+// that fraction is off the nearest quarter turn, in units of 2^-34 turns; of
+// its 32 bits fp32 holds 24, and the rest is brought in as a first-order
+// change (the whole fraction rounded to fp32 would be off by 2^-26 turns, and
+// a sine near the half turn by many of its own units).
 //
 // Bound by memory: q and k are read and written once.  A CTA handles one
 // packed row (of few rows: a range of its heads; of many rows with few heads:
@@ -78,8 +81,16 @@ __device__ __forceinline__ void ro_angles(const RopePosArgs& a, int64_t row, int
     const int32_t* pp = a.pos + (row + r) * a.axes + p / a.freqs;
     const int32_t pos = in_bounds<int32_t>(a.pos, a.pos_elems, pp, 1, a.err, 60) ? *pp : 0;
     const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[p];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns in [-1, 1)
+    const uint32_t quarter = ((uint32_t)(turn >> 32) + 0x20000000u) >> 30;   // the nearest one, 0..3
+    const int32_t off = (int32_t)(uint32_t)(turn >> 30);                     // from it, 2^-34 turns each
+    const float f = (float)off;
+    const float low = (float)(off - __float2int_rn(f)) * 3.6572953e-10f;     // 2 pi 2^-34: radians
+    float s0, c0;
+    sincospif(f * 1.16415321826934814453e-10f, &s0, &c0);                    // 2^-33: half turns in [-1/4, 1/4]
+    const float s1 = __fmaf_rn(c0, low, s0), c1 = __fmaf_rn(-s0, low, c0);
+    const bool odd = quarter & 1u, back = quarter & 2u;
+    const float s = back ? -(odd ? c1 : s1) : (odd ? c1 : s1);
+    const float c = back != odd ? -(odd ? s1 : c1) : (odd ? s1 : c1);
     cs[i] = c * a.magnitude;
     sn[i] = s * a.sin_scale;
   }
