@@ -1234,11 +1234,17 @@ inline size_t view_elems(int64_t rows, int64_t heads, int64_t width, int64_t row
 }
 size_t attn_bwd_ws_bytes(int64_t S, int64_t H) { return al256((size_t)((S + 127) / 128) * (size_t)H * 256 * 4); }
 
-// Strides of a [rows][heads][width] view (one head: its stride is not used).
-h3_status check_strides(int64_t width, int32_t heads, int64_t row_stride, int64_t head_stride, int64_t unit) {
-  if (row_stride < width || (heads > 1 && head_stride < width)) return H3_ERR_SHAPE;
-  if (row_stride % unit || (heads > 1 && head_stride % unit)) return H3_ERR_ALIGN;
+// Strides of a [rows][heads][width] view (that of one row or one head is not
+// used).
+h3_status check_strides(int64_t width, int32_t rows, int32_t heads, int64_t row_stride, int64_t head_stride,
+                        int64_t unit) {
+  if ((rows > 1 && row_stride < width) || (heads > 1 && head_stride < width)) return H3_ERR_SHAPE;
+  if ((rows > 1 && row_stride % unit) || (heads > 1 && head_stride % unit)) return H3_ERR_ALIGN;
   return H3_OK;
+}
+// Whether two views of one pointer are the same view.
+bool same_strides(int32_t rows, int32_t heads, int64_t row_a, int64_t head_a, int64_t row_b, int64_t head_b) {
+  return (rows == 1 || row_a == row_b) && (heads == 1 || head_a == head_b);
 }
 // Whether an output view's elements are apart: a row's heads end before the
 // next row, or a head's rows before the next head.
@@ -1370,8 +1376,8 @@ h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos,
   if (!pos || !q_in || !q_out || (n_k_heads > 0 && (!k_in || !k_out))) return H3_ERR_NULL;
   const int heads = n_q_heads > n_k_heads ? n_q_heads : n_k_heads;
   const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
-  if ((s = check_strides(cfg->head_dim, heads, in_row_stride_elems, in_head_stride_elems, unit)) != H3_OK) return s;
-  if ((s = check_strides(cfg->head_dim, heads, out_row_stride_elems, out_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->head_dim, n_rows, heads, in_row_stride_elems, in_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->head_dim, n_rows, heads, out_row_stride_elems, out_head_stride_elems, unit)) != H3_OK) return s;
   if (!al16(q_in) || !al16(q_out) || (n_k_heads > 0 && (!al16(k_in) || !al16(k_out))) ||
       (reinterpret_cast<uintptr_t>(pos) & 3u))
     return H3_ERR_ALIGN;
@@ -1379,8 +1385,8 @@ h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos,
   const bool in_place = q_in == q_out;
   if (n_k_heads > 0 && (in_place != (k_in == k_out) || k_out == q_out || k_out == q_in || q_out == k_in))
     return H3_ERR_SHAPE;
-  if (in_place && (in_row_stride_elems != out_row_stride_elems ||
-                   (heads > 1 && in_head_stride_elems != out_head_stride_elems)))
+  if (in_place && !same_strides(n_rows, heads, in_row_stride_elems, in_head_stride_elems, out_row_stride_elems,
+                                out_head_stride_elems))
     return H3_ERR_SHAPE;
   RopePosArgs a{};
   a.rows = n_rows;
@@ -1399,9 +1405,9 @@ h3_status h3_rope(const h3_rope_config* cfg, int32_t n_rows, const int32_t* pos,
   a.k_in = k_in;
   a.q_out = q_out;
   a.k_out = k_out;
-  a.in_row = in_row_stride_elems;
+  a.in_row = n_rows > 1 ? in_row_stride_elems : 0;
   a.in_head = heads > 1 ? in_head_stride_elems : 0;
-  a.out_row = out_row_stride_elems;
+  a.out_row = n_rows > 1 ? out_row_stride_elems : 0;
   a.out_head = heads > 1 ? out_head_stride_elems : 0;
   a.pos_elems = (size_t)n_rows * cfg->n_axes;
   a.q_in_elems = view_elems(n_rows, n_q_heads, cfg->head_dim, a.in_row, a.in_head);
@@ -1422,19 +1428,19 @@ h3_status h3_norm_forward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_h
   if (s != H3_OK) return s;
   if (!x || !y) return H3_ERR_NULL;
   const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
-  if ((s = check_strides(cfg->width, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
-  if ((s = check_strides(cfg->width, n_heads, y_row_stride_elems, y_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_rows, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_rows, n_heads, y_row_stride_elems, y_head_stride_elems, unit)) != H3_OK) return s;
   if (!al16(x) || !al16(y) || !al16n(gain) || !al16n(bias)) return H3_ERR_ALIGN;
   if (!apart(n_rows, n_heads, cfg->width, y_row_stride_elems, y_head_stride_elems)) return H3_ERR_SHAPE;
-  if (x == y && (x_row_stride_elems != y_row_stride_elems ||
-                 (n_heads > 1 && x_head_stride_elems != y_head_stride_elems)))
+  if (x == y && !same_strides(n_rows, n_heads, x_row_stride_elems, x_head_stride_elems, y_row_stride_elems,
+                              y_head_stride_elems))
     return H3_ERR_SHAPE;
   NormArgs a = norm_args(*cfg, n_rows, n_heads);
   a.x = x;
-  a.x_row = x_row_stride_elems;
+  a.x_row = n_rows > 1 ? x_row_stride_elems : 0;
   a.x_head = n_heads > 1 ? x_head_stride_elems : 0;
   a.y = y;
-  a.y_row = y_row_stride_elems;
+  a.y_row = n_rows > 1 ? y_row_stride_elems : 0;
   a.y_head = n_heads > 1 ? y_head_stride_elems : 0;
   a.gain = gain;
   a.bias = bias;
@@ -1458,15 +1464,15 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   const bool params = dgain || dbias;
   if (!x || !dy || !dx || (params && !workspace)) return H3_ERR_NULL;
   const int64_t unit = cfg->dtype == H3_FP32 ? 4 : 8;
-  if ((s = check_strides(cfg->width, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
-  if ((s = check_strides(cfg->width, n_heads, dy_row_stride_elems, dy_head_stride_elems, unit)) != H3_OK) return s;
-  if ((s = check_strides(cfg->width, n_heads, dx_row_stride_elems, dx_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_rows, n_heads, x_row_stride_elems, x_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_rows, n_heads, dy_row_stride_elems, dy_head_stride_elems, unit)) != H3_OK) return s;
+  if ((s = check_strides(cfg->width, n_rows, n_heads, dx_row_stride_elems, dx_head_stride_elems, unit)) != H3_OK) return s;
   if (!al16(x) || !al16(dy) || !al16(dx) || !al16n(gain) || (reinterpret_cast<uintptr_t>(dgain) & 3u) ||
       (reinterpret_cast<uintptr_t>(dbias) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return H3_ERR_ALIGN;
   if (!apart(n_rows, n_heads, cfg->width, dx_row_stride_elems, dx_head_stride_elems)) return H3_ERR_SHAPE;
   auto same = [&](const void* p, int64_t row, int64_t head) {
-    return p != dx || (row == dx_row_stride_elems && (n_heads == 1 || head == dx_head_stride_elems));
+    return p != dx || same_strides(n_rows, n_heads, row, head, dx_row_stride_elems, dx_head_stride_elems);
   };
   if (!same(x, x_row_stride_elems, x_head_stride_elems) || !same(dy, dy_row_stride_elems, dy_head_stride_elems) ||
       (dgain && dgain == dbias))
@@ -1474,13 +1480,13 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   if (params && ws_bytes < norm_bwd_ws_bytes(*cfg, n_rows, n_heads)) return H3_ERR_WORKSPACE;
   NormArgs a = norm_args(*cfg, n_rows, n_heads);
   a.x = x;
-  a.x_row = x_row_stride_elems;
+  a.x_row = n_rows > 1 ? x_row_stride_elems : 0;
   a.x_head = n_heads > 1 ? x_head_stride_elems : 0;
   a.dy = dy;
-  a.dy_row = dy_row_stride_elems;
+  a.dy_row = n_rows > 1 ? dy_row_stride_elems : 0;
   a.dy_head = n_heads > 1 ? dy_head_stride_elems : 0;
   a.dx = dx;
-  a.dx_row = dx_row_stride_elems;
+  a.dx_row = n_rows > 1 ? dx_row_stride_elems : 0;
   a.dx_head = n_heads > 1 ? dx_head_stride_elems : 0;
   a.gain = gain;
   a.part = params ? static_cast<float*>(workspace) : nullptr;

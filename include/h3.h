@@ -414,14 +414,15 @@ typedef struct {
  * k.  fp32 arithmetic, one rounding.  Each output may be its input, with equal
  * strides (in place: the channels that pass through are then not touched), else they must not
  * overlap.  In place for one of q and k and not for the other is refused
- * (H3_ERR_SHAPE).  Strides are in elements, multiples of 16 bytes. */
+ * (H3_ERR_SHAPE).  Strides are in elements, multiples of 16 bytes; the row
+ * strides of one row and the head strides of one head are not looked at. */
 h3_status h3_rope(const h3_rope_config *cfg, int32_t n_rows, const int32_t *pos, int32_t direction,
                   const void *q_in, void *q_out, int32_t n_q_heads, const void *k_in, void *k_out,
                   int32_t n_k_heads, int64_t in_row_stride_elems, int64_t in_head_stride_elems,
                   int64_t out_row_stride_elems, int64_t out_head_stride_elems, cudaStream_t stream);
 
-/* Layer norm and RMS norm over rows of `width` channels (1 .. 8192, any
- * number; H3_ERR_UNSUPPORTED beyond).  dtype: x, y and their gradients;
+/* Layer norm and RMS norm over rows of `width` channels (1 .. 8192, odd
+ * numbers too; H3_ERR_UNSUPPORTED beyond).  dtype: x, y and their gradients;
  * param_dtype: gain and bias.  eps > 0. */
 typedef enum { H3_NORM_RMS = 0, H3_NORM_LAYER = 1 } h3_norm_kind;
 typedef struct {
@@ -437,7 +438,9 @@ typedef struct {
  *   y = c / sqrt(mean(c^2) + eps) * gain + bias      (fp32, one rounding)
  * gain and bias [width], each may be NULL (1 and 0).  y may be x with equal
  * strides, else they must not overlap.  Strides are in elements, multiples of
- * 16 bytes; with n_heads = 1 the head strides are not looked at. */
+ * 16 bytes (several rows of a width that is no such multiple need padding
+ * between them); the row strides of one row and the head strides of one head
+ * are not looked at. */
 h3_status h3_norm_forward(const h3_norm_config *cfg, int32_t n_rows, int32_t n_heads, const void *x,
                           int64_t x_row_stride_elems, int64_t x_head_stride_elems, const void *gain,
                           const void *bias, void *y, int64_t y_row_stride_elems,
