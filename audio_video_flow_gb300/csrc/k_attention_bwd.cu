@@ -31,7 +31,9 @@
 // is: tf32 operands have half the rate and twice the bytes.  Each result so
 // carries the error of one such rounding (2^-8 of each term, independent ones)
 // beside that of its own; statistics, dS before the rounding and the
-// accumulators are fp32.
+// accumulators are fp32.  Nothing else is lost: against the formulas in 64 bits
+// with those two roundings put in, 99.2 % (4099 rows) to 99.9 % (72 rows) of the
+// results have the same bits.
 // On the key side each warp hands P and dS over in two halves of its columns,
 // so that the products that read them begin while the second half is computed
 // (8192 rows x 56 heads, that side alone: 1994 -> 1946 us).
@@ -71,11 +73,9 @@ __device__ __forceinline__ float ab_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The MMA warp runs its loop converged, so that descriptors and addresses are
-// computed in uniform registers, and one lane (`one` != 0) issues.  (With one
-// lane's branch around the loop every operand of every MMA was moved over from
-// vector registers; a product then took 800 cycles, not 512, and 8192 rows x 56
-// heads 4.5 ms, not 3.5.)
+// The MMA warp runs its loop converged, and one lane (`one` != 0) issues.  With
+// one lane's branch around the loop instead, a product took about 800 cycles, not
+// 600-640, and 8192 rows x 56 heads 4.5 ms, not 3.5.
 // Four K steps of 16.  Operand steps are immediate: SA, SB in descriptor units
 // of 16 bytes (shared memory) or TMEM columns.
 template <int SA, int SB>

@@ -14,9 +14,10 @@
 // a fixed order, so results repeat bit for bit.
 //
 // Channels are handled in chunks of 8: thread t of a row's `tpr` threads owns
-// chunks t, t + tpr, ...; only the last chunk of a row may be partial.  Rows of
-// at most 1024 channels belong to a group of up to 32 threads, which reduces by
-// shuffles alone, several groups to a CTA; wider rows to a whole CTA.
+// chunks t, t + tpr, ...; only the last chunk of a row may be partial.  Narrow
+// rows (up to 1024 channels forward, up to 512 backward) belong to a group of up
+// to 32 threads, which reduces by shuffles alone, several groups to a CTA; wider
+// rows to a whole CTA.
 #include "h3_device.cuh"
 #include "h3_internal.h"
 
@@ -26,9 +27,9 @@
 namespace h3 {
 
 namespace {
-constexpr int NORM_GROUP_THREADS = 256;   // CTA of rows of at most 1024 channels
-constexpr int NORM_BWD_GROUP_THREADS = 256, NORM_BWD_GROUP_CTAS = 2;   // the same of the backward kernel
-constexpr int NORM_GROUP_CHUNKS = 128;    // the widest such row
+constexpr int NORM_GROUP_THREADS = 256;   // forward: CTA of rows of at most 1024 channels
+constexpr int NORM_BWD_GROUP_THREADS = 256, NORM_BWD_GROUP_CTAS = 2;   // backward: of at most 512
+constexpr int NORM_GROUP_CHUNKS = 128;    // forward: the widest such row
 constexpr int NORM_MAX_WARPS = 8;
 
 // Eight channels as they lie in memory.
@@ -157,8 +158,10 @@ __device__ __forceinline__ void row_sum(float (&s)[NV], int tpr, float* slot) {
 // Forward: R rows per thread group at a time, NC chunks of each row per
 // thread, kept in registers as read; every row is read and written once.
 // Bound by memory.  Few threads with many chunks each keep more rows, and so
-// more bytes, in flight on an SM than many threads with few (15,860 x 5376 bf16:
-// 56 us, 6.1 TB/s; with three chunks of 256 threads unpacked on loading 94 us).
+// more bytes, in flight on an SM than many threads with few (15,860 x 5376 bf16
+// RMS: 56 us, 6.1 TB/s; with three chunks of 256 threads unpacked on loading 94
+// us).  A layer norm waits for two reductions, one after the other: 76 us there,
+// in fp32 125 us against the RMS norm's 106 (the copy rate: 50 and 101).
 // ---------------------------------------------------------------------------
 template <typename T, int NC, int R, bool LAYER, bool BLOCK>
 __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const NormArgs a) {
@@ -268,8 +271,9 @@ __global__ void __launch_bounds__(NORM_GROUP_THREADS) norm_fwd_kernel(const Norm
 // norm_param_kernel adds them in CTA order.
 // Measured, with both launches: 15,860 x 5376 bf16 RMS 86 us (5.9 TB/s), layer norm with
 // bias 115 us (4.4 TB/s: its two reductions and the accumulators of both
-// parameters, 48 registers of a thread, leave 14 warps to an SM); 1824 x 56 rows
-// of 128 20 us, 15,860 x 56 of them 116 us (5.9 TB/s).
+// parameters, 48 registers of a thread, leave 14 warps to an SM), in fp32 153 and
+// 209 us (6.7 and 4.9 TB/s); 1824 x 56 rows of 128 20 us, 15,860 x 56 of them 116
+// us (5.9 TB/s), layer norms 128.
 // ---------------------------------------------------------------------------
 namespace {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
@@ -594,7 +598,7 @@ constexpr int kNormSmemMax = 227 * 1024;
 constexpr int kNormBwdCtasPerSm = 4;
 
 // Thread layout of a width: chunks per thread nc, threads per row tpr (a power
-// of two up to 32 for rows of at most 1024 channels, whole warps beyond).
+// of two up to 32 for a thread group, whole warps for a CTA).
 struct NormLayout {
   int nc, tpr;
   bool block;
@@ -621,8 +625,13 @@ NormLayout fwd_layout(int width) {
   const int n = (width + 7) / 8;
   return n > NORM_GROUP_CHUNKS ? block_layout(n, 8) : group_layout(n);
 }
-// Backward: as many chunks as 8 warps need, at most 3 while they reach (the
-// accumulators are 16 registers a chunk).
+// Backward: a thread group while two chunks of 32 threads reach, then one chunk
+// of up to 8 warps, then three of them, then four (the accumulators are 16
+// registers a chunk).  Both sides of each limit, 2^25 channels in all, RMS bf16 /
+// layer fp32, us: group against CTA at 400 channels 39 / 70 against 82 / 98, at 512
+// 34 / 67 against 66 / 82; CTA of one chunk against a group of four at 1000 43 / 83
+// against 61 / 148; one chunk against three at 1536 41 / 76 against 57 / 127, at
+// 2048 39 / 77 against 40 / 85.
 NormLayout bwd_layout(int width) {
   const int n = (width + 7) / 8;
   if (n <= 64) return group_layout(n);
@@ -632,7 +641,10 @@ NormLayout bwd_layout(int width) {
 // Rows per group and step, ring stages, and whether rows are held as fp32.
 // Wide bf16 layer norms take two rows at a time and unpack them for every pass:
 // their second reduction costs more than the unpacking (8192 channels: 112 us
-// against 123 held; RMS norms measure the same either way).
+// against 123 held; RMS norms measure the same either way).  fp32 rows are held:
+// two at a time do not fit in shared memory at four chunks, and one at a time read
+// again measures 102, 100 and 106 us at 2688, 5376 and 8192 channels (2^25 in all)
+// against 89, 94 and 92 held.
 struct NormBwdShape {
   int rows, stages;
   bool hold;
