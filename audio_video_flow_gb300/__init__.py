@@ -70,6 +70,16 @@ class NormConfig(ctypes.Structure):
                 ("eps", c_float)]
 
 
+class Window(ctypes.Structure):
+    _fields_ = [("left", c_int32), ("right", c_int32), ("n_first", c_int32), ("unit", c_int32), ("origin", c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("n_pages", c_int32), ("page_size", c_int32),
+                ("n_kv_heads", c_int32), ("n_seqs", c_int32), ("table_width", c_int32), ("table", c_void_p),
+                ("length", c_void_p)]
+
+
 _lib = None
 
 
@@ -84,6 +94,7 @@ def lib() -> ctypes.CDLL:
         i32, sz, vp = c_int32, c_size_t, c_void_p
         cfgp, wp, mp = ctypes.POINTER(BlockConfig), ctypes.POINTER(BlockWeights), ctypes.POINTER(PackedMeta)
         ropep, normp = ctypes.POINTER(RopeConfig), ctypes.POINTER(NormConfig)
+        winp, cachep, i64 = ctypes.POINTER(Window), ctypes.POINTER(Cache), c_int64
         sig = {
             "h3_block_workspace_bytes": (sz, [cfgp, i32, i32]),
             "h3_block_adaln_side_ctas": (i32, [cfgp, i32]),
@@ -106,6 +117,16 @@ def lib() -> ctypes.CDLL:
             "h3_attention_backward_workspace_bytes": (sz, [i32, i32]),
             "h3_attention_backward": (i32, [i32, i32, vp, vp, vp, c_int64, c_int64, vp, vp, vp, vp, vp, vp, c_int64,
                                             c_int64, vp, sz, vp]),
+            "h3_attention_window_workspace_bytes": (sz, [i32, i32, i32]),
+            "h3_attention_window": (i32, [winp, i32, i32, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+            "h3_attention_window_backward_workspace_bytes": (sz, [i32, i32, i32]),
+            "h3_attention_window_backward": (i32, [winp, i32, i32, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp,
+                                                   i64, i64, vp, vp, i64, i64, vp, sz, vp]),
+            "h3_cache_append": (i32, [cachep, i32, vp, vp, vp, i64, i64, vp, vp]),
+            "h3_attention_cached_workspace_bytes": (sz, [cachep, i32, i32]),
+            "h3_attention_cached": (i32, [cachep, winp, i32, i32, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+            "h3_cache_weights": (i32, [cachep, winp, i32, i32, vp, vp, i64, i64, vp, vp, vp, vp]),
+            "h3_cache_evict": (i32, [cachep, cachep, i32, i32, i32, vp, vp, vp, vp, vp]),
             "h3_rope": (i32, [ropep, i32, vp, i32, vp, vp, i32, vp, vp, i32, c_int64, c_int64, c_int64, c_int64, vp]),
             "h3_norm_forward": (i32, [normp, i32, i32, vp, c_int64, c_int64, vp, vp, vp, c_int64, c_int64, vp]),
             "h3_norm_backward_workspace_bytes": (sz, [normp, i32, i32]),
@@ -222,6 +243,25 @@ def make_rope_config(head_dim: int, n_axes: int, n_freqs: int, layout: int = H3_
 def make_norm_config(kind: int, width: int, dtype: int = H3_BF16, param_dtype: int = H3_BF16,
                      eps: float = 1e-5) -> NormConfig:
     return NormConfig(kind, width, dtype, param_dtype, eps)
+
+
+def make_window(left: int = -1, right: int = -1, n_first: int = 0, unit: int = 1, origin: int = 0) -> Window:
+    """What a row sees: the units (of `unit` rows, counted from row `origin`) from `left` before its own to `right`
+    after it, -1 for all of them, and the first n_first keys that are not after those."""
+    return Window(left, right, n_first, unit, origin)
+
+
+def make_cache(k_pages, v_pages, table, length) -> Cache:
+    """k_pages, v_pages: bf16 [n_pages][n_kv_heads][page_size][128]; table int32 [n_seqs][table_width], length int32
+    [n_seqs], all contiguous on the device.  The struct keeps the tensors alive while it lives."""
+    n_pages, n_kv_heads, page_size, width = (int(n) for n in k_pages.shape)
+    if width != 128 or tuple(v_pages.shape) != tuple(k_pages.shape) or table.dim() != 2 \
+            or tuple(length.shape) != (int(table.shape[0]),):
+        raise H3Error(H3_ERR_SHAPE, "make_cache")
+    s = Cache(_ptr(k_pages), _ptr(v_pages), n_pages, page_size, n_kv_heads, int(table.shape[0]), int(table.shape[1]),
+              _ptr(table), _ptr(length))
+    s._tensors = (k_pages, v_pages, table, length)
+    return s
 
 
 # ---------------------------------------------------------------------------
@@ -372,6 +412,66 @@ def h3_attention_backward(n_rows: int, n_heads: int, q, k, v, row_stride: int, h
                                        _ptr(d_o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), d_row_stride,
                                        d_head_stride, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream(stream)), "h3_attention_backward")
+
+
+def h3_attention_window_workspace_bytes(n_rows: int, n_heads: int, n_kv_heads: int) -> int:
+    return int(lib().h3_attention_window_workspace_bytes(n_rows, n_heads, n_kv_heads))
+
+
+def h3_attention_window(window: Window, n_rows: int, n_heads: int, n_kv_heads: int, q, q_row_stride: int,
+                        q_head_stride: int, k, v, kv_row_stride: int, kv_head_stride: int, o, lse, workspace,
+                        stream=None) -> None:
+    _check(lib().h3_attention_window(ctypes.byref(window), n_rows, n_heads, n_kv_heads, _ptr(q), q_row_stride,
+                                     q_head_stride, _ptr(k), _ptr(v), kv_row_stride, kv_head_stride, _ptr(o),
+                                     _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream)), "h3_attention_window")
+
+
+def h3_attention_window_backward_workspace_bytes(n_rows: int, n_heads: int, n_kv_heads: int) -> int:
+    return int(lib().h3_attention_window_backward_workspace_bytes(n_rows, n_heads, n_kv_heads))
+
+
+def h3_attention_window_backward(window: Window, n_rows: int, n_heads: int, n_kv_heads: int, q, q_row_stride: int,
+                                 q_head_stride: int, k, v, kv_row_stride: int, kv_head_stride: int, o, d_o, lse, dq,
+                                 dq_row_stride: int, dq_head_stride: int, dk, dv, dkv_row_stride: int,
+                                 dkv_head_stride: int, workspace, stream=None) -> None:
+    _check(lib().h3_attention_window_backward(ctypes.byref(window), n_rows, n_heads, n_kv_heads, _ptr(q), q_row_stride,
+                                              q_head_stride, _ptr(k), _ptr(v), kv_row_stride, kv_head_stride, _ptr(o),
+                                              _ptr(d_o), _ptr(lse), _ptr(dq), dq_row_stride, dq_head_stride, _ptr(dk),
+                                              _ptr(dv), dkv_row_stride, dkv_head_stride, _ptr(workspace),
+                                              workspace.numel() * workspace.element_size(), _stream(stream)),
+           "h3_attention_window_backward")
+
+
+def h3_cache_append(cache: Cache, n_rows: int, seq_start, k, v, row_stride: int, head_stride: int, weights=None,
+                    stream=None) -> None:
+    _check(lib().h3_cache_append(ctypes.byref(cache), n_rows, _ptr(seq_start), _ptr(k), _ptr(v), row_stride,
+                                 head_stride, _ptr(weights), _stream(stream)), "h3_cache_append")
+
+
+def h3_attention_cached_workspace_bytes(cache: Cache, n_rows: int, n_heads: int) -> int:
+    return int(lib().h3_attention_cached_workspace_bytes(ctypes.byref(cache), n_rows, n_heads))
+
+
+def h3_attention_cached(cache: Cache, window: Window, n_rows: int, n_heads: int, seq_start, q, q_row_stride: int,
+                        q_head_stride: int, o, lse, workspace, stream=None) -> None:
+    _check(lib().h3_attention_cached(ctypes.byref(cache), ctypes.byref(window), n_rows, n_heads, _ptr(seq_start),
+                                     _ptr(q), q_row_stride, q_head_stride, _ptr(o), _ptr(lse), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+           "h3_attention_cached")
+
+
+def h3_cache_weights(cache: Cache, window: Window, n_rows: int, n_heads: int, seq_start, q, q_row_stride: int,
+                     q_head_stride: int, lse, weights_in, weights_out, stream=None) -> None:
+    _check(lib().h3_cache_weights(ctypes.byref(cache), ctypes.byref(window), n_rows, n_heads, _ptr(seq_start), _ptr(q),
+                                  q_row_stride, q_head_stride, _ptr(lse), _ptr(weights_in), _ptr(weights_out),
+                                  _stream(stream)), "h3_cache_weights")
+
+
+def h3_cache_evict(cache: Cache, to: Cache, budget: int, n_first: int, n_recent: int, weights, weights_to, kept,
+                   length_out, stream=None) -> None:
+    _check(lib().h3_cache_evict(ctypes.byref(cache), ctypes.byref(to), budget, n_first, n_recent, _ptr(weights),
+                                _ptr(weights_to), _ptr(kept), _ptr(length_out), _stream(stream)), "h3_cache_evict")
 
 
 def h3_rope(cfg: RopeConfig, n_rows: int, pos, direction: int, q_in, q_out, n_q_heads: int, k_in, k_out,

@@ -60,7 +60,7 @@ std::mutex g_site_mu;
 // barrier's shared-memory byte offset / 8, or kSiteStreamKFlag).
 void note_error_site(uint32_t site) {
   static const char* const names[] = {"unknown", "gemm", "attention-1q", "attention-2q", "adaln-table",
-                                      "rope-qknorm", "attention-backward"};
+                                      "rope-qknorm", "attention-backward", "attention-window", "cache-weights"};
   const uint32_t k = site >> 24, lo = site & 0xFFFFFFu;
   const char* kn = k < sizeof(names) / sizeof(names[0]) ? names[k] : "unknown";
   std::lock_guard<std::mutex> lk(g_site_mu);
@@ -149,6 +149,31 @@ bool make_tmap_qkv(CUtensorMap* tm, const void* base, uint64_t n_rows, uint64_t 
   const cuuint32_t box[3] = {64, 1, box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_q_shared(CUtensorMap* tm, const void* base, uint64_t n_rows, uint64_t kv_heads, uint64_t G,
+                        uint64_t row_stride, uint64_t head_stride, uint32_t box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {128, G, kv_heads, n_rows};
+  const cuuint64_t strides[3] = {head_stride * 2, head_stride * G * 2, row_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, box_rows};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_pages(CUtensorMap* tm, const void* base, uint64_t n_pages, uint64_t kv_heads, uint64_t page_size) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {128, page_size, kv_heads, n_pages};
+  const cuuint64_t strides[3] = {256, page_size * 256, kv_heads * page_size * 256};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(page_size < 128 ? page_size : 128), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1353,14 +1378,14 @@ h3_status h3_attention_backward(int32_t n_rows, int32_t n_heads, const void* q, 
   a.dq = static_cast<__nv_bfloat16*>(dq);
   a.dk = static_cast<__nv_bfloat16*>(dk);
   a.dv = static_cast<__nv_bfloat16*>(dv);
-  a.d_row_stride = d_row_stride_elems;
-  a.d_head_stride = d_head_stride_elems;
+  a.d_row_stride = a.dkv_row_stride = d_row_stride_elems;
+  a.d_head_stride = a.dkv_head_stride = d_head_stride_elems;
   a.scale = (float)(1.0 / std::sqrt(128.0));
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
   a.o_elems = (size_t)S * H * 128;
   a.lse_elems = (size_t)S * H;
   a.rowval_elems = (size_t)a.tiles * H * 256;
-  a.d_elems = view_elems(n_rows, n_heads, 128, d_row_stride_elems, d_head_stride_elems);
+  a.d_elems = a.dkv_elems = view_elems(n_rows, n_heads, 128, d_row_stride_elems, d_head_stride_elems);
   a.err = device_error_word();
   return cuda_st(launch_attention_bwd(tq, tk, tv, to, a, stream));
 }
@@ -1495,6 +1520,325 @@ h3_status h3_norm_backward(const h3_norm_config* cfg, int32_t n_rows, int32_t n_
   a.dx_elems = view_elems(n_rows, n_heads, cfg->width, a.dx_row, a.dx_head);
   a.part_elems = params ? (size_t)norm_bwd_ctas(a.units, a.width, a.fp32, a.layer) * 2 * a.part_width : 0;
   return cuda_st(launch_norm_bwd(a, dgain, dbias, stream));
+}
+
+// ===========================================================================
+// windows and the paged cache
+// ===========================================================================
+namespace {
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+h3_status check_window(const h3_window* w) {
+  if (!w) return H3_ERR_NULL;
+  if (w->left < -1 || w->right < -1 || w->n_first < 0 || w->unit < 1 || w->origin < 0) return H3_ERR_SHAPE;
+  return H3_OK;
+}
+WindowArgs window_args(const h3_window& w) { return {w.left, w.right, w.n_first, w.unit, w.origin}; }
+
+// Query heads over KV heads of 128 channels: G = n_heads / n_kv_heads share one.
+h3_status check_shared(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
+  if (n_rows < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return H3_ERR_SHAPE;
+  if (n_rows > kCacheMaxRows || n_heads > 32767 || n_heads / n_kv_heads > 128) return H3_ERR_UNSUPPORTED;
+  return H3_OK;
+}
+// Strides of a bf16 [rows][heads][128] view, and those that a tensor map is given
+// (one row's or one head's is not used, and replaced by a valid one).
+h3_status check_view(int32_t rows, int32_t heads, int64_t& row_stride, int64_t& head_stride) {
+  const h3_status s = check_strides(128, rows, heads, row_stride, head_stride, 8);
+  if (s != H3_OK) return s;
+  if (rows == 1) row_stride = 128;
+  if (heads == 1) head_stride = 128;
+  // a tensor map's strides, with that over the heads that share one, are below 2^40 bytes
+  if (row_stride >= (int64_t(1) << 39) || head_stride >= (int64_t(1) << 39) / heads) return H3_ERR_UNSUPPORTED;
+  return H3_OK;
+}
+
+h3_status check_cache(const h3_cache* c) {
+  if (!c || !c->k || !c->v || !c->table || !c->length) return H3_ERR_NULL;
+  if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_seqs < 1 || c->table_width < 1) return H3_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return H3_ERR_UNSUPPORTED;
+  if (c->n_kv_heads > 1024 || c->n_seqs > kCacheMaxSeqs ||
+      (int64_t)c->table_width * c->page_size > kCacheMaxRows)
+    return H3_ERR_UNSUPPORTED;
+  if (!al16(c->k) || !al16(c->v) || !al4(c->table) || !al4(c->length)) return H3_ERR_ALIGN;
+  if (c->k == c->v) return H3_ERR_SHAPE;
+  return H3_OK;
+}
+CacheArgs cache_args(const h3_cache& c, const int32_t* start) {
+  return {c.n_pages, c.page_size, c.n_kv_heads, c.n_seqs, c.table_width, c.table, c.length, start};
+}
+size_t cache_rows(const h3_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * c.page_size; }
+
+size_t attn_win_ws_bytes(int64_t n_rows, int64_t n_heads, int64_t n_kv_heads, int64_t n_seqs, int64_t max_keys,
+                         int* ctas, size_t* desc, size_t* part_elems) {
+  int rows, slots;
+  const int G = (int)(n_heads / n_kv_heads);
+  *ctas = attn_win_ctas(n_rows, n_kv_heads, n_seqs, G, max_keys);
+  attn_win_part(n_rows, G, &rows, &slots);
+  *desc = attn_win_desc_bytes(*ctas);
+  *part_elems = (size_t)*ctas * slots * rows * 130;
+  return al256(*desc + *part_elems * 4);
+}
+
+// The call over one document (c null) or a cache, its arguments checked.
+h3_status run_attention_window(const h3_window& w, const h3_cache* c, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                               const int32_t* start, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               void* o, float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  AttnWinArgs a{};
+  int ctas = 0;
+  size_t desc = 0;
+  const int64_t seqs = c ? c->n_seqs : 1, keys = c ? (int64_t)c->table_width * c->page_size : n_rows;
+  if (ws_bytes < attn_win_ws_bytes(n_rows, n_heads, n_kv_heads, seqs, keys, &ctas, &desc, &a.part_elems))
+    return H3_ERR_WORKSPACE;
+  a.w = window_args(w);
+  if (c) {
+    a.c = cache_args(*c, start);
+  } else {
+    a.c.n_kv_heads = n_kv_heads;
+    a.c.n_seqs = 1;
+  }
+  a.n_rows = n_rows;
+  a.H = n_heads;
+  a.G = n_heads / n_kv_heads;
+  a.R = 128 / a.G;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.desc = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + desc);
+  attn_win_part(n_rows, a.G, &a.part_rows, &a.part_slots);
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  a.o_elems = (size_t)n_rows * n_heads * 128;
+  a.lse_elems = lse ? (size_t)n_rows * n_heads : 0;
+  a.err = device_error_word();
+  return cuda_st(launch_attention_window(tq, tk, tv, a, ctas, stream));
+}
+}  // namespace
+
+size_t h3_attention_window_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
+  if (check_shared(n_rows, n_heads, n_kv_heads) != H3_OK) return 0;
+  int ctas;
+  size_t desc, elems;
+  return attn_win_ws_bytes(n_rows, n_heads, n_kv_heads, 1, n_rows, &ctas, &desc, &elems);
+}
+
+h3_status h3_attention_window(const h3_window* window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads, const void* q,
+                              int64_t q_row_stride_elems, int64_t q_head_stride_elems, const void* k, const void* v,
+                              int64_t kv_row_stride_elems, int64_t kv_head_stride_elems, void* o, float* lse_opt,
+                              void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  h3_status s = check_window(window);
+  if (s != H3_OK) return s;
+  if ((s = check_shared(n_rows, n_heads, n_kv_heads)) != H3_OK) return s;
+  if (!q || !k || !v || !o || !workspace) return H3_ERR_NULL;
+  if ((s = check_view(n_rows, n_heads, q_row_stride_elems, q_head_stride_elems)) != H3_OK) return s;
+  if ((s = check_view(n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems)) != H3_OK) return s;
+  if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || !al4(lse_opt) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return H3_ERR_ALIGN;
+  if (o == q || o == k || o == v || o == workspace || lse_opt == o || lse_opt == workspace) return H3_ERR_SHAPE;
+  CUtensorMap tq, tk, tv;
+  const uint32_t G = (uint32_t)(n_heads / n_kv_heads);
+  if (!make_tmap_q_shared(&tq, q, n_rows, n_kv_heads, G, q_row_stride_elems, q_head_stride_elems, 128 / G) ||
+      !make_tmap_qkv(&tk, k, n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems, 128) ||
+      !make_tmap_qkv(&tv, v, n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems, 128))
+    return H3_ERR_CUDA;
+  return run_attention_window(*window, nullptr, n_rows, n_heads, n_kv_heads, nullptr, tq, tk, tv, o, lse_opt, workspace,
+                              ws_bytes, stream);
+}
+
+size_t h3_attention_window_backward_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
+  if (check_shared(n_rows, n_heads, n_kv_heads) != H3_OK) return 0;
+  return attn_bwd_ws_bytes(n_rows, n_heads);
+}
+
+h3_status h3_attention_window_backward(const h3_window* window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                                       const void* q, int64_t q_row_stride_elems, int64_t q_head_stride_elems,
+                                       const void* k, const void* v, int64_t kv_row_stride_elems,
+                                       int64_t kv_head_stride_elems, const void* o, const void* d_o, const float* lse,
+                                       void* dq, int64_t dq_row_stride_elems, int64_t dq_head_stride_elems, void* dk,
+                                       void* dv, int64_t dkv_row_stride_elems, int64_t dkv_head_stride_elems,
+                                       void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  h3_status s = check_window(window);
+  if (s != H3_OK) return s;
+  if ((s = check_shared(n_rows, n_heads, n_kv_heads)) != H3_OK) return s;
+  if (!q || !k || !v || !o || !d_o || !lse || !dq || !dk || !dv || !workspace) return H3_ERR_NULL;
+  if ((s = check_view(n_rows, n_heads, q_row_stride_elems, q_head_stride_elems)) != H3_OK) return s;
+  if ((s = check_view(n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems)) != H3_OK) return s;
+  if ((s = check_view(n_rows, n_heads, dq_row_stride_elems, dq_head_stride_elems)) != H3_OK) return s;
+  if ((s = check_view(n_rows, n_kv_heads, dkv_row_stride_elems, dkv_head_stride_elems)) != H3_OK) return s;
+  if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || !al16(d_o) || !al16(dq) || !al16(dk) || !al16(dv) || !al4(lse) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return H3_ERR_ALIGN;
+  if (!apart(n_rows, n_heads, 128, dq_row_stride_elems, dq_head_stride_elems) ||
+      !apart(n_rows, n_kv_heads, 128, dkv_row_stride_elems, dkv_head_stride_elems))
+    return H3_ERR_SHAPE;
+  const void* const in[] = {q, k, v, o, d_o, lse, workspace};
+  void* const out[] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* p : in)
+      if (out[i] == p) return H3_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return H3_ERR_SHAPE;
+  }
+  if (ws_bytes < attn_bwd_ws_bytes(n_rows, n_heads)) return H3_ERR_WORKSPACE;
+  CUtensorMap tq, tk, tv, to;
+  const uint64_t S = (uint64_t)n_rows, H = (uint64_t)n_heads, Hk = (uint64_t)n_kv_heads;
+  if (!make_tmap_qkv(&tq, q, S, H, q_row_stride_elems, q_head_stride_elems, 128) ||
+      !make_tmap_qkv(&tk, k, S, Hk, kv_row_stride_elems, kv_head_stride_elems, 128) ||
+      !make_tmap_qkv(&tv, v, S, Hk, kv_row_stride_elems, kv_head_stride_elems, 128) ||
+      !make_tmap_qkv(&to, d_o, S, H, H * 128, 128, 128))
+    return H3_ERR_CUDA;
+  AttnBwdArgs a{};
+  a.S = n_rows;
+  a.H = n_heads;
+  a.G = n_heads / n_kv_heads;
+  a.w = window_args(*window);
+  a.tiles = (int)(((int64_t)n_rows + 127) / 128);
+  a.o = static_cast<const __nv_bfloat16*>(o);
+  a.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  a.lse = lse;
+  a.rowvals = static_cast<float*>(workspace);
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.d_row_stride = dq_row_stride_elems;
+  a.d_head_stride = dq_head_stride_elems;
+  a.dkv_row_stride = dkv_row_stride_elems;
+  a.dkv_head_stride = dkv_head_stride_elems;
+  a.scale = (float)(1.0 / std::sqrt(128.0));
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  a.o_elems = (size_t)S * H * 128;
+  a.lse_elems = (size_t)S * H;
+  a.rowval_elems = (size_t)a.tiles * H * 256;
+  a.d_elems = view_elems(n_rows, n_heads, 128, dq_row_stride_elems, dq_head_stride_elems);
+  a.dkv_elems = view_elems(n_rows, n_kv_heads, 128, dkv_row_stride_elems, dkv_head_stride_elems);
+  a.err = device_error_word();
+  return cuda_st(launch_attention_window_bwd(tq, tk, tv, to, a, stream));
+}
+
+h3_status h3_cache_append(const h3_cache* cache, int32_t n_rows, const int32_t* seq_start, const void* k, const void* v,
+                          int64_t row_stride_elems, int64_t head_stride_elems, float* weights_opt, cudaStream_t stream) {
+  h3_status s = check_cache(cache);
+  if (s != H3_OK) return s;
+  if (n_rows < 1) return H3_ERR_SHAPE;
+  if (n_rows > kCacheMaxRows) return H3_ERR_UNSUPPORTED;
+  if (!seq_start || !k || !v) return H3_ERR_NULL;
+  if ((s = check_view(n_rows, cache->n_kv_heads, row_stride_elems, head_stride_elems)) != H3_OK) return s;
+  if (!al16(k) || !al16(v) || !al4(seq_start) || !al4(weights_opt)) return H3_ERR_ALIGN;
+  if (k == cache->k || k == cache->v || v == cache->k || v == cache->v) return H3_ERR_SHAPE;
+  AppendArgs a{};
+  a.c = cache_args(*cache, seq_start);
+  a.n_rows = n_rows;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.row_stride = row_stride_elems;
+  a.head_stride = head_stride_elems;
+  a.k_pages = static_cast<__nv_bfloat16*>(cache->k);
+  a.v_pages = static_cast<__nv_bfloat16*>(cache->v);
+  a.weights = weights_opt;
+  a.page_elems = cache_rows(*cache) * 128;
+  a.src_elems = view_elems(n_rows, cache->n_kv_heads, 128, row_stride_elems, head_stride_elems);
+  a.err = device_error_word();
+  return cuda_st(launch_cache_append(a, stream));
+}
+
+size_t h3_attention_cached_workspace_bytes(const h3_cache* cache, int32_t n_rows, int32_t n_heads) {
+  if (check_cache(cache) != H3_OK || check_shared(n_rows, n_heads, cache->n_kv_heads) != H3_OK) return 0;
+  int ctas;
+  size_t desc, elems;
+  return attn_win_ws_bytes(n_rows, n_heads, cache->n_kv_heads, cache->n_seqs,
+                           (int64_t)cache->table_width * cache->page_size, &ctas, &desc, &elems);
+}
+
+h3_status h3_attention_cached(const h3_cache* cache, const h3_window* window, int32_t n_rows, int32_t n_heads,
+                              const int32_t* seq_start, const void* q, int64_t q_row_stride_elems,
+                              int64_t q_head_stride_elems, void* o, float* lse_opt, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream) {
+  h3_status s = check_cache(cache);
+  if (s != H3_OK) return s;
+  if ((s = check_window(window)) != H3_OK) return s;
+  if ((s = check_shared(n_rows, n_heads, cache->n_kv_heads)) != H3_OK) return s;
+  if (!seq_start || !q || !o || !workspace) return H3_ERR_NULL;
+  if ((s = check_view(n_rows, n_heads, q_row_stride_elems, q_head_stride_elems)) != H3_OK) return s;
+  if (!al16(q) || !al16(o) || !al4(seq_start) || !al4(lse_opt) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return H3_ERR_ALIGN;
+  if (o == q || o == cache->k || o == cache->v || o == workspace || lse_opt == o || lse_opt == workspace)
+    return H3_ERR_SHAPE;
+  CUtensorMap tq, tk, tv;
+  const uint32_t G = (uint32_t)(n_heads / cache->n_kv_heads);
+  if (!make_tmap_q_shared(&tq, q, n_rows, cache->n_kv_heads, G, q_row_stride_elems, q_head_stride_elems, 128 / G) ||
+      !make_tmap_pages(&tk, cache->k, cache->n_pages, cache->n_kv_heads, cache->page_size) ||
+      !make_tmap_pages(&tv, cache->v, cache->n_pages, cache->n_kv_heads, cache->page_size))
+    return H3_ERR_CUDA;
+  return run_attention_window(*window, cache, n_rows, n_heads, cache->n_kv_heads, seq_start, tq, tk, tv, o, lse_opt,
+                              workspace, ws_bytes, stream);
+}
+
+h3_status h3_cache_weights(const h3_cache* cache, const h3_window* window, int32_t n_rows, int32_t n_heads,
+                           const int32_t* seq_start, const void* q, int64_t q_row_stride_elems,
+                           int64_t q_head_stride_elems, const float* lse, const float* weights_in_opt,
+                           float* weights_out, cudaStream_t stream) {
+  h3_status s = check_cache(cache);
+  if (s != H3_OK) return s;
+  if ((s = check_window(window)) != H3_OK) return s;
+  if ((s = check_shared(n_rows, n_heads, cache->n_kv_heads)) != H3_OK) return s;
+  if (!seq_start || !q || !lse || !weights_out) return H3_ERR_NULL;
+  if ((s = check_view(n_rows, n_heads, q_row_stride_elems, q_head_stride_elems)) != H3_OK) return s;
+  if (!al16(q) || !al4(seq_start) || !al4(lse) || !al4(weights_in_opt) || !al4(weights_out)) return H3_ERR_ALIGN;
+  if (weights_out == lse || (const void*)weights_out == q || (void*)weights_out == cache->k ||
+      (void*)weights_out == cache->v)
+    return H3_ERR_SHAPE;
+  CUtensorMap tq, tk;
+  CacheWeightsArgs a{};
+  a.w = window_args(*window);
+  a.c = cache_args(*cache, seq_start);
+  a.n_rows = n_rows;
+  a.G = n_heads / cache->n_kv_heads;
+  a.R = 128 / a.G;
+  if (!make_tmap_q_shared(&tq, q, n_rows, cache->n_kv_heads, a.G, q_row_stride_elems, q_head_stride_elems, a.R) ||
+      !make_tmap_pages(&tk, cache->k, cache->n_pages, cache->n_kv_heads, cache->page_size))
+    return H3_ERR_CUDA;
+  a.lse = lse;
+  a.in = weights_in_opt;
+  a.out = weights_out;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  a.lse_elems = (size_t)n_rows * n_heads;
+  a.page_rows = cache_rows(*cache);
+  a.err = device_error_word();
+  return cuda_st(launch_cache_weights(tq, tk, a, stream));
+}
+
+h3_status h3_cache_evict(const h3_cache* from, const h3_cache* to, int32_t budget, int32_t n_first, int32_t n_recent,
+                         const float* weights, float* weights_to_opt, int32_t* kept, int32_t* length_out,
+                         cudaStream_t stream) {
+  h3_status s = check_cache(from);
+  if (s != H3_OK) return s;
+  if ((s = check_cache(to)) != H3_OK) return s;
+  if (!weights || !kept || !length_out) return H3_ERR_NULL;
+  if (from->n_kv_heads != to->n_kv_heads || from->n_seqs != to->n_seqs) return H3_ERR_SHAPE;
+  if (budget < 1 || n_first < 0 || n_recent < 0 || (int64_t)n_first + n_recent > budget) return H3_ERR_SHAPE;
+  if (budget > kCacheMaxRows) return H3_ERR_UNSUPPORTED;
+  if (!al4(weights) || !al4(weights_to_opt) || !al4(kept) || !al4(length_out)) return H3_ERR_ALIGN;
+  // the rows move to pages of their own; the lengths that are read are not those written
+  if (from->table == to->table || from->length == length_out || (const void*)kept == (const void*)length_out ||
+      from->k == to->v || from->v == to->k)
+    return H3_ERR_SHAPE;
+  EvictArgs a{};
+  a.from = cache_args(*from, nullptr);
+  a.to = cache_args(*to, nullptr);
+  a.budget = budget;
+  a.first = n_first;
+  a.recent = n_recent;
+  a.weights = weights;
+  a.weights_to = weights_to_opt;
+  a.k_from = static_cast<const __nv_bfloat16*>(from->k);
+  a.v_from = static_cast<const __nv_bfloat16*>(from->v);
+  a.k_to = static_cast<__nv_bfloat16*>(to->k);
+  a.v_to = static_cast<__nv_bfloat16*>(to->v);
+  a.kept = kept;
+  a.length = length_out;
+  a.from_rows = cache_rows(*from);
+  a.to_rows = cache_rows(*to);
+  a.err = device_error_word();
+  return cuda_st(launch_cache_evict(a, stream));
 }
 
 h3_status h3_out_projection(const h3_block_config* cfg, const h3_packed_meta* meta, const void* table,

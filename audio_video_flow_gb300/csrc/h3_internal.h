@@ -21,6 +21,13 @@ bool make_tmap_2d(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t col
 bool make_tmap_qkv(CUtensorMap* tm, const void* base, uint64_t n_rows, uint64_t n_heads,
                    uint64_t row_stride, uint64_t head_stride, uint32_t box_rows);
 
+// 4-D bf16 query view (channel c < 128, head g < G that shares KV head h < Hk, row i) at
+// base + i*row_stride + (h*G + g)*head_stride + c, box (64, G, 1, box_rows).
+bool make_tmap_q_shared(CUtensorMap* tm, const void* base, uint64_t n_rows, uint64_t kv_heads, uint64_t G,
+                        uint64_t row_stride, uint64_t head_stride, uint32_t box_rows);
+// 4-D pages [n_pages][kv_heads][page_size][128], box (64, min(page_size, 128), 1, 1).
+bool make_tmap_pages(CUtensorMap* tm, const void* base, uint64_t n_pages, uint64_t kv_heads, uint64_t page_size);
+
 int num_sms();
 
 // Launch with programmatic stream serialization (the kernel may start while
@@ -277,22 +284,105 @@ cudaError_t launch_attention(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
 // ---------------------------------------------------------------------------
 // attention gradient (tcgen05, k_attention_bwd.cu)
 // ---------------------------------------------------------------------------
+struct WindowArgs {
+  int left, right, first, unit, origin;   // as h3_window
+};
 struct AttnBwdArgs {
   int S, H;
+  WindowArgs w;           // with a window only, as G: query heads that share a KV head
+  int G;
   int tiles;              // 128-row tiles: ceil(S / 128)
   const __nv_bfloat16* o;     // [S][H*128]
   const __nv_bfloat16* d_o;   // [S][H*128]
   const float* lse;           // [H][S]
   float* rowvals;             // workspace [H][tiles][2][128]: lse * log2(e), rowsum(dO o O)
   __nv_bfloat16 *dq, *dk, *dv;
-  int64_t d_row_stride, d_head_stride;
+  int64_t d_row_stride, d_head_stride;      // dq
+  int64_t dkv_row_stride, dkv_head_stride;  // dk, dv
   float scale;                // 1 / sqrt(128)
   float scale_log2;           // log2(e) / sqrt(128)
-  size_t o_elems, lse_elems, rowval_elems, d_elems;   // extents for the bounds-checked build
+  size_t o_elems, lse_elems, rowval_elems, d_elems, dkv_elems;   // extents for the bounds-checked build
   uint32_t* err;
 };
 cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                  const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream);
+// the same with a window and shared KV heads
+cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                        const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// attention with a window, over one document or a paged cache
+// (k_attention_window.cu, k_cache.cu)
+// ---------------------------------------------------------------------------
+// A paged cache: pages [n_pages][n_kv_heads][page_size][128], and the rows of
+// each sequence.  One document of its own (not paged): start is null, n_seqs 1.
+struct CacheArgs {
+  int n_pages, page_size, n_kv_heads, n_seqs, table_width;
+  const int32_t* table;    // [n_seqs][table_width]
+  const int32_t* length;   // [n_seqs]
+  const int32_t* start;    // [n_seqs + 1], new rows
+};
+constexpr int kCacheMaxSeqs = 1024;
+constexpr int kCacheMaxRows = 1 << 24;    // new rows of a call, and slots of a sequence
+struct AttnWinArgs {
+  WindowArgs w;
+  CacheArgs c;
+  int n_rows, H, G, R;        // G query heads share a KV head; a 128-row tile holds R rows x G heads
+  __nv_bfloat16* o;           // [n_rows][H*128]
+  float* lse;                 // [H][n_rows] or null
+  int4* desc;                 // workspace: per CTA the partial tiles that it leaves (AwDesc)
+  float* part;                // workspace: partial results
+  int part_rows, part_slots;  // rows of a partial tile, partial tiles per CTA
+  float scale_log2;           // log2(e) / sqrt(128)
+  size_t o_elems, lse_elems, part_elems;   // extents for the bounds-checked build
+  uint32_t* err;
+};
+// CTAs, bytes of workspace and the split into desc and part for a call of
+// n_rows rows of H query heads over KV heads shared by G
+int attn_win_ctas(int64_t n_rows, int64_t kv_heads, int64_t n_seqs, int G, int64_t max_keys);
+size_t attn_win_desc_bytes(int ctas);
+void attn_win_part(int64_t n_rows, int G, int* part_rows, int* part_slots);
+cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    const AttnWinArgs& a, int ctas, cudaStream_t stream);
+
+struct AppendArgs {
+  CacheArgs c;
+  int n_rows;
+  const __nv_bfloat16 *k, *v;
+  int64_t row_stride, head_stride;
+  __nv_bfloat16 *k_pages, *v_pages;
+  float* weights;             // or null
+  size_t page_elems, src_elems;            // extents for the bounds-checked build
+  uint32_t* err;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
+struct CacheWeightsArgs {
+  WindowArgs w;
+  CacheArgs c;
+  int n_rows, G, R;           // as AttnWinArgs
+  int tiles;                  // 128-key tiles of a unit, set by the launcher
+  const float* lse;           // [H][n_rows]
+  const float* in;            // or null
+  float* out;
+  float scale_log2;
+  size_t lse_elems, page_rows;             // extents for the bounds-checked build
+  uint32_t* err;
+};
+cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK, CacheWeightsArgs a,
+                                 cudaStream_t stream);
+struct EvictArgs {
+  CacheArgs from, to;
+  int budget, first, recent;
+  const float* weights;
+  float* weights_to;          // or null
+  const __nv_bfloat16 *k_from, *v_from;
+  __nv_bfloat16 *k_to, *v_to;
+  int32_t* kept;              // [n_seqs][n_kv_heads][budget]
+  int32_t* length;            // [n_seqs]
+  size_t from_rows, to_rows;               // extents for the bounds-checked build
+  uint32_t* err;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // row norms (k_norm.cu) and rotary positions (k_rope.cu)

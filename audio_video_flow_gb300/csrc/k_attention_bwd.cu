@@ -51,7 +51,7 @@
 // Tried and slower: G tiles multicast to a pair of CTAs (3.69 ms at 8192 rows:
 // the two then wait for each other), persistent CTAs (3.6 to 3.8), 8 softmax
 // warps of 64 columns (the same).
-#include "h3_device.cuh"
+#include "attention_device.cuh"
 #include "h3_internal.h"
 
 #include <cmath>
@@ -68,75 +68,6 @@ constexpr int AB_ROWVALS = 2 * 128 * 4;      // a tile's log-sum-exp (base 2) an
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_A1 = 256, TM_A2 = 384, TM_Q = 384, TM_DS = 448;   // TMEM columns
 constexpr int AB_SMEM = AB_TILE * (2 + AB_ST1 + AB_ST2) + 2 * AB_ROWVALS + 256;
 
-__device__ __forceinline__ float ab_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// The MMA warp runs its loop converged, and one lane (`one` != 0) issues.  With
-// one lane's branch around the loop instead, a product took about 800 cycles, not
-// 600-640, and 8192 rows x 56 heads 4.5 ms, not 3.5.
-// Four K steps of 16.  Operand steps are immediate: SA, SB in descriptor units
-// of 16 bytes (shared memory) or TMEM columns.
-template <int SA, int SB>
-__device__ __forceinline__ void ab_mma4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\t"
-      "add.s64 a2, a1, %6;\n\tadd.s64 b2, b1, %7;\n\t"
-      "add.s64 a3, a2, %6;\n\tadd.s64 b3, b2, %7;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one), "n"(SA), "n"(SB)
-      : "memory");
-}
-template <int SA, int SB>
-__device__ __forceinline__ void ab_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "add.s32 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\t"
-      "add.s32 a2, a1, %6;\n\tadd.s64 b2, b1, %7;\n\t"
-      "add.s32 a3, a2, %6;\n\tadd.s64 b3, b2, %7;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one), "n"(SA), "n"(SB)
-      : "memory");
-}
-__device__ __forceinline__ void ab_commit(uint64_t* bar, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
-      "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ uint32_t ab_elect() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(one));
-  return one;
-}
-__device__ __forceinline__ void ab_tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // Eight packed columns to TMEM, then this warp's arrival at the barrier that the
 // MMA warp waits on.
 __device__ __forceinline__ void ab_hand_over(uint32_t taddr, const uint32_t* r, uint64_t* bar, int lane) {
@@ -147,17 +78,6 @@ __device__ __forceinline__ void ab_hand_over(uint32_t taddr, const uint32_t* r, 
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-__device__ __forceinline__ void ab_drain(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > kWaitLimitNs) return;
-  }
-}
-// A whole warp's wait: one outcome for all lanes, so that a wait that runs out
-// leaves no lane behind.
-__device__ __forceinline__ bool ab_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, c));
 }
 __device__ __forceinline__ void ab_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -297,48 +217,84 @@ __device__ __forceinline__ void ab_own_rows(const AttnBwdArgs& a, const AbSmem& 
   }
 }
 
-// One CTA's work: KEYS = true computes dK and dV of key tile `tile`, false dQ
-// of query tile `tile`.  OWN = true: at most two tiles, and the CTA computes
-// their row values itself.
-template <bool KEYS, bool OWN>
+// The streamed tiles of a CTA's steps.  Without a window all tiles of its head,
+// in order.  With one, the key side takes the query tiles [lo, lo + per) that see
+// its keys, of each head that shares them; the query side the first `sink` key
+// tiles, then those from lo on.
+template <bool KEYS, bool WIN>
+struct AbSteps {
+  int n, lo, per, sink, head0;
+  __device__ __forceinline__ AbSteps(const AttnBwdArgs& a, int tile, int head) {
+    n = a.tiles;
+    lo = sink = 0;
+    per = n;
+    head0 = head;
+    if (!WIN) return;
+    const int first = tile * 128, last = min(first + 128, a.S) - 1;
+    if (KEYS) {
+      lo = win_row_lo(a.w, first, a.S) >> 7;
+      per = ((max(win_row_hi(a.w, first, a.S), win_row_hi(a.w, last, a.S)) + 127) >> 7) - lo;
+      head0 = head * a.G;
+      n = per * a.G;
+    } else {
+      lo = win_lo(a.w, first, a.S) >> 7;
+      sink = min((min(a.w.first, win_lo(a.w, last, a.S)) + 127) >> 7, lo);
+      n = sink + ((win_hi(a.w, last, a.S) + 127) >> 7) - lo;
+      head0 = head / a.G;
+    }
+  }
+  __device__ __forceinline__ int tile(int j) const {
+    if (!WIN) return j;
+    if (KEYS) return lo + j % per;
+    return j < sink ? j : lo + j - sink;
+  }
+  __device__ __forceinline__ int head(int j) const { return WIN && KEYS ? head0 + j / per : head0; }
+};
+
+// One CTA's work: KEYS = true computes dK and dV of key tile `tile` of (KV) head
+// `head`, false dQ of query tile `tile`.  OWN = true: at most two tiles, and the
+// CTA computes their row values itself.  WIN = true: with a window and, where
+// query heads share a KV head, over all of them on the key side.
+template <bool KEYS, bool OWN, bool WIN>
 __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorMap* tmF2, const CUtensorMap* tmG1,
                                         const CUtensorMap* tmG2, const AttnBwdArgs& a, const AbSmem& sm,
                                         uint32_t tmem_base, int tile, int head, const WaitCtl& ctl) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = a.tiles;
+  const AbSteps<KEYS, WIN> steps(a, tile, head);
+  const int n = steps.n;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       bool ok = true;
       int i1 = 0, i2 = 0;
-      auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int t) {
-        tma_load_3d(dst, tm, bar, 0, head, t * 128);
-        tma_load_3d(dst + AB_BOX, tm, bar, 64, head, t * 128);
+      auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int h, int t) {
+        tma_load_3d(dst, tm, bar, 0, h, t * 128);
+        tma_load_3d(dst + AB_BOX, tm, bar, 64, h, t * 128);
       };
       mbar_arrive_expect_tx(sm.f1_full, AB_TILE);
-      load(sm.f1, tmF1, sm.f1_full, tile);
+      load(sm.f1, tmF1, sm.f1_full, head, tile);
       for (int j = 0; j < n && ok; ++j) {
         const int s1 = j % AB_ST1, s2 = j % AB_ST2;
         if (!mbar_wait(&sm.g1_empty[s1], ((uint32_t)(j / AB_ST1) & 1u) ^ 1u, ctl)) { ok = false; break; }
         mbar_arrive_expect_tx(&sm.g1_full[s1], AB_TILE);
-        load(sm.g1 + s1 * AB_TILE, tmG1, &sm.g1_full[s1], j);
+        load(sm.g1 + s1 * AB_TILE, tmG1, &sm.g1_full[s1], steps.head(j), steps.tile(j));
         ++i1;
         if (j == 0) {
           mbar_arrive_expect_tx(sm.f2_full, AB_TILE);
-          load(sm.f2, tmF2, sm.f2_full, tile);
+          load(sm.f2, tmF2, sm.f2_full, head, tile);
         }
         if (!mbar_wait(&sm.g2_empty[s2], ((uint32_t)(j / AB_ST2) & 1u) ^ 1u, ctl)) { ok = false; break; }
         mbar_arrive_expect_tx(&sm.g2_full[s2], AB_TILE);
-        load(sm.g2 + s2 * AB_TILE, tmG2, &sm.g2_full[s2], j);
+        load(sm.g2 + s2 * AB_TILE, tmG2, &sm.g2_full[s2], steps.head(j), steps.tile(j));
         ++i2;
       }
       if (!ok) {  // let issued loads land before the CTA exits
-        ab_drain(sm.f1_full, 0);
-        if (i1 > 0) ab_drain(sm.f2_full, 0);
+        at_drain(sm.f1_full, 0);
+        if (i1 > 0) at_drain(sm.f2_full, 0);
         for (int j = (i1 > AB_ST1 ? i1 - AB_ST1 : 0); j < i1; ++j)
-          ab_drain(&sm.g1_full[j % AB_ST1], (uint32_t)(j / AB_ST1) & 1u);
+          at_drain(&sm.g1_full[j % AB_ST1], (uint32_t)(j / AB_ST1) & 1u);
         for (int j = (i2 > AB_ST2 ? i2 - AB_ST2 : 0); j < i2; ++j)
-          ab_drain(&sm.g2_full[j % AB_ST2], (uint32_t)(j / AB_ST2) & 1u);
+          at_drain(&sm.g2_full[j % AB_ST2], (uint32_t)(j / AB_ST2) & 1u);
       }
     }
     __syncwarp();
@@ -350,12 +306,12 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       for (int j = 0; j < n; ++j) {
         if (!mbar_wait(&sm.rv_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, ctl)) { ok = false; break; }
         mbar_arrive_expect_tx(&sm.rv_full[j & 1], AB_ROWVALS);
-        ab_bulk_load(sm.rowvals + (j & 1) * AB_ROWVALS, a.rowvals + ((size_t)head * n + j) * 256, AB_ROWVALS,
+        ab_bulk_load(sm.rowvals + (j & 1) * AB_ROWVALS, a.rowvals + ((size_t)steps.head(j) * a.tiles + steps.tile(j)) * 256, AB_ROWVALS,
                      &sm.rv_full[j & 1]);
         ++i;
       }
       if (!ok)
-        for (int j = (i > 2 ? i - 2 : 0); j < i; ++j) ab_drain(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u);
+        for (int j = (i > 2 ? i - 2 : 0); j < i; ++j) at_drain(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -363,50 +319,50 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
     constexpr uint32_t idesc_a = idesc_bf16(128, 128, false, true);   // G1, G2 MN-major
     constexpr uint64_t kTile = AB_TILE >> 4, kBox = AB_BOX >> 4;      // descriptor address steps
-    const uint32_t one = ab_elect();
+    const uint32_t one = at_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     const uint64_t f1 = sdesc_kmajor(smem_u32(sm.f1)), f2 = sdesc_kmajor(smem_u32(sm.f2));
     const uint64_t g1k = sdesc_kmajor(smem_u32(sm.g1)), g2k = sdesc_kmajor(smem_u32(sm.g2));
     const uint64_t g1m = sdesc_sw128(smem_u32(sm.g1), AB_BOX, 1024), g2m = sdesc_sw128(smem_u32(sm.g2), AB_BOX, 1024);
     auto issue_ss = [&](uint32_t d, uint64_t f, uint64_t g) {   // F G^T: two 64-channel boxes
-      ab_mma4_ss<2, 2>(tm + d, f, g, idesc_s, 0u, one);
-      ab_mma4_ss<2, 2>(tm + d, f + kBox, g + kBox, idesc_s, 1u, one);
+      at_mma4_ss<2, 2>(tm + d, f, g, idesc_s, 0u, one);
+      at_mma4_ss<2, 2>(tm + d, f + kBox, g + kBox, idesc_s, 1u, one);
     };
     auto issue_q = [&](uint32_t d, uint64_t g) {                // Q in TMEM times G^T
-      ab_mma4_ts<8, 2>(tm + d, tm + TM_Q, g, idesc_s, 0u, one);
-      ab_mma4_ts<8, 2>(tm + d, tm + TM_Q + 32u, g + kBox, idesc_s, 1u, one);
+      at_mma4_ts<8, 2>(tm + d, tm + TM_Q, g, idesc_s, 0u, one);
+      at_mma4_ts<8, 2>(tm + d, tm + TM_Q + 32u, g + kBox, idesc_s, 1u, one);
     };
     // accumulator += A G, A bf16 in TMEM.  Key side, half h: the first or
     // second 16 of each warpgroup's 32 columns, 8 packed ones at 32 w + 8 h.
     auto issue_half = [&](uint32_t d, uint32_t s, uint64_t g, int h, uint32_t accumulate) {
-      ab_mma4_ts<32, 256>(tm + d, tm + s + (uint32_t)(8 * h), g + (uint64_t)(128 * h), idesc_a, accumulate, one);
+      at_mma4_ts<32, 256>(tm + d, tm + s + (uint32_t)(8 * h), g + (uint64_t)(128 * h), idesc_a, accumulate, one);
     };
     auto issue_ds = [&](uint64_t g, uint32_t accumulate) {      // query side: 64 packed columns in a row
-      ab_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS, g, idesc_a, accumulate, one);
-      ab_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS + 32u, g + 512u, idesc_a, 1u, one);
+      at_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS, g, idesc_a, accumulate, one);
+      at_mma4_ts<8, 128>(tm + TM_A1, tm + TM_DS + 32u, g + 512u, idesc_a, 1u, one);
     };
     // S and dP of the next tile: stages and phases of the rings go round here
     uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;   // the next tile's stage and phase in each ring
     auto issue_s = [&]() -> bool {
-      if (!ab_wait(&sm.g1_full[s1], p1, ctl)) return false;
+      if (!at_wait(&sm.g1_full[s1], p1, ctl)) return false;
       tc_fence_after();
       if (KEYS) issue_ss(TM_S, f1, g1k + s1 * kTile);
       else issue_q(TM_S, g1k + s1 * kTile);
-      ab_commit(sm.s_full, one);
+      at_commit(sm.s_full, one);
       if (++s1 == AB_ST1) { s1 = 0; p1 ^= 1u; }
       return true;
     };
     auto issue_dp = [&]() -> bool {
-      if (!ab_wait(&sm.g2_full[s2], p2, ctl)) return false;
+      if (!at_wait(&sm.g2_full[s2], p2, ctl)) return false;
       tc_fence_after();
       issue_ss(TM_DP, f2, g2k + s2 * kTile);
-      if (!KEYS) ab_commit(&sm.g2_empty[s2], one);
-      ab_commit(sm.dp_full, one);
+      if (!KEYS) at_commit(&sm.g2_empty[s2], one);
+      at_commit(sm.dp_full, one);
       if (++s2 == AB_ST2) { s2 = 0; p2 ^= 1u; }
       return true;
     };
-    bool ok = ab_wait(KEYS ? sm.f1_full : sm.f_full, 0, ctl);
-    if (ok) ok = issue_s() && ab_wait(sm.f2_full, 0, ctl) && issue_dp();
+    bool ok = at_wait(KEYS ? sm.f1_full : sm.f_full, 0, ctl);
+    if (ok) ok = issue_s() && at_wait(sm.f2_full, 0, ctl) && issue_dp();
     uint32_t c1 = 0, c2 = 0;                   // this tile's stages
     for (int j = 0; j < n && ok; ++j) {
       const bool more = j + 1 < n;
@@ -414,39 +370,39 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       if (KEYS) {
         // A2 += P G2 in the halves that the softmax hands over, then the next
         // S over P
-        if (!ab_wait(&sm.p_full[0], ph, ctl)) { ok = false; break; }
+        if (!at_wait(&sm.p_full[0], ph, ctl)) { ok = false; break; }
         tc_fence_after();
         issue_half(TM_A2, TM_S, g2m + c2 * kTile, 0, accumulate);
-        if (!ab_wait(&sm.p_full[1], ph, ctl)) { ok = false; break; }
+        if (!at_wait(&sm.p_full[1], ph, ctl)) { ok = false; break; }
         tc_fence_after();
         issue_half(TM_A2, TM_S, g2m + c2 * kTile, 1, 1u);
-        ab_commit(&sm.g2_empty[c2], one);
+        at_commit(&sm.g2_empty[c2], one);
         if (more && !issue_s()) { ok = false; break; }
       } else if (more) {
         // S (and dP) of the next tile as soon as the softmax holds this one's
-        if (!ab_wait(sm.s_empty, ph, ctl) || !issue_s()) { ok = false; break; }
-        if (!ab_wait(sm.dp_empty, ph, ctl) || !issue_dp()) { ok = false; break; }
+        if (!at_wait(sm.s_empty, ph, ctl) || !issue_s()) { ok = false; break; }
+        if (!at_wait(sm.dp_empty, ph, ctl) || !issue_dp()) { ok = false; break; }
       }
-      if (!ab_wait(&sm.ds_full[0], ph, ctl)) { ok = false; break; }
+      if (!at_wait(&sm.ds_full[0], ph, ctl)) { ok = false; break; }
       tc_fence_after();
       if (KEYS) {
         issue_half(TM_A1, TM_DP, g1m + c1 * kTile, 0, accumulate);
-        if (!ab_wait(&sm.ds_full[1], ph, ctl)) { ok = false; break; }
+        if (!at_wait(&sm.ds_full[1], ph, ctl)) { ok = false; break; }
         tc_fence_after();
         issue_half(TM_A1, TM_DP, g1m + c1 * kTile, 1, 1u);
       } else {
         issue_ds(g1m + c1 * kTile, accumulate);
       }
-      ab_commit(&sm.g1_empty[c1], one);
-      if (!KEYS) ab_commit(sm.ds_empty, one);
+      at_commit(&sm.g1_empty[c1], one);
+      if (!KEYS) at_commit(sm.ds_empty, one);
       if (KEYS && more && !issue_dp()) { ok = false; break; }
-      if (!more) ab_commit(sm.acc_full, one);
+      if (!more) at_commit(sm.acc_full, one);
       if (++c1 == AB_ST1) c1 = 0;
       if (++c2 == AB_ST2) c2 = 0;
     }
     if (!ok) {
-      ab_commit(sm.drain, one);
-      if (one) ab_drain(sm.drain, 0);
+      at_commit(sm.drain, one);
+      if (one) at_drain(sm.drain, 0);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -467,7 +423,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       asm volatile("bar.sync 1, %0;" ::"n"(32 * AB_WARPS) : "memory");
     }
     if (!KEYS) {
-      const float* rv = a.rowvals + ((size_t)head * n + tile) * 256 + row;
+      const float* rv = a.rowvals + ((size_t)head * a.tiles + tile) * 256 + row;
       if (OWN) {
         my_l2 = reinterpret_cast<const float*>(sm.rowvals)[row];
         my_d = reinterpret_cast<const float*>(sm.rowvals)[128 + row];
@@ -477,7 +433,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       }
       // Q from its tile into TMEM, where it is the left operand of every S:
       // warpgroup w takes channels [32 w, 32 w + 32) of the row
-      ok = ab_wait(sm.f1_full, 0, ctl);
+      ok = at_wait(sm.f1_full, 0, ctl);
       if (ok) {
         uint32_t pk[16];
 #pragma unroll
@@ -489,22 +445,46 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
           pk[4 * c + 2] = v.z;
           pk[4 * c + 3] = v.w;
         }
-        ab_tmem_st16(tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_Q + (uint32_t)(wg * 16)), pk);
+        at_tmem_st16(tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_Q + (uint32_t)(wg * 16)), pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.f_full);
       }
     }
+    // what this thread's key (or query) sees: [see_lo, see_hi) and [0, see_first)
+    int see_lo = 0, see_hi = 0, see_first = 0;
+    if (WIN) {
+      const int at = min(tile * 128 + row, a.S - 1);
+      see_lo = KEYS ? win_row_lo(a.w, at, a.S) : win_lo(a.w, at, a.S);
+      see_hi = KEYS ? win_row_hi(a.w, at, a.S) : win_hi(a.w, at, a.S);
+      if (!KEYS) see_first = min(a.w.first, see_hi);
+    }
+    int at_tile = steps.tile(0);   // the tile of step j, without a division each
     for (int j = 0; j < n && ok; ++j) {
       const uint32_t ph = (uint32_t)j & 1u;
       const float* rv = reinterpret_cast<const float*>(sm.rowvals + (j & 1) * AB_ROWVALS) + wg * 32;
-      if (KEYS && !OWN && !ab_wait(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl)) { ok = false; break; }
-      if (!ab_wait(sm.s_full, ph, ctl)) { ok = false; break; }
+      if (KEYS && !OWN && !at_wait(&sm.rv_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl)) { ok = false; break; }
+      if (!at_wait(sm.s_full, ph, ctl)) { ok = false; break; }
       tc_fence_after();
       uint32_t p[32], pk[16];
       tmem_ld32(s_base, p);
       tmem_ld_wait(p);
+      if (WIN) {
+        const int c0 = at_tile * 128 + wg * 32;
+        const uint32_t see = (win_bits(see_hi - c0) & ~win_bits(see_lo - c0)) | win_bits(see_first - c0);
+        if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((see >> c) & 1u)) p[c] = __float_as_uint(-INFINITY);
+        }
+        ++at_tile;
+        if (KEYS) {
+          if (at_tile == steps.lo + steps.per) at_tile = steps.lo;
+        } else if (j + 1 == steps.sink) {
+          at_tile = steps.lo;
+        }
+      }
       if (!KEYS) {
         tc_fence_before();
         __syncwarp();
@@ -520,7 +500,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
                                        make_float2(-l.x, -l.y));
           const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(p[c + 2]), __uint_as_float(p[c + 3])), sl2,
                                        make_float2(-l.z, -l.w));
-          const float e0 = ab_ex2(z0.x), e1 = ab_ex2(z0.y), e2 = ab_ex2(z1.x), e3 = ab_ex2(z1.y);
+          const float e0 = at_ex2(z0.x), e1 = at_ex2(z0.y), e2 = at_ex2(z1.x), e3 = at_ex2(z1.y);
           p[c] = __float_as_uint(e0);
           p[c + 1] = __float_as_uint(e1);
           p[c + 2] = __float_as_uint(e2);
@@ -532,7 +512,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
         }
         if (KEYS) ab_hand_over(s_base + (uint32_t)(8 * h), &pk[8 * h], &sm.p_full[h], lane);
       }
-      if (!KEYS && j == n - 1) {
+      if (!KEYS && !WIN && j == n - 1) {
         // keys past the end: their K rows are zero, but exp(-lse) times 0
         // must not become NaN where lse is far below 0
         const int valid = a.S - j * 128 - wg * 32;
@@ -540,7 +520,7 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
         for (int c = 0; c < 32; ++c)
           if (c >= valid) p[c] = 0u;
       }
-      if (!ab_wait(sm.dp_full, ph, ctl)) { ok = false; break; }
+      if (!at_wait(sm.dp_full, ph, ctl)) { ok = false; break; }
       tc_fence_after();
       uint32_t d[32];
       tmem_ld32(dp_base, d);
@@ -570,31 +550,31 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       if (KEYS) {
         if (lane == 0) mbar_arrive(&sm.rv_empty[j & 1]);
       } else {   // once the previous dS has been read
-        if (!ab_wait(sm.ds_empty, ph ^ 1u, ctl)) { ok = false; break; }
+        if (!at_wait(sm.ds_empty, ph ^ 1u, ctl)) { ok = false; break; }
         tc_fence_after();
-        ab_tmem_st16(ds_base, pk);
+        at_tmem_st16(ds_base, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ds_full[0]);
       }
     }
-    if (ok && ab_wait(sm.acc_full, 0, ctl)) {
+    if (ok && at_wait(sm.acc_full, 0, ctl)) {
       tc_fence_after();
       // the accumulators leave through the G rings, idle now (acc_full covers
       // every MMA, and every load has been consumed by one)
       uint8_t* stg = sm.g1 + (warp - 4) * 4096;
       const int row0 = tile * 128 + qq * 32;
       const uint32_t acc = tmem_addr(tmem_base, (uint32_t)(qq * 32), TM_A1);
-      const int64_t at_head = head * a.d_head_stride;
+      const int64_t at_head = head * (KEYS ? a.dkv_head_stride : a.d_head_stride);
       if (KEYS) {
         const int half = (wg & 1) * 64;
         if (wg < 2)
           ab_store<64>(acc + (TM_A2 - TM_A1) + (uint32_t)half, 1.0f, stg, lane, row0, a.S, a.dv + at_head + half,
-                       a.d_row_stride, a.dv, a.d_elems, a.err);
+                       a.dkv_row_stride, a.dv, a.dkv_elems, a.err);
         else
-          ab_store<64>(acc + (uint32_t)half, a.scale, stg, lane, row0, a.S, a.dk + at_head + half, a.d_row_stride,
-                       a.dk, a.d_elems, a.err);
+          ab_store<64>(acc + (uint32_t)half, a.scale, stg, lane, row0, a.S, a.dk + at_head + half, a.dkv_row_stride,
+                       a.dk, a.dkv_elems, a.err);
       } else {
         ab_store<32>(acc + (uint32_t)(wg * 32), a.scale, stg, lane, row0, a.S, a.dq + at_head + wg * 32,
                      a.d_row_stride, a.dq, a.d_elems, a.err);
@@ -605,8 +585,9 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
 }  // namespace
 
 // blockIdx.x: 128-row tile, blockIdx.y: head; z = 0 the key side, z = 1 the
-// query side (the longer key-side CTAs are scheduled first).
-template <bool OWN>
+// query side (the longer key-side CTAs are scheduled first).  WIN: z = 0, and y
+// counts the KV heads of the key side, then the query heads.
+template <bool OWN, bool WIN>
 __global__ void __launch_bounds__(AB_THREADS, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -694,10 +675,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   // a wait of an earlier launch ran out: this launch skips its work, before
   // any copy or MMA is issued
   if (OWN ? skip == 0 : *ctl.flag == 0) {
-    if (blockIdx.z == 0)
-      ab_tile<true, OWN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
-    else
-      ab_tile<false, OWN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
+    const int kv_heads = WIN ? args.H / args.G : 0;
+    const bool keys = WIN ? (int)blockIdx.y < kv_heads : blockIdx.z == 0;
+    const int head = WIN && !keys ? (int)blockIdx.y - kv_heads : (int)blockIdx.y;
+    if (keys) ab_tile<true, OWN, WIN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, head, ctl);
+    else ab_tile<false, OWN, WIN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, head, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -722,7 +704,7 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   cudaError_t e = cudaSuccess;
   if (!own) e = launch_kernel(attention_bwd_rows_kernel, rows_grid, dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
-  const auto kernel = own ? attention_bwd_kernel<true> : attention_bwd_kernel<false>;
+  const auto kernel = own ? attention_bwd_kernel<true, false> : attention_bwd_kernel<false, false>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
@@ -730,6 +712,23 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   set_kernel_info("attention_bwd_kernel tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d,%d acc=f32 "
                   "P,dS-in-TMEM grid=%ux%ux2%s",
                   AB_ST1, AB_ST2, grid.x, grid.y, own ? " own-row-values" : "");
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                        const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream) {
+  if (!tmem_exclusive(AB_SMEM)) return cudaErrorNotSupported;
+  const dim3 rows_grid((unsigned)a.tiles, (unsigned)a.H), grid((unsigned)a.tiles, (unsigned)(a.H / a.G + a.H));
+  cudaError_t e = launch_kernel(attention_bwd_rows_kernel, rows_grid, dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  const auto kernel = attention_bwd_kernel<false, true>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
+  if (e != cudaSuccess) return e;
+  set_kernel_info("attention_bwd_kernel<window> tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d,%d acc=f32 "
+                  "P,dS-in-TMEM shared=%d grid=%ux%u",
+                  AB_ST1, AB_ST2, a.G, grid.x, grid.y);
   return cudaGetLastError();
 }
 

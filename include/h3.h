@@ -364,6 +364,137 @@ h3_status h3_attention_backward(int32_t n_rows, int32_t n_heads, const void *q, 
                                 void *dv, int64_t d_row_stride_elems, int64_t d_head_stride_elems,
                                 void *workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ----------------------------------------------------------------------- */
+/* Attention in windows, and a paged cache of keys and values               */
+/* (operators of a user who generates or trains long clips frame by frame;  */
+/* the pages have no counterpart: the released path attends without a mask) */
+/* ----------------------------------------------------------------------- */
+
+/* What a row sees.  Rows are counted in units (1, or the rows of a frame):
+ * unit(i) = floor((i - origin) / unit), rows before origin in units of their
+ * own.  Row i sees key j if
+ *   unit(j) <= unit(i) + right                 (right = -1: no such bound) and
+ *   unit(j) >= unit(i) - left or j < n_first   (left = -1: no such bound),
+ * so every row sees itself.  left, right >= -1, n_first, origin >= 0,
+ * unit >= 1 (H3_ERR_SHAPE). */
+typedef struct {
+  int32_t left, right;   /* units before and after the row's own */
+  int32_t n_first;       /* first keys that stay visible */
+  int32_t unit, origin;
+} h3_window;
+
+/* h3_attention with a window, n_heads query heads over n_kv_heads key and value
+ * heads (head h reads head h / (n_heads / n_kv_heads); n_heads a multiple of
+ * n_kv_heads, at most 128 times it): o[i][h*128 + c] = bf16(sum over the visible
+ * j of P_ij v[j][.][c]), P the softmax of q_i . k_j / sqrt(128) over them.
+ * Element (row i, head h, channel c) at ptr + i*row_stride + h*head_stride + c,
+ * q with strides of its own, k and v with common ones (in elements, multiples of
+ * 8; those of one row or one head are not looked at).  o bf16 [n_rows]
+ * [n_heads*128], lse_opt NULL or fp32 [n_heads][n_rows] as for h3_attention;
+ * neither may overlap an input.  A non-finite k or v of a row makes the results of the rows
+ * near it that see its 128-row tile undefined, as well as of those that see it.
+ * Only tiles that some row sees are read.  Up to 2^24 rows and 32767 heads
+ * (H3_ERR_UNSUPPORTED).  The key tiles are split over the SMs, so the result is
+ * bitwise repeatable on a given GPU, but the order of its sums follows the row
+ * count.  workspace: device, 256-byte aligned, at least
+ * h3_attention_window_workspace_bytes (0 for invalid sizes) on the device that
+ * runs the call; scratch of one call. */
+size_t h3_attention_window_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads);
+h3_status h3_attention_window(const h3_window *window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                              const void *q, int64_t q_row_stride_elems, int64_t q_head_stride_elems,
+                              const void *k, const void *v, int64_t kv_row_stride_elems,
+                              int64_t kv_head_stride_elems, void *o, float *lse_opt, void *workspace,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* Gradient of h3_attention_window, as h3_attention_backward is that of
+ * h3_attention: q, k, v and strides as given to the forward call, o its output,
+ * lse its log-sum-exp, d_o the gradient of o (bf16 [n_rows][n_heads*128]).  dk
+ * and dv are summed over the heads that share them, in fp32.  dq and dk, dv have
+ * strides of their own (multiples of 8; rows that hold their heads or heads that
+ * hold their rows, else H3_ERR_SHAPE) and overlap neither each other nor an
+ * input.  Bitwise repeatable: no atomics.  workspace: as
+ * h3_attention_backward's. */
+size_t h3_attention_window_backward_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads);
+h3_status h3_attention_window_backward(const h3_window *window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                                       const void *q, int64_t q_row_stride_elems, int64_t q_head_stride_elems,
+                                       const void *k, const void *v, int64_t kv_row_stride_elems,
+                                       int64_t kv_head_stride_elems, const void *o, const void *d_o,
+                                       const float *lse, void *dq, int64_t dq_row_stride_elems,
+                                       int64_t dq_head_stride_elems, void *dk, void *dv,
+                                       int64_t dkv_row_stride_elems, int64_t dkv_head_stride_elems,
+                                       void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Keys and values of n_seqs sequences in pages of one pool.  Slot t of sequence
+ * s is row t % page_size of page table[s][t / page_size]; length[s] slots are in
+ * use.  The page pools are bf16 [n_pages][n_kv_heads][page_size][128]; page_size
+ * 16, 32, 64, 128 or 256.  At most 1024 sequences and heads, and 2^24 slots in a
+ * table's width (H3_ERR_UNSUPPORTED).  table and length are read on the device
+ * when a call runs, so a captured call follows them.  A length above the table's
+ * width or below the sequence's new rows, a seq_start that decreases or leaves
+ * [0, n_rows], and a page that a row needs outside [0, n_pages) are reported
+ * (H3_ERR_INDEX from h3_sync_check): such a sequence's results are left as they
+ * were or, for a page, undefined; nothing outside the buffers is read or written. */
+typedef struct {
+  void *k, *v;               /* device page pools */
+  int32_t n_pages, page_size, n_kv_heads;
+  int32_t n_seqs, table_width;
+  const int32_t *table;      /* device [n_seqs][table_width] */
+  const int32_t *length;     /* device [n_seqs] */
+} h3_cache;
+
+/* Writes new rows into the cache: rows [seq_start[s], seq_start[s+1]) of k and v
+ * (n_rows rows in all, device int32 seq_start [n_seqs+1]) are the last slots of
+ * sequence s, length[s] - (seq_start[s+1] - seq_start[s]) and on: length counts
+ * them already.  k and v bf16, element (row i, head h, channel c) at ptr +
+ * i*row_stride + h*head_stride + c (strides multiples of 8).  weights_opt: NULL or
+ * the sums of h3_cache_weights, zeroed for these slots.  Rows of no sequence are
+ * not read. */
+h3_status h3_cache_append(const h3_cache *cache, int32_t n_rows, const int32_t *seq_start, const void *k,
+                          const void *v, int64_t row_stride_elems, int64_t head_stride_elems, float *weights_opt,
+                          cudaStream_t stream);
+
+/* Attention of new rows over the cache that holds them (after h3_cache_append),
+ * single rows or chunks of any length, every sequence its own: new row r of
+ * sequence s stands at slot length[s] - (seq_start[s+1] - seq_start[s]) + r and
+ * sees the slots that the window gives, as in h3_attention_window.  q and its
+ * heads as there; o bf16 [n_rows][n_heads*128], lse_opt NULL or fp32
+ * [n_heads][n_rows]; rows of no sequence are left as they were.  Pages none of whose slots a
+ * new row sees are not looked at (a window's old pages may be given back), nor is what
+ * the pages hold past a sequence's last slot.  workspace: device, 256-byte
+ * aligned, at least h3_attention_cached_workspace_bytes (0 for invalid
+ * arguments); scratch of one call. */
+size_t h3_attention_cached_workspace_bytes(const h3_cache *cache, int32_t n_rows, int32_t n_heads);
+h3_status h3_attention_cached(const h3_cache *cache, const h3_window *window, int32_t n_rows, int32_t n_heads,
+                              const int32_t *seq_start, const void *q, int64_t q_row_stride_elems,
+                              int64_t q_head_stride_elems, void *o, float *lse_opt, void *workspace,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* Attention weight that each cached row collected: for every slot of every
+ * sequence, weights_out = weights_in + sum over its new rows and the heads that
+ * share the KV head of exp(q_i . k_j / sqrt(128) - lse_i), visible ones.  Rows,
+ * window and q as for h3_attention_cached, lse [n_heads][n_rows] as that call
+ * left it.  weights fp32 [n_pages][n_kv_heads][page_size]; weights_in NULL: 0, or
+ * weights_out itself.  Slots of no sequence are left as they were.  Bitwise
+ * repeatable: no atomics. */
+h3_status h3_cache_weights(const h3_cache *cache, const h3_window *window, int32_t n_rows, int32_t n_heads,
+                           const int32_t *seq_start, const void *q, int64_t q_row_stride_elems,
+                           int64_t q_head_stride_elems, const float *lse, const float *weights_in_opt,
+                           float *weights_out, cudaStream_t stream);
+
+/* Cuts every sequence and head of `from` to at most `budget` slots: those of a
+ * sequence of more are its first n_first, its last n_recent and, of the others,
+ * the ones of the largest weight (the earlier of equal ones; a NaN counts as the
+ * least).  They keep their order, which is that of their new slots 0, 1, ...; K,
+ * V and, with weights_to, the weights move to the pages of `to` (pages that `from`
+ * does not use: the two may lie in one pool).  Shorter sequences move whole.
+ * kept int32 [n_seqs][n_kv_heads][budget] receives the slots, -1 behind the last;
+ * length_out [n_seqs] the new lengths (it may be to->length, which is not read,
+ * and is not from->length).  The two caches have the same heads and sequences;
+ * n_first + n_recent <= budget (H3_ERR_SHAPE). */
+h3_status h3_cache_evict(const h3_cache *from, const h3_cache *to, int32_t budget, int32_t n_first,
+                         int32_t n_recent, const float *weights, float *weights_to_opt, int32_t *kept,
+                         int32_t *length_out, cudaStream_t stream);
+
 /* Element types of the norm and rotary calls below. */
 typedef enum { H3_BF16 = 0, H3_FP32 = 1 } h3_dtype;
 
@@ -663,7 +794,8 @@ h3_status h3_last_kernel_info(char *buf, size_t len);
 /* Where the first device-side wait that ran out was, as recorded on the
  * device and read by the most recent h3_sync_check of this process that
  * returned H3_ERR_TIMEOUT: "none", or the kernel ("gemm", "attention-1q",
- * "attention-2q", "adaln-table", "rope-qknorm", "attention-backward") and the wait (an mbarrier at
+ * "attention-2q", "adaln-table", "rope-qknorm", "attention-backward",
+ * "attention-window", "cache-weights") and the wait (an mbarrier at
  * a shared-memory byte offset, or a stream-K partial-sum flag).  Diagnostic
  * only: the pages define no counterpart.  Writes a NUL-terminated string of
  * at most len bytes; H3_ERR_NULL when buf is NULL or len is 0. */
