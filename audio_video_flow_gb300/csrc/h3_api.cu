@@ -1533,7 +1533,17 @@ h3_status check_window(const h3_window* w) {
   if (w->left < -1 || w->right < -1 || w->n_first < 0 || w->unit < 1 || w->origin < 0) return H3_ERR_SHAPE;
   return H3_OK;
 }
-WindowArgs window_args(const h3_window& w) { return {w.left, w.right, w.n_first, w.unit, w.origin}; }
+// The same window in small numbers: rows and keys are below 2^24, so units of more
+// rows are as good as that long, and the origin counts modulo a unit.
+WindowArgs window_args(const h3_window& w) {
+  constexpr int kFar = 1 << 25;
+  WindowArgs a{w.left < kFar ? w.left : kFar, w.right < kFar ? w.right : kFar, w.n_first, w.unit, w.origin % w.unit};
+  if (a.unit > kCacheMaxRows) {
+    a.unit = kCacheMaxRows;
+    if (a.origin >= kCacheMaxRows) a.origin = 0;
+  }
+  return a;
+}
 
 // Query heads over KV heads of 128 channels: G = n_heads / n_kv_heads share one.
 h3_status check_shared(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
@@ -1569,15 +1579,10 @@ CacheArgs cache_args(const h3_cache& c, const int32_t* start) {
 }
 size_t cache_rows(const h3_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * c.page_size; }
 
-size_t attn_win_ws_bytes(int64_t n_rows, int64_t n_heads, int64_t n_kv_heads, int64_t n_seqs, int64_t max_keys,
-                         int* ctas, size_t* desc, size_t* part_elems) {
-  int rows, slots;
-  const int G = (int)(n_heads / n_kv_heads);
-  *ctas = attn_win_ctas(n_rows, n_kv_heads, n_seqs, G, max_keys);
-  attn_win_part(n_rows, G, &rows, &slots);
-  *desc = attn_win_desc_bytes(*ctas);
-  *part_elems = (size_t)*ctas * slots * rows * 130;
-  return al256(*desc + *part_elems * 4);
+// Bytes that hold for every window.
+size_t attn_win_ws_bytes(int64_t n_rows, int64_t n_heads, int64_t n_kv_heads) {
+  const int G = (int)(n_heads / n_kv_heads), R = 128 / G, ctas = num_sms();
+  return al256(attn_win_ctrl_bytes(ctas) + attn_win_part_bytes(ctas, (int)(n_rows < R ? n_rows : R) * G));
 }
 
 // The call over one document (c null) or a cache, its arguments checked.
@@ -1585,12 +1590,11 @@ h3_status run_attention_window(const h3_window& w, const h3_cache* c, int32_t n_
                                const int32_t* start, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                void* o, float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   AttnWinArgs a{};
-  int ctas = 0;
-  size_t desc = 0;
+  AttnWinPlan p{};
   const int64_t seqs = c ? c->n_seqs : 1, keys = c ? (int64_t)c->table_width * c->page_size : n_rows;
-  if (ws_bytes < attn_win_ws_bytes(n_rows, n_heads, n_kv_heads, seqs, keys, &ctas, &desc, &a.part_elems))
-    return H3_ERR_WORKSPACE;
   a.w = window_args(w);
+  if (!attn_win_plan(&p, n_rows, n_kv_heads, seqs, n_heads / n_kv_heads, keys, c != nullptr, a.w)) return H3_ERR_UNSUPPORTED;
+  if (ws_bytes < attn_win_ws_bytes(n_rows, n_heads, n_kv_heads)) return H3_ERR_WORKSPACE;
   if (c) {
     a.c = cache_args(*c, start);
   } else {
@@ -1603,22 +1607,24 @@ h3_status run_attention_window(const h3_window& w, const h3_cache* c, int32_t n_
   a.R = 128 / a.G;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.desc = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + desc);
-  attn_win_part(n_rows, a.G, &a.part_rows, &a.part_slots);
+  a.ctrl = static_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ctrl_bytes);
+  a.part_rows = p.part_rows;
+  a.part_slots = p.part_slots;
+  a.part_elems = p.part_elems;
+  a.M = p.M;
+  a.U = p.U;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
   a.o_elems = (size_t)n_rows * n_heads * 128;
   a.lse_elems = lse ? (size_t)n_rows * n_heads : 0;
   a.err = device_error_word();
-  return cuda_st(launch_attention_window(tq, tk, tv, a, ctas, stream));
+  return cuda_st(launch_attention_window(tq, tk, tv, a, p, stream));
 }
 }  // namespace
 
 size_t h3_attention_window_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
   if (check_shared(n_rows, n_heads, n_kv_heads) != H3_OK) return 0;
-  int ctas;
-  size_t desc, elems;
-  return attn_win_ws_bytes(n_rows, n_heads, n_kv_heads, 1, n_rows, &ctas, &desc, &elems);
+  return attn_win_ws_bytes(n_rows, n_heads, n_kv_heads);
 }
 
 h3_status h3_attention_window(const h3_window* window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads, const void* q,
@@ -1742,10 +1748,7 @@ h3_status h3_cache_append(const h3_cache* cache, int32_t n_rows, const int32_t* 
 
 size_t h3_attention_cached_workspace_bytes(const h3_cache* cache, int32_t n_rows, int32_t n_heads) {
   if (check_cache(cache) != H3_OK || check_shared(n_rows, n_heads, cache->n_kv_heads) != H3_OK) return 0;
-  int ctas;
-  size_t desc, elems;
-  return attn_win_ws_bytes(n_rows, n_heads, cache->n_kv_heads, cache->n_seqs,
-                           (int64_t)cache->table_width * cache->page_size, &ctas, &desc, &elems);
+  return attn_win_ws_bytes(n_rows, n_heads, cache->n_kv_heads);
 }
 
 h3_status h3_attention_cached(const h3_cache* cache, const h3_window* window, int32_t n_rows, int32_t n_heads,

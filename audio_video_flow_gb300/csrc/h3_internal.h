@@ -284,8 +284,10 @@ cudaError_t launch_attention(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
 // ---------------------------------------------------------------------------
 // attention gradient (tcgen05, k_attention_bwd.cu)
 // ---------------------------------------------------------------------------
+// An h3_window for rows and keys below 2^24: 0 <= origin < unit <= 2^24 (origin 0
+// where unit is 1), left and right at most 2^25.
 struct WindowArgs {
-  int left, right, first, unit, origin;   // as h3_window
+  int left, right, first, unit, origin;
 };
 struct AttnBwdArgs {
   int S, H;
@@ -327,23 +329,29 @@ constexpr int kCacheMaxRows = 1 << 24;    // new rows of a call, and slots of a 
 struct AttnWinArgs {
   WindowArgs w;
   CacheArgs c;
+  int M, U;                   // CTAs of a gang (consecutive ones), rows of a unit
   int n_rows, H, G, R;        // G query heads share a KV head; a 128-row tile holds R rows x G heads
   __nv_bfloat16* o;           // [n_rows][H*128]
   float* lse;                 // [H][n_rows] or null
-  int4* desc;                 // workspace: per CTA the partial tiles that it leaves (AwDesc)
+  int* ctrl;                  // workspace: control words of the CTAs
   float* part;                // workspace: partial results
   int part_rows, part_slots;  // rows of a partial tile, partial tiles per CTA
   float scale_log2;           // log2(e) / sqrt(128)
   size_t o_elems, lse_elems, part_elems;   // extents for the bounds-checked build
   uint32_t* err;
 };
-// CTAs, bytes of workspace and the split into desc and part for a call of
-// n_rows rows of H query heads over KV heads shared by G
-int attn_win_ctas(int64_t n_rows, int64_t kv_heads, int64_t n_seqs, int G, int64_t max_keys);
-size_t attn_win_desc_bytes(int ctas);
-void attn_win_part(int64_t n_rows, int G, int* part_rows, int* part_slots);
+struct AttnWinPlan {
+  int mode, U, M, ctas, split;
+  int part_rows, part_slots;
+  size_t ctrl_bytes, part_elems;
+};
+size_t attn_win_ctrl_bytes(int ctas);
+size_t attn_win_part_bytes(int ctas, int rows);   // at most, for tiles of that many rows
+// False where a call has more than 2^31 pairs of a unit and a key tile.
+bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_seqs, int G, int64_t max_keys, bool paged,
+                   const WindowArgs& w);
 cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    const AttnWinArgs& a, int ctas, cudaStream_t stream);
+                                    const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream);
 
 struct AppendArgs {
   CacheArgs c;
