@@ -111,26 +111,26 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
 // Key j is seen by the rows [win_row_lo, win_row_hi).  Both ends grow with the
 // row or key, so a tile's range runs from its first row's to its last row's.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int win_unit(const WindowArgs& w, int i) {   // -1 for rows before the origin
+__host__ __device__ inline int win_unit(const WindowArgs& w, int i) {   // -1 for rows before the origin
   return w.unit == 1 ? i : (int)((uint32_t)(i - w.origin + w.unit) / (uint32_t)w.unit) - 1;
 }
-__device__ __forceinline__ int win_edge(const WindowArgs& w, int unit, int n) {   // where a unit begins, within [0, n]
+__host__ __device__ inline int win_edge(const WindowArgs& w, int unit, int n) {   // where a unit begins, within [0, n]
   const int64_t x = w.origin + (int64_t)unit * w.unit;
   return x < 0 ? 0 : (x > n ? n : (int)x);
 }
 // of a row in unit u
-__device__ __forceinline__ int win_lo_of(const WindowArgs& w, int u, int keys) {
+__host__ __device__ inline int win_lo_of(const WindowArgs& w, int u, int keys) {
   return w.left < 0 ? 0 : win_edge(w, u - w.left, keys);
 }
-__device__ __forceinline__ int win_hi_of(const WindowArgs& w, int u, int keys) {
+__host__ __device__ inline int win_hi_of(const WindowArgs& w, int u, int keys) {
   return w.right < 0 ? keys : win_edge(w, u + w.right + 1, keys);
 }
-__device__ __forceinline__ int win_lo(const WindowArgs& w, int i, int keys) { return win_lo_of(w, win_unit(w, i), keys); }
-__device__ __forceinline__ int win_hi(const WindowArgs& w, int i, int keys) { return win_hi_of(w, win_unit(w, i), keys); }
-__device__ __forceinline__ int win_row_lo(const WindowArgs& w, int j, int rows) {
+__host__ __device__ inline int win_lo(const WindowArgs& w, int i, int keys) { return win_lo_of(w, win_unit(w, i), keys); }
+__host__ __device__ inline int win_hi(const WindowArgs& w, int i, int keys) { return win_hi_of(w, win_unit(w, i), keys); }
+__host__ __device__ inline int win_row_lo(const WindowArgs& w, int j, int rows) {
   return w.right < 0 ? 0 : win_edge(w, win_unit(w, j) - w.right, rows);
 }
-__device__ __forceinline__ int win_row_hi(const WindowArgs& w, int j, int rows) {
+__host__ __device__ inline int win_row_hi(const WindowArgs& w, int j, int rows) {
   return w.left < 0 || j < w.first ? rows : win_edge(w, win_unit(w, j) + w.left + 1, rows);
 }
 // bits [0, x) of a word

@@ -1614,6 +1614,8 @@ h3_status run_attention_window(const h3_window& w, const h3_cache* c, int32_t n_
   a.part_elems = p.part_elems;
   a.M = p.M;
   a.U = p.U;
+  a.gangs = p.gangs;
+  a.gangs_inv = (uint64_t(1) << 32) / (uint64_t)p.gangs + 1;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
   a.o_elems = (size_t)n_rows * n_heads * 128;
   a.lse_elems = lse ? (size_t)n_rows * n_heads : 0;
@@ -1652,7 +1654,7 @@ h3_status h3_attention_window(const h3_window* window, int32_t n_rows, int32_t n
 
 size_t h3_attention_window_backward_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
   if (check_shared(n_rows, n_heads, n_kv_heads) != H3_OK) return 0;
-  return attn_bwd_ws_bytes(n_rows, n_heads);
+  return attn_bwd_ws_bytes(n_rows, n_heads) + attn_bwd_part_bytes(n_rows, n_heads, n_kv_heads);
 }
 
 h3_status h3_attention_window_backward(const h3_window* window, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
@@ -1676,6 +1678,7 @@ h3_status h3_attention_window_backward(const h3_window* window, int32_t n_rows, 
   if (!apart(n_rows, n_heads, 128, dq_row_stride_elems, dq_head_stride_elems) ||
       !apart(n_rows, n_kv_heads, 128, dkv_row_stride_elems, dkv_head_stride_elems))
     return H3_ERR_SHAPE;
+  if (((int64_t)n_rows + 127) / 128 * n_heads > (int64_t(1) << 29)) return H3_ERR_UNSUPPORTED;
   const void* const in[] = {q, k, v, o, d_o, lse, workspace};
   void* const out[] = {dq, dk, dv};
   for (int i = 0; i < 3; ++i) {
@@ -1684,7 +1687,8 @@ h3_status h3_attention_window_backward(const h3_window* window, int32_t n_rows, 
     for (int j = 0; j < i; ++j)
       if (out[i] == out[j]) return H3_ERR_SHAPE;
   }
-  if (ws_bytes < attn_bwd_ws_bytes(n_rows, n_heads)) return H3_ERR_WORKSPACE;
+  if (ws_bytes < attn_bwd_ws_bytes(n_rows, n_heads) + attn_bwd_part_bytes(n_rows, n_heads, n_kv_heads))
+    return H3_ERR_WORKSPACE;
   CUtensorMap tq, tk, tv, to;
   const uint64_t S = (uint64_t)n_rows, H = (uint64_t)n_heads, Hk = (uint64_t)n_kv_heads;
   if (!make_tmap_qkv(&tq, q, S, H, q_row_stride_elems, q_head_stride_elems, 128) ||
@@ -1702,6 +1706,8 @@ h3_status h3_attention_window_backward(const h3_window* window, int32_t n_rows, 
   a.d_o = static_cast<const __nv_bfloat16*>(d_o);
   a.lse = lse;
   a.rowvals = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_bwd_ws_bytes(n_rows, n_heads));
+  attn_bwd_split(&a);
   a.dq = static_cast<__nv_bfloat16*>(dq);
   a.dk = static_cast<__nv_bfloat16*>(dk);
   a.dv = static_cast<__nv_bfloat16*>(dv);

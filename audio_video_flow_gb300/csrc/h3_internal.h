@@ -291,8 +291,12 @@ struct WindowArgs {
 };
 struct AttnBwdArgs {
   int S, H;
-  WindowArgs w;           // with a window only, as G: query heads that share a KV head
-  int G;
+  // with a window only, as G: query heads that share a KV head; how the key side
+  // is split (attn_bwd_split)
+  WindowArgs w;
+  int G, first_tiles, first_pieces, other_pieces;
+  float* part;            // workspace [KV heads][pieces of split tiles][2][128 channels][128 rows]: dV, dK
+  size_t part_elems;      // for the bounds-checked build
   int tiles;              // 128-row tiles: ceil(S / 128)
   const __nv_bfloat16* o;     // [S][H*128]
   const __nv_bfloat16* d_o;   // [S][H*128]
@@ -309,6 +313,8 @@ struct AttnBwdArgs {
 cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                  const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream);
 // the same with a window and shared KV heads
+void attn_bwd_split(AttnBwdArgs* a);
+size_t attn_bwd_part_bytes(int64_t S, int64_t H, int64_t Hk);
 cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                         const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream);
 
@@ -330,6 +336,8 @@ struct AttnWinArgs {
   WindowArgs w;
   CacheArgs c;
   int M, U;                   // CTAs of a gang (consecutive ones), rows of a unit
+  int gangs;
+  uint64_t gangs_inv;         // 2^32 / gangs + 1
   int n_rows, H, G, R;        // G query heads share a KV head; a 128-row tile holds R rows x G heads
   __nv_bfloat16* o;           // [n_rows][H*128]
   float* lse;                 // [H][n_rows] or null
@@ -341,7 +349,7 @@ struct AttnWinArgs {
   uint32_t* err;
 };
 struct AttnWinPlan {
-  int mode, U, M, ctas, split;
+  int mode, U, M, ctas, gangs, split;
   int part_rows, part_slots;
   size_t ctrl_bytes, part_elems;
 };

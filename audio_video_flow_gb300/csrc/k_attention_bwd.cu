@@ -54,6 +54,7 @@
 #include "attention_device.cuh"
 #include "h3_internal.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace h3 {
@@ -143,6 +144,12 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdAr
 }
 
 namespace {
+// Places for pieces of split key tiles, per KV head.
+__host__ __device__ inline int ab_part_slots(const AttnBwdArgs& a) {
+  return (a.first_pieces > 1 ? a.first_tiles * a.first_pieces : 0) +
+         (a.other_pieces > 1 ? (a.tiles - a.first_tiles) * a.other_pieces : 0);
+}
+
 struct AbSmem {
   uint8_t *f1, *f2, *g1, *g2, *rowvals;
   uint64_t *f1_full, *f2_full, *g1_full, *g1_empty, *g2_full, *g2_empty, *rv_full, *rv_empty;
@@ -184,6 +191,21 @@ __device__ __forceinline__ void ab_store(uint32_t taddr, float scale, uint8_t* s
   }
 }
 
+// The same rows and columns as they are, one row per lane.
+template <int NC>
+__device__ __forceinline__ void ab_store_part(uint32_t taddr, float* to, const AttnBwdArgs& a) {
+#pragma unroll
+  for (int c = 0; c < NC; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(taddr + (uint32_t)c, o);
+    tmem_ld_wait(o);
+    if (in_bounds<float>(a.part, a.part_elems, to + (c + 31) * 128, 1, a.err, 46)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) to[(c + e) * 128] = __uint_as_float(o[e]);
+    }
+  }
+}
+
 // The row values of tile t into slot `slot` of shared memory, by the softmax
 // warps themselves (the same sums as attention_bwd_rows_kernel's).
 __device__ __forceinline__ void ab_own_rows(const AttnBwdArgs& a, const AbSmem& sm, int t, int slot, int head) {
@@ -219,14 +241,14 @@ __device__ __forceinline__ void ab_own_rows(const AttnBwdArgs& a, const AbSmem& 
 
 // The streamed tiles of a CTA's steps.  Without a window all tiles of its head,
 // in order.  With one, the key side takes the query tiles [lo, lo + per) that see
-// its keys, of each head that shares them; the query side the first `sink` key
-// tiles, then those from lo on.
+// its keys, of each head that shares them (or piece `piece` of `pieces` of these
+// steps); the query side the first `sink` key tiles, then those from lo on.
 template <bool KEYS, bool WIN>
 struct AbSteps {
-  int n, lo, per, sink, head0;
-  __device__ __forceinline__ AbSteps(const AttnBwdArgs& a, int tile, int head) {
+  int n, lo, per, sink, head0, from;
+  __device__ __forceinline__ AbSteps(const AttnBwdArgs& a, int tile, int head, int piece, int pieces) {
     n = a.tiles;
-    lo = sink = 0;
+    lo = sink = from = 0;
     per = n;
     head0 = head;
     if (!WIN) return;
@@ -236,6 +258,8 @@ struct AbSteps {
       per = ((max(win_row_hi(a.w, first, a.S), win_row_hi(a.w, last, a.S)) + 127) >> 7) - lo;
       head0 = head * a.G;
       n = per * a.G;
+      from = (int)((int64_t)n * piece / pieces);
+      n = (int)((int64_t)n * (piece + 1) / pieces) - from;
     } else {
       lo = win_lo(a.w, first, a.S) >> 7;
       sink = min((min(a.w.first, win_lo(a.w, last, a.S)) + 127) >> 7, lo);
@@ -245,10 +269,10 @@ struct AbSteps {
   }
   __device__ __forceinline__ int tile(int j) const {
     if (!WIN) return j;
-    if (KEYS) return lo + j % per;
+    if (KEYS) return lo + (from + j) % per;
     return j < sink ? j : lo + j - sink;
   }
-  __device__ __forceinline__ int head(int j) const { return WIN && KEYS ? head0 + j / per : head0; }
+  __device__ __forceinline__ int head(int j) const { return WIN && KEYS ? head0 + (from + j) / per : head0; }
 };
 
 // One CTA's work: KEYS = true computes dK and dV of key tile `tile` of (KV) head
@@ -258,10 +282,17 @@ struct AbSteps {
 template <bool KEYS, bool OWN, bool WIN>
 __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorMap* tmF2, const CUtensorMap* tmG1,
                                         const CUtensorMap* tmG2, const AttnBwdArgs& a, const AbSmem& sm,
-                                        uint32_t tmem_base, int tile, int head, const WaitCtl& ctl) {
+                                        uint32_t tmem_base, int tile, int head, const WaitCtl& ctl, int piece = 0,
+                                        int pieces = 1, int slot = 0) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const AbSteps<KEYS, WIN> steps(a, tile, head);
+  const AbSteps<KEYS, WIN> steps(a, tile, head, piece, pieces);
   const int n = steps.n;
+  if (WIN && KEYS && n == 0) {   // a tile of fewer steps than pieces: this one adds nothing
+    float* to = a.part + (int64_t)slot * 2 * 128 * 128;
+    if (in_bounds<float>(a.part, a.part_elems, to, 2 * 128 * 128, a.err, 46))
+      for (int i = threadIdx.x; i < 2 * 128 * 128; i += AB_THREADS) to[i] = 0.0f;
+    return;
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -569,7 +600,10 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
       const int64_t at_head = head * (KEYS ? a.dkv_head_stride : a.d_head_stride);
       if (KEYS) {
         const int half = (wg & 1) * 64;
-        if (wg < 2)
+        if (WIN && pieces > 1)   // one of several pieces: fp32, [channel][row], dV then dK
+          ab_store_part<64>(acc + (wg < 2 ? TM_A2 - TM_A1 : 0u) + (uint32_t)half,
+                            a.part + ((int64_t)slot * 2 + (wg < 2 ? 0 : 1)) * 128 * 128 + half * 128 + qq * 32 + lane, a);
+        else if (wg < 2)
           ab_store<64>(acc + (TM_A2 - TM_A1) + (uint32_t)half, 1.0f, stg, lane, row0, a.S, a.dv + at_head + half,
                        a.dkv_row_stride, a.dv, a.dkv_elems, a.err);
         else
@@ -585,8 +619,10 @@ __device__ __forceinline__ void ab_tile(const CUtensorMap* tmF1, const CUtensorM
 }  // namespace
 
 // blockIdx.x: 128-row tile, blockIdx.y: head; z = 0 the key side, z = 1 the
-// query side (the longer key-side CTAs are scheduled first).  WIN: z = 0, and y
-// counts the KV heads of the key side, then the query heads.
+// query side (the longer key-side CTAs are scheduled first).  WIN: a line of
+// CTAs, for each KV head the pieces of its key tiles (first_pieces for each of the
+// first_tiles ones, which all rows may see, then other_pieces), then for each
+// query head its tiles.
 template <bool OWN, bool WIN>
 __global__ void __launch_bounds__(AB_THREADS, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -675,11 +711,28 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   // a wait of an earlier launch ran out: this launch skips its work, before
   // any copy or MMA is issued
   if (OWN ? skip == 0 : *ctl.flag == 0) {
-    const int kv_heads = WIN ? args.H / args.G : 0;
-    const bool keys = WIN ? (int)blockIdx.y < kv_heads : blockIdx.z == 0;
-    const int head = WIN && !keys ? (int)blockIdx.y - kv_heads : (int)blockIdx.y;
-    if (keys) ab_tile<true, OWN, WIN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, head, ctl);
-    else ab_tile<false, OWN, WIN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, head, ctl);
+    if (!WIN) {
+      if (blockIdx.z == 0)
+        ab_tile<true, OWN, WIN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
+      else
+        ab_tile<false, OWN, WIN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, blockIdx.x, blockIdx.y, ctl);
+    } else {
+      const int firsts = args.first_tiles * args.first_pieces;
+      const int per_head = firsts + (args.tiles - args.first_tiles) * args.other_pieces;
+      const int id = (int)blockIdx.x, key_ctas = args.H / args.G * per_head;
+      if (id < key_ctas) {
+        const int head = id / per_head, x = id - head * per_head;
+        const bool first = x < firsts;
+        const int pieces = first ? args.first_pieces : args.other_pieces, y = first ? x : x - firsts;
+        const int tile = y / pieces + (first ? 0 : args.first_tiles);
+        // a piece's place among those of split tiles
+        const int slot = head * ab_part_slots(args) + (first || args.first_pieces == 1 ? y : firsts + y);
+        ab_tile<true, OWN, WIN>(&tmK, &tmV, &tmQ, &tmO, args, sm, tmem_base, tile, head, ctl, y % pieces, pieces, slot);
+      } else {
+        const int y = id - key_ctas, head = y / args.tiles;
+        ab_tile<false, OWN, WIN>(&tmQ, &tmO, &tmK, &tmV, args, sm, tmem_base, y - head * args.tiles, head, ctl);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -715,10 +768,86 @@ cudaError_t launch_attention_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   return cudaGetLastError();
 }
 
+// dV and dK of the key tiles that several pieces computed: their sums, in order.
+// Block: 32 rows of a split tile (x), KV head (y), dV or dK (z).
+__global__ void __launch_bounds__(256) attention_bwd_join_kernel(const AttnBwdArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int x = blockIdx.x >> 2, lane = threadIdx.x & 31, row = (blockIdx.x & 3) * 32 + lane, ch = (threadIdx.x >> 5) * 16;
+  const int firsts = a.first_pieces > 1 ? a.first_tiles : 0;    // split ones among the first tiles
+  const bool first = x < firsts;
+  const int tile = first ? x : x - firsts + a.first_tiles, pieces = first ? a.first_pieces : a.other_pieces;
+  const int slot = blockIdx.y * ab_part_slots(a) + (first ? x * pieces : firsts * a.first_pieces + (x - firsts) * pieces);
+  const float* from = a.part + ((int64_t)slot * 2 + blockIdx.z) * 128 * 128 + ch * 128 + row;
+  float sum[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
+  for (int p = 0; p < pieces; ++p, from += 2 * 128 * 128) {
+    if (!in_bounds<float>(a.part, a.part_elems, from + 15 * 128, 1, a.err, 47)) continue;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] += from[e * 128];
+  }
+  const int grow = tile * 128 + row;
+  if (grow >= a.S) return;
+  const float scale = blockIdx.z == 0 ? 1.0f : a.scale;
+  __nv_bfloat16* base = blockIdx.z == 0 ? a.dv : a.dk;
+  __nv_bfloat16* to = base + (int64_t)grow * a.dkv_row_stride + (int64_t)blockIdx.y * a.dkv_head_stride + ch;
+  if (!in_bounds<__nv_bfloat16>(base, a.dkv_elems, to, 16, a.err, 48)) return;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8)
+    *reinterpret_cast<uint4*>(to + e) =
+        make_uint4(pack_bf16x2(sum[e] * scale, sum[e + 1] * scale), pack_bf16x2(sum[e + 2] * scale, sum[e + 3] * scale),
+                   pack_bf16x2(sum[e + 4] * scale, sum[e + 5] * scale), pack_bf16x2(sum[e + 6] * scale, sum[e + 7] * scale));
+}
+
+// How the key side is split.  Key tiles that all rows see (the first ones), or of
+// heads that many share, take many more steps than a query tile; one of more steps
+// than an SM's share of all the work (a key step counts 4 products, a query step
+// 3) would run alone at the end, and is cut into pieces of half that share, at
+// least kPieceSteps (4099 rows, 24 heads over 4, 640 keys and 3 first: one CTA of
+// 198 steps, 281 us; in pieces %SHARED% us).
+constexpr int kPieceSteps = 16, kMaxPieces = 520;
+void attn_bwd_split(AttnBwdArgs* a) {
+  a->first_tiles = a->w.left < 0 ? 0 : (int)std::min<int64_t>(a->tiles, ((int64_t)a->w.first + 127) / 128);
+  a->first_pieces = a->other_pieces = 1;
+  int64_t steps = 0;
+  int most[2] = {0, 0};
+  for (int t = 0; t < a->tiles; ++t) {
+    const int j0 = t * 128, j1 = std::min(j0 + 128, a->S) - 1;
+    const int lo = win_row_lo(a->w, j0, a->S) >> 7;
+    const int hi = std::max(win_row_hi(a->w, j0, a->S), win_row_hi(a->w, j1, a->S));
+    const int n = (((hi + 127) >> 7) - lo) * a->G;
+    steps += n;
+    int& m = most[t < a->first_tiles ? 0 : 1];
+    m = std::max(m, n);
+  }
+  const int heads = a->H / a->G;
+  const int64_t share = steps * heads * 7 / 4 / num_sms();
+  auto pieces = [&](int n) -> int {
+    if (n <= share || n <= kPieceSteps) return 1;
+    const int64_t each = std::max<int64_t>(kPieceSteps, share / 2);
+    return (int)((n + each - 1) / each);
+  };
+  a->first_pieces = pieces(most[0]);
+  a->other_pieces = pieces(most[1]);
+  if ((int64_t)heads * ab_part_slots(*a) > kMaxPieces) a->other_pieces = 1;
+  if ((int64_t)heads * ab_part_slots(*a) > kMaxPieces) a->first_pieces = 1;
+  a->part_elems = (size_t)heads * ab_part_slots(*a) * 2 * 128 * 128;
+}
+// Bytes of pieces, for every window.
+size_t attn_bwd_part_bytes(int64_t S, int64_t H, int64_t Hk) {
+  const int64_t tiles = (S + 127) / 128, n = tiles * (H / Hk);
+  if (n <= kPieceSteps) return 0;
+  const int64_t most = std::min<int64_t>(kMaxPieces, Hk * tiles * ((n + kPieceSteps - 1) / kPieceSteps));
+  return (size_t)most * 2 * 128 * 128 * 4;
+}
+
 cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                         const CUtensorMap& tmO, const AttnBwdArgs& a, cudaStream_t stream) {
   if (!tmem_exclusive(AB_SMEM)) return cudaErrorNotSupported;
-  const dim3 rows_grid((unsigned)a.tiles, (unsigned)a.H), grid((unsigned)a.tiles, (unsigned)(a.H / a.G + a.H));
+  const int heads = a.H / a.G;
+  const int64_t key_ctas = (int64_t)heads * (a.first_tiles * a.first_pieces + (a.tiles - a.first_tiles) * a.other_pieces);
+  const dim3 rows_grid((unsigned)a.tiles, (unsigned)a.H), grid((unsigned)(key_ctas + (int64_t)a.H * a.tiles));
   cudaError_t e = launch_kernel(attention_bwd_rows_kernel, rows_grid, dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   const auto kernel = attention_bwd_kernel<false, true>;
@@ -726,9 +855,14 @@ cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMa
   if (e != cudaSuccess) return e;
   e = launch_kernel(kernel, grid, dim3(AB_THREADS), AB_SMEM, stream, tmQ, tmK, tmV, tmO, a);
   if (e != cudaSuccess) return e;
+  const int split = (a.first_pieces > 1 ? a.first_tiles : 0) + (a.other_pieces > 1 ? a.tiles - a.first_tiles : 0);
+  if (split > 0) {
+    e = launch_kernel(attention_bwd_join_kernel, dim3((unsigned)(split * 4), (unsigned)heads, 2), dim3(256), 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
   set_kernel_info("attention_bwd_kernel<window> tcgen05.mma.cta_group::1.kind::f16 tile=128x128 stages=%d,%d acc=f32 "
-                  "P,dS-in-TMEM shared=%d grid=%ux%u",
-                  AB_ST1, AB_ST2, a.G, grid.x, grid.y);
+                  "P,dS-in-TMEM shared=%d grid=%u pieces=%d,%d",
+                  AB_ST1, AB_ST2, a.G, grid.x, a.first_pieces, a.other_pieces);
   return cudaGetLastError();
 }
 

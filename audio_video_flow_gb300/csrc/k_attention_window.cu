@@ -94,32 +94,51 @@ __device__ __forceinline__ AwSeq aw_seq(const AttnWinArgs& a, int s) {
     return {0, 0, -1};
   return {b, e - b, len};
 }
+// The setup and the segments are straight-line code that each CTA runs a few
+// times, so their time is that of fetching it: divisions and the key tiles of a
+// unit are functions that are not inlined (setup 6000 -> %SETUP% cycles).
+__device__ __noinline__ uint32_t aw_div(uint32_t a, uint32_t b) { return a / b; }
+__device__ __forceinline__ int aw_unit_of(const WindowArgs& w, int i) {   // win_unit
+  return w.unit == 1 ? i : (int)aw_div((uint32_t)(i - w.origin + w.unit), (uint32_t)w.unit) - 1;
+}
 // Key tiles of a unit (U rows): [0, nsink) and [wbeg, wbeg + n - nsink).
 struct AwUnit { int rows, pos0, lo, hi, first, nsink, wbeg, n; };
-__device__ __forceinline__ AwUnit aw_unit(const AttnWinArgs& a, const AwSeq& q, int unit) {
+__device__ __forceinline__ AwUnit aw_unit(const WindowArgs& w, int U, int rows, int keys, int unit) {
   AwUnit p;
-  const int at = unit * a.U;
-  p.rows = min(a.U, q.rows - at);
-  p.pos0 = q.keys - q.rows + at;
-  const int u0 = win_unit(a.w, p.pos0), u1 = win_unit(a.w, p.pos0 + p.rows - 1);
-  p.lo = win_lo_of(a.w, u0, q.keys);
-  p.hi = win_hi_of(a.w, u1, q.keys);
-  p.first = min(a.w.first, win_lo_of(a.w, u1, q.keys));   // first keys that only they make visible
+  const int at = unit * U;
+  p.rows = min(U, rows - at);
+  p.pos0 = keys - rows + at;
+  const int u0 = aw_unit_of(w, p.pos0), u1 = aw_unit_of(w, p.pos0 + p.rows - 1);
+  p.lo = win_lo_of(w, u0, keys);
+  p.hi = win_hi_of(w, u1, keys);
+  p.first = min(w.first, win_lo_of(w, u1, keys));   // first keys that only they make visible
   p.wbeg = p.lo >> 7;
   p.nsink = min((p.first + 127) >> 7, p.wbeg);
   p.n = p.nsink + ((p.hi + 127) >> 7) - p.wbeg;
   return p;
 }
-__device__ __forceinline__ int aw_units(const AttnWinArgs& a, int rows) { return (rows + a.U - 1) / a.U; }
-__device__ __forceinline__ int aw_groups(const AttnWinArgs& a, int rows) { return (rows + a.U * a.M - 1) / (a.U * a.M); }
+__device__ __forceinline__ int aw_units(const AttnWinArgs& a, int rows) { return aw_div(rows + a.U - 1, a.U); }
+__device__ __forceinline__ int aw_groups(const AttnWinArgs& a, int rows) { return aw_div(rows + a.U * a.M - 1, a.U * a.M); }
 // The weight of a group of M units: its key tiles over M, from its first and last
 // unit's.
+__device__ __noinline__ int aw_weight(WindowArgs w, int U, int M, int rows, int keys, int group) {
+  const int p0 = group * M, n0 = aw_unit(w, U, rows, keys, p0).n;
+  if (M == 1) return n0;
+  const int p1 = min(p0 + M, (int)aw_div(rows + U - 1, U)) - 1;
+  return aw_div((n0 + aw_unit(w, U, rows, keys, p1).n) * (p1 - p0 + 1) + 2 * M - 1, 2 * M);
+}
 __device__ __forceinline__ int aw_group(const AttnWinArgs& a, const AwSeq& q, int group) {
-  if (a.M == 1) return aw_unit(a, q, group).n;
-  const int p0 = group * a.M, p1 = min(p0 + a.M, aw_units(a, q.rows)) - 1;
-  return ((aw_unit(a, q, p0).n + aw_unit(a, q, p1).n) * (p1 - p0 + 1) + 2 * a.M - 1) / (2 * a.M);
+  return aw_weight(a.w, a.U, a.M, q.rows, q.keys, group);
 }
 
+// Where gang g's run begins, before the move to a near border: all g / gangs.
+struct AwBorder {
+  int each, rest;
+  uint64_t inv;                  // 2^32 / gangs + 1; rest g is below 2^16
+  __device__ __forceinline__ AwBorder(const AttnWinArgs& a, int all)
+      : each((int)aw_div(all, a.gangs)), rest(all - each * a.gangs), inv(a.gangs_inv) {}
+  __device__ __forceinline__ int at(int g) const { return each * g + (int)(((uint32_t)(rest * g) * inv) >> 32); }
+};
 // Where a run begins: `off` of the weight n of group `group` of sequence `seq`,
 // head `head`; off = n: at the end of that group.
 struct AwLoc { int head, seq, group, off, n, x; };
@@ -144,7 +163,7 @@ __device__ __forceinline__ AwLoc aw_locate(const AttnWinArgs& a, const int* pre,
   AwLoc l;
   const int lane = threadIdx.x & 31;
   l.x = x;
-  l.head = x / per_head;
+  l.head = (int)aw_div(x, per_head);
   l.seq = l.group = l.off = l.n = 0;
   if (l.head >= a.c.n_kv_heads) return l;
   int y = x - l.head * per_head;
@@ -448,9 +467,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
   }
   __syncthreads();
   const int per_head = sh->total, all = per_head * a.c.n_kv_heads;
+  const int gang = (int)aw_div(blockIdx.x, a.M);
   if (warp < 2 && all > 0) {
-    const int c = blockIdx.x / a.M + warp, gangs = gridDim.x / a.M;
-    const AwLoc l = aw_locate<PAGED>(a, pre, per_head, all / gangs * c + all % gangs * c / gangs);
+    const AwLoc l = aw_locate<PAGED>(a, pre, per_head, AwBorder(a, all).at(gang + warp));
     if (lane == 0) sh->loc[warp] = l;
   }
   fence_proxy_async_smem();   // the sums were read; the ring's loads may overwrite them
@@ -475,7 +494,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       AwSeq q = aw_seq<PAGED>(a, seq);
       int ng = aw_groups(a, q.rows);
       bool here = off < b.n, first_group = here; // else the run begins with the group after this one
-      const int member = blockIdx.x % a.M, gangs = gridDim.x / a.M;
+      const int member = blockIdx.x - gang * a.M;
       int x0 = b.x - (here ? off : 0), w0 = 0;   // where the group begins, its weight
       for (uint32_t n = 0;;) {
         if (!here && rem > 0) {
@@ -501,22 +520,18 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           // the gang's part of the group's weight, in proportion of this CTA's unit.
           // The members take turns, so that units of growing windows even out.
           const int weight = first_group ? b.n : aw_group(a, q, group), part = min(rem, weight - off);
-          const int unit = group * a.M + (a.M == 1 ? 0 : (member + group + head) % a.M);
+          int turn = member + group + head;
+          turn -= (int)aw_div(turn, a.M) * a.M;
+          const int unit = group * a.M + turn;
           first_group = false;
           w0 = weight;
           rem -= part;
           if (unit >= aw_units(a, q.rows)) continue;
-          const AwUnit p = aw_unit(a, q, unit);
-          if (off == 0 && part == weight) {
-            g.off = 0;
-            g.cnt = p.n;
-          } else if (weight == p.n) {
-            g.off = off;
-            g.cnt = part;
-          } else {
-            g.off = (int)((int64_t)off * p.n / weight);
-            g.cnt = (int)((int64_t)(off + part) * p.n / weight) - g.off;
-          }
+          const AwUnit p = aw_unit(a.w, a.U, q.rows, q.keys, unit);
+          const float ratio = __fdividef((float)p.n, (float)weight);
+          const int done = off + part;
+          g.off = min((int)((float)off * ratio), p.n);
+          g.cnt = (done == weight ? p.n : min((int)((float)done * ratio), p.n)) - g.off;
           if (g.cnt == 0) continue;
           g.head = head;
           g.seq = seq;
@@ -532,11 +547,12 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           g.n = p.n;
           g.owner = g.parts = 0;
           if (g.cnt < p.n) {
-            // the gangs whose runs hold the group's beginning and its end (their
-            // borders as they are after the moves)
-            const int64_t from = ((int64_t)(x0 + kSnap + 1) * gangs - 1) / all;
-            const int64_t to = ((int64_t)(x0 + weight - kSnap) * gangs - 1) / all;
-            const int first = (int)(from < gangs - 1 ? from : gangs - 1), last = (int)(to < gangs - 1 ? to : gangs - 1);
+            // the gangs whose runs hold the group's beginning and its end: the last
+            // whose border, as it is after the move, is no later
+            const AwBorder border(a, all);
+            int first = gang, last = gang;
+            while (off > 0 && border.at(first) > x0 + kSnap) --first;
+            while (last + 1 < a.gangs && border.at(last + 1) < x0 + weight - kSnap) ++last;
             g.owner = first * a.M + member;
             g.parts = 2 * (last - first + 1) + (off == 0 ? 1 : 0);
           }
@@ -691,7 +707,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AW_REGS_MANY));
     const int t = (warp - 4) >> 2;
     const int qq = warp & 3;
-    const int row = qq * 32 + lane;            // (row, head) pair of the tile
+    const int row = qq * 32 + lane, row_r = (int)aw_div(row, a.G);   // (row, head) pair of the tile, its row
     const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), (uint32_t)(t * 128));
     const uint32_t o_base = s_base + 256u;
     const float sl2 = a.scale_log2;
@@ -713,9 +729,10 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       const bool active = qq * 32 < nrows * a.G;
       int lo, hi, first;
       {
-        const int pos = g->pos0 + rbase + min(row / a.G, nrows - 1), keys = g->keys;
-        lo = win_lo(a.w, pos, keys);
-        hi = win_hi(a.w, pos, keys);
+        const int pos = g->pos0 + rbase + min(row_r, nrows - 1), keys = g->keys;
+        const int u = aw_unit_of(a.w, pos);
+        lo = win_lo_of(a.w, u, keys);
+        hi = win_hi_of(a.w, u, keys);
         first = min(a.w.first, hi);
       }
       const int step = dual ? 1 : 2, off = g->off + (dual ? 0 : t), nsink = g->nsink, wshift = g->wbeg - nsink;
@@ -826,7 +843,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           l = l_run * fa + b.y * fb;
         }
       }
-      const int r = row / a.G, qhead = g->head * a.G + row - r * a.G;
+      const int r = row_r, qhead = g->head * a.G + row - r * a.G;
       const int64_t at = ((int64_t)(g->row0 + rbase + r) * a.H + qhead) * 128;   // the row in o
       const int who = (dual ? t : 0) * 4 + qq, few = MODE != AW_ROWS && g->parts <= 2 * kFew + 1;
       // A part of a unit.  Few parts: counted in now; who completes the count
@@ -1076,6 +1093,7 @@ bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_s
     }
   }
   p->ctas = ctas / p->M * p->M;
+  p->gangs = ctas / p->M;
   p->split = tiles > 2 * kSnap + 1;                  // else every end moves to a unit's
   p->part_rows = (int)(n_rows < R ? n_rows : R) * G;
   p->part_slots = p->mode != AW_ROWS && n_rows > R ? 4 : 2;

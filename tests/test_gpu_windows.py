@@ -461,3 +461,17 @@ def test_evict(lengths, heads, page, budget, first, recent, kind):
             moved, old = to.w[pages, h, places], c.data[s][2][rows, h]
             assert torch.equal(moved.view(torch.int32), old.view(torch.int32))
     assert (to.w[~used] == 3.0).all() and (to.k[~used] == 3.0).all() and (to.v[~used] == 3.0).all()
+
+
+@pytest.mark.parametrize("S, H, Hk, w", [
+    (2600, 2, 1, dict(left=100, right=0, n_first=5)),             # key tile 0 is seen by every row: split alone
+    (2600, 4, 1, dict(right=0)),                                  # later key tiles have fewer steps than pieces
+    (1500, 8, 1, dict(left=40, right=40, n_first=300)),
+    (3000, 1, 1, dict(left=-1, right=0, unit=700, origin=50))])
+def test_window_backward_split_key_tiles(S, H, Hk, w):
+    """Key tiles whose steps are shared out over several CTAs, and joined."""
+    q, k, v = window_case(S, H, Hk, S + H)
+    args = (w, q, k, v, *backward_inputs(w, q, k, v, torch.Generator().manual_seed(S)))
+    grads = run_backward(*args)
+    ok()
+    check_backward(*args, grads, f"S={S} H={H}/{Hk}")
