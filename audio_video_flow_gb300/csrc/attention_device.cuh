@@ -52,6 +52,23 @@ __device__ __forceinline__ void at_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one), "n"(SA), "n"(SB)
       : "memory");
 }
+// One K step of 16.
+__device__ __forceinline__ void at_mma1_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+// Shared-memory descriptor of a K-major operand without swizzle, K = 16: cores of
+// 8 rows x 16 bytes, the two of a row group side by side (row r, channel k at
+// (r / 8) 256 + (k / 8) 128 + (r % 8) 16 + (k % 8) 2 bytes).
+__device__ __forceinline__ uint64_t at_sdesc_plain16(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(256u >> 4) << 32 | (uint64_t)1 << 46;
+}
 __device__ __forceinline__ void at_commit(uint64_t* bar, uint32_t one) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -127,11 +144,18 @@ __host__ __device__ inline int win_hi_of(const WindowArgs& w, int u, int keys) {
 }
 __host__ __device__ inline int win_lo(const WindowArgs& w, int i, int keys) { return win_lo_of(w, win_unit(w, i), keys); }
 __host__ __device__ inline int win_hi(const WindowArgs& w, int i, int keys) { return win_hi_of(w, win_unit(w, i), keys); }
+// of a key in unit u
+__host__ __device__ inline int win_row_lo_of(const WindowArgs& w, int u, int rows) {
+  return w.right < 0 ? 0 : win_edge(w, u - w.right, rows);
+}
+__host__ __device__ inline int win_row_hi_of(const WindowArgs& w, int u, int j, int rows) {
+  return w.left < 0 || j < w.first ? rows : win_edge(w, u + w.left + 1, rows);
+}
 __host__ __device__ inline int win_row_lo(const WindowArgs& w, int j, int rows) {
-  return w.right < 0 ? 0 : win_edge(w, win_unit(w, j) - w.right, rows);
+  return win_row_lo_of(w, win_unit(w, j), rows);
 }
 __host__ __device__ inline int win_row_hi(const WindowArgs& w, int j, int rows) {
-  return w.left < 0 || j < w.first ? rows : win_edge(w, win_unit(w, j) + w.left + 1, rows);
+  return win_row_hi_of(w, win_unit(w, j), j, rows);
 }
 // bits [0, x) of a word
 __device__ __forceinline__ uint32_t win_bits(int x) {

@@ -1575,7 +1575,8 @@ h3_status check_cache(const h3_cache* c) {
   return H3_OK;
 }
 CacheArgs cache_args(const h3_cache& c, const int32_t* start) {
-  return {c.n_pages, c.page_size, c.n_kv_heads, c.n_seqs, c.table_width, c.table, c.length, start};
+  return {c.n_pages, c.page_size, __builtin_ctz((unsigned)c.page_size), c.n_kv_heads, c.n_seqs, c.table_width, c.table,
+          c.length, start};
 }
 size_t cache_rows(const h3_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * c.page_size; }
 
@@ -1795,6 +1796,9 @@ h3_status h3_cache_weights(const h3_cache* cache, const h3_window* window, int32
   if (weights_out == lse || (const void*)weights_out == q || (void*)weights_out == cache->k ||
       (void*)weights_out == cache->v)
     return H3_ERR_SHAPE;
+  if ((int64_t)cache->n_seqs * cache->n_kv_heads * (((int64_t)cache->table_width * cache->page_size + 127) / 128) >=
+      (int64_t(1) << 31))
+    return H3_ERR_UNSUPPORTED;
   CUtensorMap tq, tk;
   CacheWeightsArgs a{};
   a.w = window_args(*window);

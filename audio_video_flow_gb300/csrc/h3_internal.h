@@ -325,7 +325,7 @@ cudaError_t launch_attention_window_bwd(const CUtensorMap& tmQ, const CUtensorMa
 // A paged cache: pages [n_pages][n_kv_heads][page_size][128], and the rows of
 // each sequence.  One document of its own (not paged): start is null, n_seqs 1.
 struct CacheArgs {
-  int n_pages, page_size, n_kv_heads, n_seqs, table_width;
+  int n_pages, page_size, page_shift, n_kv_heads, n_seqs, table_width;   // page_size = 1 << page_shift
   const int32_t* table;    // [n_seqs][table_width]
   const int32_t* length;   // [n_seqs]
   const int32_t* start;    // [n_seqs + 1], new rows

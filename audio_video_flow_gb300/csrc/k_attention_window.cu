@@ -223,7 +223,7 @@ __device__ __forceinline__ int aw_page(const AttnWinArgs& a, const AwSeg& g, int
   if (lane >= 256 / rows) return 0;
   const int slot = tile * 128 + (lane >> 1) * rows;
   if (slot >= g.keys || !(slot < g.first || (slot + rows > g.lo && slot < g.hi))) return a.c.n_pages;
-  const int id = a.c.table[(int64_t)g.seq * a.c.table_width + slot / a.c.page_size];
+  const int id = a.c.table[(int64_t)g.seq * a.c.table_width + (slot >> a.c.page_shift)];
   if (id >= 0 && id < a.c.n_pages) return id;
   record_error(a.err, DEVERR_INDEX);
   return a.c.n_pages;

@@ -14,10 +14,10 @@ namespace {
 // Element offset of a slot's row in the pages (of 128 channels; of 1 in the
 // weights).
 __device__ __forceinline__ int64_t page_row(const CacheArgs& c, int page, int head, int slot) {
-  return ((int64_t)page * c.n_kv_heads + head) * c.page_size + slot % c.page_size;
+  return (((int64_t)page * c.n_kv_heads + head) << c.page_shift) + (slot & (c.page_size - 1));
 }
 __device__ __forceinline__ int page_of(const CacheArgs& c, int seq, int slot) {
-  return c.table[(int64_t)seq * c.table_width + slot / c.page_size];
+  return c.table[(int64_t)seq * c.table_width + (slot >> c.page_shift)];
 }
 __device__ __forceinline__ int64_t cache_slots(const CacheArgs& c) { return (int64_t)c.table_width * c.page_size; }
 }  // namespace
@@ -67,20 +67,32 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
 // the KV head of P_ij = exp(q_i . k_j / sqrt(128) - lse_i).  Keys are the rows
 // of the score tiles (S = K Q^T), so that each key's sum stays in one thread,
 // in an order that nothing but the row count fixes: no atomics.
-//   A unit is up to four 128-key tiles of one KV head and sequence, each owned
-//   by one warpgroup; the tiles of 128 (row, head) pairs that see any of them
-//   stream past, each used by all four.  CTA c takes units c, c + grid, ...
+//   A unit is a few 128-key tiles of one KV head and sequence; CTA c takes units
+// c, c + grid, ...  The tiles of 128 (row, head) pairs that see any of its keys
+// are held in shared memory, up to four at a time (a pass), and the key tiles
+// stream past them, each half (64 channels) a stage of the ring.  Of a pass, tile
+// i of rows lies in slot (s + i) % 4, s where the pass before ended, so that the
+// next pass's rows load while this one's last are used.
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 the rows' log-sum-exp,
-//   warps 4-19 exponentials and sums.
-// TMEM: S of key tile w at [128 w, 128 w + 128).
-// Many rows are bound by the exponentials (16 a clock and SM: 1024 cycles a
-// tile, its product 512), single rows by reading K.
+//   warps 4-7 exponentials and sums of slots 0 and 2, 8-11 of 1 and 3 (a key per
+//   thread),
+//   warp 3 adds the slots' sums of a key tile, in their order, to the weights.
+// TMEM: S of slot i at [128 i, 128 i + 128).  A product has as many columns as
+// its tile has pairs, rounded up to 16: single rows cost little beside reading K.
+// Shared memory is what the products themselves fill, so the rows' log-sum-exp is
+// not read from it column by column by every thread (16 KB a product and warp, as
+// much as the operands: 124 us of a call of 405 rows) but comes with the product,
+// as a K step of its own: ones times -lse sqrt(128) in three bf16 parts, 2^-26 of
+// it off.
+// Measured: %WEIGHTS%
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int CW_THREADS = 32 * 20;
-constexpr int CW_KT = 4, CW_QST = 2;
+constexpr int CW_THREADS = 32 * 12;
+constexpr int CW_SLOTS = 4, CW_KST = 4, CW_RED = 2;
 constexpr int CW_TILE = 128 * 128 * 2, CW_BOX = 128 * 64 * 2;
-constexpr int CW_SMEM = CW_TILE * (CW_KT + CW_QST) + 8 * kCacheMaxSeqs + CW_QST * 512 + 256;
+constexpr int CW_STEP = 128 * 16 * 2;   // an operand of one K step
+constexpr int CW_SMEM =
+    CW_TILE * CW_SLOTS + CW_BOX * CW_KST + CW_STEP * (CW_SLOTS + 1) + 4 * kCacheMaxSeqs + CW_SLOTS * CW_RED * 512 + 512;
 
 struct CwUnit {
   int head, seq, key0, tiles;    // key tiles of the unit, from key0
@@ -91,17 +103,19 @@ __device__ __forceinline__ bool cw_seq_ok(const CacheArgs& c, int n_rows, int s)
   const int b = c.start[s], e = c.start[s + 1], len = c.length[s];
   return b >= 0 && e >= b && e <= n_rows && len >= e - b && (int64_t)len <= cache_slots(c);
 }
-__device__ __forceinline__ CwUnit cw_unit(const CacheWeightsArgs& a, const int64_t* pre, int64_t per_head, int64_t u) {
+// Not inlined: every role calls it once per unit, and fetching the code is what a
+// first call costs.
+__device__ __noinline__ CwUnit cw_unit(const CacheWeightsArgs& a, const int* pre, int per_head, int u) {
   CwUnit x;
-  x.head = (int)(u / per_head);
-  const int64_t y = u - (int64_t)x.head * per_head;
+  x.head = u / per_head;
+  const int y = u - x.head * per_head;
   int s = 0;
   for (int lo = 0, hi = a.c.n_seqs - 1; lo <= hi;) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= y) { s = mid; lo = mid + 1; } else { hi = mid - 1; }
   }
   x.seq = s;
-  x.key0 = (int)(y - pre[s]) * a.tiles * 128;
+  x.key0 = (y - pre[s]) * a.tiles * 128;
   x.row0 = a.c.start[s];
   x.rows = a.c.start[s + 1] - x.row0;
   x.keys = a.c.length[s];
@@ -114,45 +128,77 @@ __device__ __forceinline__ CwUnit cw_unit(const CacheWeightsArgs& a, const int64
   x.nq = hi > lo ? (hi + a.R - 1) / a.R - x.q0 : 0;
   return x;
 }
+// exp2(s scale) over the columns [ca, cb) of 32 Q, added to acc; s_empty is
+// arrived at once the scores are in registers.
+template <int Q>
+__device__ __forceinline__ void cw_sums(uint32_t s_at, int ca, int cb, float2 scale, float2 (&acc)[4], uint64_t* s_empty) {
+  uint32_t s[Q][32];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) tmem_ld32(s_at + (uint32_t)(q * 32), s[q]);
+  tmem_ld_wait(s[0]);
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(s_empty);
+  if (!__all_sync(0xffffffffu, ca <= 0 && cb >= 32 * Q)) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t see = win_bits(cb - q * 32) & ~win_bits(ca - q * 32);
+      if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (!((see >> c) & 1u)) s[q][c] = __float_as_uint(-INFINITY);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 z = __fmul2_rn(make_float2(__uint_as_float(s[q][2 * c]), __uint_as_float(s[q][2 * c + 1])), scale);
+      acc[c & 3] = __fadd2_rn(acc[c & 3], make_float2(at_ex2(z.x), at_ex2(z.y)));
+    }
+}
 }  // namespace
 
 __global__ void __launch_bounds__(CW_THREADS, 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                         const CacheWeightsArgs a) {
+                         const __grid_constant__ CacheWeightsArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sk = smem_raw;
-  uint8_t* sq = sk + CW_KT * CW_TILE;
-  int64_t* pre = reinterpret_cast<int64_t*>(sq + CW_QST * CW_TILE);
-  float* sl = reinterpret_cast<float*>(pre + kCacheMaxSeqs);   // [CW_QST][128] log-sum-exp, base 2
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sl + CW_QST * 128);
-  uint64_t* k_full = bars;
-  uint64_t* k_empty = k_full + CW_KT;
-  uint64_t* q_full = k_empty + CW_KT;
-  uint64_t* q_empty = q_full + CW_QST;
-  uint64_t* l_full = q_empty + CW_QST;
-  uint64_t* l_empty = l_full + CW_QST;
-  uint64_t* s_full = l_empty + CW_QST;
-  uint64_t* s_empty = s_full + CW_KT;
-  uint64_t* drain = s_empty + CW_KT;
-  int64_t* total = reinterpret_cast<int64_t*>(drain + 1);
+  uint8_t* sq = smem_raw;
+  uint8_t* sk = sq + CW_SLOTS * CW_TILE;
+  uint8_t* sl = sk + CW_KST * CW_BOX;                          // [slot] the rows' part of the last K step, then the ones
+  int* pre = reinterpret_cast<int*>(sl + (CW_SLOTS + 1) * CW_STEP);
+  float* red = reinterpret_cast<float*>(pre + kCacheMaxSeqs);  // [slot][CW_RED][128] sums of a product
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(red + CW_SLOTS * CW_RED * 128);
+  uint64_t* k_empty = k_full + CW_KST;
+  uint64_t* q_full = k_empty + CW_KST;
+  uint64_t* q_empty = q_full + CW_SLOTS;
+  uint64_t* l_full = q_empty + CW_SLOTS;
+  uint64_t* l_empty = l_full + CW_SLOTS;
+  uint64_t* s_full = l_empty + CW_SLOTS;
+  uint64_t* s_empty = s_full + CW_SLOTS;
+  uint64_t* r_full = s_empty + CW_SLOTS;                       // [slot][CW_RED]
+  uint64_t* r_empty = r_full + CW_SLOTS * CW_RED;
+  uint64_t* drain = r_empty + CW_SLOTS * CW_RED;
+  int* total = reinterpret_cast<int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  static_assert((4 * CW_KT + 4 * CW_QST + 2) * 8 + 8 <= 256, "barriers fit");
+  static_assert((2 * CW_KST + 6 * CW_SLOTS + 2 * CW_SLOTS * CW_RED + 1) * 8 + 12 <= 512, "barriers fit");
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int w = 0; w < CW_KT; ++w) {
-      mbar_init(&k_full[w], 1);
-      mbar_init(&k_empty[w], 1);
-      mbar_init(&s_full[w], 1);
-      mbar_init(&s_empty[w], 4);
-    }
-    for (int s = 0; s < CW_QST; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
-      mbar_init(&l_full[s], 1);
-      mbar_init(&l_empty[s], 16);
+    for (int s = 0; s < CW_KST; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    for (int i = 0; i < CW_SLOTS; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&l_full[i], 1);
+      mbar_init(&l_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+      for (int b = 0; b < CW_RED; ++b) {
+        mbar_init(&r_full[i * CW_RED + b], 4);
+        mbar_init(&r_empty[i * CW_RED + b], 1);
+      }
     }
     mbar_init(drain, 1);
     *abort_flag = timeout_recorded(a.err) ? 1 : 0;   // sticky timeout of an earlier launch
@@ -163,20 +209,27 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     tma_prefetch_desc(&tmK);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
+  // ones for every key in the first three channels of the last K step; its second
+  // eight channels are zero on both sides
+  for (int i = threadIdx.x; i < (CW_SLOTS + 1) * 256; i += CW_THREADS) {
+    const bool ones = i >= CW_SLOTS * 256 && ((i >> 3) & 1) == 0;
+    reinterpret_cast<uint4*>(sl)[i] = make_uint4(ones ? 0x3F803F80u : 0u, ones ? 0x3F80u : 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   griddep_wait();
-  if (warp == 2) {   // groups of key tiles before each sequence
-    int64_t carry = 0;
+  if (warp == 2) {   // units before each sequence
+    int carry = 0;
     for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
       const int s = s0 + lane;
-      int64_t mine = 0;
+      int mine = 0;
       if (s < a.c.n_seqs) {
         if (cw_seq_ok(a.c, a.n_rows, s)) mine = (a.c.length[s] + a.tiles * 128 - 1) / (a.tiles * 128);
         else if (blockIdx.x == 0) record_error(a.err, DEVERR_INDEX);
       }
-      int64_t sum = mine;
+      int sum = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, sum, d);
+        const int t = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += t;
       }
       if (s < a.c.n_seqs) pre[s] = carry + sum - mine;
@@ -189,182 +242,253 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl ctl{abort_flag, a.err, KID_CACHE_WEIGHTS};
-  const int64_t per_head = *total, units = per_head * a.c.n_kv_heads;
+  const int per_head = *total, units = per_head * a.c.n_kv_heads;
 
   if (*ctl.flag != 0) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    uint32_t kph[CW_KT] = {0, 0, 0, 0}, st = 0, ph = 0, issued = 0, loaded = 0;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    uint32_t qph = 0, slot = 0, st = 0, ph = 0, issued = 0, loaded = 0;   // qph: a phase bit per slot
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
-      if (x.nq == 0) continue;
-      const int ps = a.c.page_size, rows = min(ps, 128);
-#pragma unroll
-      for (int w = 0; w < CW_KT; ++w) {
-        if (w >= x.tiles || !ok) continue;
-        if (!at_wait(&k_empty[w], kph[w] ^ 1u, ctl)) { ok = false; continue; }
-        kph[w] ^= 1u;
-        loaded |= 1u << w;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[w], CW_TILE);
-        __syncwarp();
-        if (lane < 256 / rows) {
-          const int box = lane >> 1, slot = x.key0 + w * 128 + box * rows;
-          int page = a.c.n_pages;   // out of range: zeros
-          if (slot < x.keys) {
-            const int id = page_of(a.c, x.seq, slot);
-            if (id >= 0 && id < a.c.n_pages) page = id;
+      const int rows = min(a.c.page_size, 128);
+      for (int p = 0; p < x.nq && ok; p += CW_SLOTS) {
+        const int n = min(CW_SLOTS, x.nq - p);
+        int page = 0;
+        auto page_at = [&](int k) -> int {   // this lane's page of key tile k, n_pages: zeros
+          const int key = x.key0 + k * 128 + lane * rows;
+          if (lane >= 128 / rows || key >= x.keys) return a.c.n_pages;
+          const int id = page_of(a.c, x.seq, key);
+          return id >= 0 && id < a.c.n_pages ? id : a.c.n_pages;
+        };
+        page = page_at(0);
+        for (int k = 0; k < x.tiles && ok; ++k) {
+          const int next = k + 1 < x.tiles ? page_at(k + 1) : 0;   // arrives during the waits
+          for (int h = 0; h < 2; ++h) {
+            if (!at_wait(&k_empty[st], ph ^ 1u, ctl)) { ok = false; break; }
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[st], CW_BOX);
+            __syncwarp();
+            if (lane < 128 / rows)
+              tma_load_4d(sk + st * CW_BOX + lane * rows * 128, &tmK, &k_full[st], h * 64,
+                          (x.key0 + k * 128 + lane * rows) & (a.c.page_size - 1), x.head, page);
+            ++issued;
+            if (++st == CW_KST) { st = 0; ph ^= 1u; }
           }
-          tma_load_4d(sk + w * CW_TILE + (lane & 1) * CW_BOX + box * rows * 128, &tmK, &k_full[w], (lane & 1) * 64,
-                      slot % ps, x.head, page);
+          page = next;
+          if (k > 0) continue;
+          for (int i = 0; i < n && ok; ++i) {                      // the pass's rows, after its first keys
+            if (!at_wait(&q_empty[slot], ((qph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            qph ^= 1u << slot;
+            loaded |= 1u << slot;
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[slot], (uint32_t)(a.R * a.G * 256));
+            __syncwarp();
+            if (lane < 2)
+              tma_load_4d(sq + slot * CW_TILE + lane * CW_BOX, &tmQ, &q_full[slot], lane * 64, 0, x.head,
+                          x.row0 + (x.q0 + p + i) * a.R);
+            slot = (slot + 1) % CW_SLOTS;
+          }
         }
       }
-      for (int i = 0; i < x.nq && ok; ++i) {
-        if (!at_wait(&q_empty[st], ph ^ 1u, ctl)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&q_full[st], (uint32_t)(a.R * a.G * 256));
-        __syncwarp();
-        if (lane < 2)
-          tma_load_4d(sq + st * CW_TILE + lane * CW_BOX, &tmQ, &q_full[st], lane * 64, 0, x.head,
-                      x.row0 + (x.q0 + i) * a.R);
-        ++issued;
-        if (++st == CW_QST) { st = 0; ph ^= 1u; }
-      }
     }
-    if (!ok && lane == 0) {   // let issued loads land before the CTA exits
-      for (uint32_t j = issued > CW_QST ? issued - CW_QST : 0; j < issued; ++j)
-        at_drain(&q_full[j % CW_QST], (j / CW_QST) & 1u);
-#pragma unroll
-      for (int w = 0; w < CW_KT; ++w)
-        if ((loaded >> w) & 1u) at_drain(&k_full[w], kph[w] ^ 1u);
+    if (*ctl.flag && lane == 0) {   // a wait ran out: let issued loads land before the CTA exits
+      for (uint32_t j = issued > CW_KST ? issued - CW_KST : 0; j < issued; ++j)
+        at_drain(&k_full[j % CW_KST], (j / CW_KST) & 1u);
+      for (uint32_t i = 0; i < CW_SLOTS; ++i)
+        if ((loaded >> i) & 1u) at_drain(&q_full[i], ((qph >> i) & 1u) ^ 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idesc0 = idesc_bf16(128, 0, false, false);
     constexpr uint64_t kTile = CW_TILE >> 4, kBox = CW_BOX >> 4;
     const uint32_t one = at_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     const uint64_t kd = sdesc_kmajor(smem_u32(sk)), qd = sdesc_kmajor(smem_u32(sq));
-    uint32_t kph = 0, sph = 0, st = 0, ph = 0;   // one phase bit per key tile
+    const uint64_t ld = at_sdesc_plain16(smem_u32(sl)), ones = ld + CW_SLOTS * (CW_STEP >> 4);
+    uint32_t qph = 0, sph = 0, slot0 = 0, st = 0, ph = 0;   // phase bits per slot
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
-      for (int i = 0; i < x.nq && ok; ++i) {
-        if (!at_wait(&q_full[st], ph, ctl)) { ok = false; break; }
-        for (int w = 0; w < x.tiles; ++w) {
-          if (i == 0) {
-            if (!at_wait(&k_full[w], (kph >> w) & 1u, ctl)) { ok = false; break; }
-            kph ^= 1u << w;
+      for (int p = 0; p < x.nq && ok; p += CW_SLOTS) {
+        const int n = min(CW_SLOTS, x.nq - p);
+        for (int k = 0; k < x.tiles && ok; ++k) {
+          uint32_t s[2];
+          for (int h = 0; h < 2 && ok; ++h) {
+            s[h] = st;
+            ok = at_wait(&k_full[st], ph, ctl);
+            if (++st == CW_KST) { st = 0; ph ^= 1u; }
           }
-          if (!at_wait(&s_empty[w], ((sph >> w) & 1u) ^ 1u, ctl)) { ok = false; break; }
-          sph ^= 1u << w;
-          tc_fence_after();
-          at_mma4_ss<2, 2>(tm + (uint32_t)(w * 128), kd + w * kTile, qd + st * kTile, idesc, 0u, one);
-          at_mma4_ss<2, 2>(tm + (uint32_t)(w * 128), kd + w * kTile + kBox, qd + st * kTile + kBox, idesc, 1u, one);
-          at_commit(&s_full[w], one);
-          if (i == x.nq - 1) at_commit(&k_empty[w], one);
+          for (int i = 0; i < n && ok; ++i) {
+            const uint32_t slot = (slot0 + i) % CW_SLOTS;
+            if (k == 0) {
+              if (!at_wait(&q_full[slot], (qph >> slot) & 1u, ctl) || !at_wait(&l_full[slot], (qph >> slot) & 1u, ctl)) {
+                ok = false;
+                break;
+              }
+              qph ^= 1u << slot;
+            }
+            if (!at_wait(&s_empty[slot], ((sph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            sph ^= 1u << slot;
+            tc_fence_after();
+            const int cols = min(a.R, x.rows - (x.q0 + p + i) * a.R) * a.G;
+            const uint32_t idesc = idesc0 | (uint32_t)((cols + 15) >> 4) << 18;   // columns / 8 at bit 17
+            const uint64_t q = qd + slot * kTile;
+            at_mma4_ss<2, 2>(tm + slot * 128u, kd + s[0] * kBox, q, idesc, 0u, one);
+            at_mma4_ss<2, 2>(tm + slot * 128u, kd + s[1] * kBox, q + kBox, idesc, 1u, one);
+            at_mma1_ss(tm + slot * 128u, ones, ld + slot * (CW_STEP >> 4), idesc, 1u, one);
+            at_commit(&s_full[slot], one);
+            if (k == x.tiles - 1) {
+              at_commit(&q_empty[slot], one);
+              at_commit(&l_empty[slot], one);
+            }
+          }
+          at_commit(&k_empty[s[0]], one);
+          at_commit(&k_empty[s[1]], one);
         }
-        at_commit(&q_empty[st], one);
-        if (++st == CW_QST) { st = 0; ph ^= 1u; }
+        slot0 = (slot0 + n) % CW_SLOTS;
       }
     }
-    if (!ok) {
+    if (*ctl.flag) {   // a wait ran out: let issued products end
       at_commit(drain, one);
       if (one) at_drain(drain, 0);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ log-sum-exp of the rows
-    uint32_t st = 0, ph = 0;
+    uint32_t lph = 0, slot = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
-      for (int i = 0; i < x.nq; ++i) {
-        float v[4];
+      auto values = [&](int i, float (&v)[4]) {           // -lse sqrt(128) of this lane's rows of tile i
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c = e * 32 + lane, r = c / a.G, row = (x.q0 + i) * a.R + r;
-          v[e] = INFINITY;
-          if (r < a.R && row < x.rows) {
+          v[e] = -1e30f;                                  // a row that adds nothing
+          if (i < x.nq && r < a.R && row < x.rows) {
             const float* at = a.lse + (int64_t)(x.head * a.G + c - r * a.G) * a.n_rows + x.row0 + row;
-            if (in_bounds<float>(a.lse, a.lse_elems, at, 1, a.err, 63)) v[e] = *at * 1.44269504088896340736f;
-            if (v[e] == -INFINITY) v[e] = INFINITY;   // a row that saw nothing adds nothing
+            if (in_bounds<float>(a.lse, a.lse_elems, at, 1, a.err, 63)) v[e] = *at * -11.313708498984761f;
+            if (v[e] == INFINITY) v[e] = -1e30f;          // it saw nothing
           }
         }
-        if (!at_wait(&l_empty[st], ph ^ 1u, ctl)) { ok = false; break; }
+      };
+      float v[4], ahead[2][4];                            // the next two tiles' arrive during the waits
+      values(0, v);
+      values(1, ahead[0]);
+      values(2, ahead[1]);
+      for (int i = 0; i < x.nq; ++i) {
+        if (i > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sl[st * 128 + e * 32 + lane] = v[e];
+          for (int e = 0; e < 4; ++e) {
+            v[e] = ahead[0][e];
+            ahead[0][e] = ahead[1][e];
+          }
+          values(i + 2, ahead[1]);
+        }
+        if (!at_wait(&l_empty[slot], ((lph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        lph ^= 1u << slot;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = e * 32 + lane;
+          const float hi = bf16_round(v[e]), mid = bf16_round(v[e] - hi), lo = v[e] - hi - mid;
+          *reinterpret_cast<uint4*>(sl + slot * CW_STEP + (c >> 3) * 256 + (c & 7) * 16) =
+              make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.0f), 0u, 0u);
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&l_full[st]);
-        if (++st == CW_QST) { st = 0; ph ^= 1u; }
+        if (lane == 0) mbar_arrive(&l_full[slot]);
+        slot = (slot + 1) % CW_SLOTS;
       }
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ exponentials and sums
-    const int w = (warp - 4) >> 2, qq = warp & 3;
-    const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), (uint32_t)(w * 128));
-    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    uint32_t st = 0, ph = 0, sph = 0;
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ sums to weights
+    uint32_t rph = 0, slot0 = 0, turn = 0;   // rph: a phase bit per slot and buffer; turn: a buffer bit per slot
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
-      const int key = x.key0 + w * 128 + qq * 32 + lane;
-      const bool mine = w < x.tiles && key < x.keys;
-      // rows of the sequence that see the key
-      const int see_lo = max(win_row_lo(a.w, min(key, x.keys - 1), x.keys) - x.pos0, 0);
-      const int see_hi = win_row_hi(a.w, min(key, x.keys - 1), x.keys) - x.pos0;
-      float sum = 0.0f;
-      for (int i = 0; i < x.nq; ++i) {
-        if (!at_wait(&l_full[st], ph, ctl)) { ok = false; break; }
-        if (w < x.tiles) {
-          if (!at_wait(&s_full[w], sph, ctl)) { ok = false; break; }
-          sph ^= 1u;
-          tc_fence_after();
-          const int at = (x.q0 + i) * a.R;            // the tile's first row
-          const int ncol = min(a.R, x.rows - at) * a.G;
-          // columns that see the key
-          const int ca = min(max(see_lo - at, 0), a.R) * a.G, cb = min(max(see_hi - at, 0) * a.G, ncol);
-          float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          for (int q4 = 0; q4 * 32 < ncol; ++q4) {
-            uint32_t s[32];
-            tmem_ld32(s_base + (uint32_t)(q4 * 32), s);
-            tmem_ld_wait(s);
-            const uint32_t see = win_bits(cb - q4 * 32) & ~win_bits(ca - q4 * 32);
-            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+      for (int p = 0; p < max(x.nq, 1) && ok; p += CW_SLOTS) {
+        const int n = min(CW_SLOTS, x.nq - p);   // 0: no row sees the unit, its weights stay
+        for (int k = 0; k < x.tiles && ok; ++k) {
+          int64_t at[4];
+          float w[4];
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!((see >> c) & 1u)) s[c] = __float_as_uint(-INFINITY);
-            }
-            const float4* l4 = reinterpret_cast<const float4*>(sl + st * 128 + q4 * 32);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 l = l4[c >> 2];
-              const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2,
-                                           make_float2(-l.x, -l.y));
-              const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2,
-                                           make_float2(-l.z, -l.w));
-              acc[0] = __fadd2_rn(acc[0], make_float2(at_ex2(z0.x), at_ex2(z0.y)));
-              acc[1] = __fadd2_rn(acc[1], make_float2(at_ex2(z1.x), at_ex2(z1.y)));
+          for (int e = 0; e < 4; ++e) {
+            const int key = x.key0 + k * 128 + e * 32 + lane;
+            at[e] = -1;
+            w[e] = 0.0f;
+            if (key < x.keys) {
+              const int page = page_of(a.c, x.seq, key);
+              if (page >= 0 && page < a.c.n_pages) {
+                at[e] = page_row(a.c, page, x.head, key);
+                if (!in_bounds<float>(a.out, a.page_rows, a.out + at[e], 1, a.err, 64)) at[e] = -1;
+              } else if (p == 0 && max(win_row_lo(a.w, key, x.keys), x.pos0) < win_row_hi(a.w, key, x.keys)) {
+                record_error(a.err, DEVERR_INDEX);   // a page that some row sees
+              }
+              // later passes add to what the first one wrote
+              if (at[e] >= 0) w[e] = p > 0 ? a.out[at[e]] : (a.in != nullptr ? a.in[at[e]] : 0.0f);
             }
           }
-          sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[w]);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int i = 0; i < n; ++i) {
+            const uint32_t slot = (slot0 + i) % CW_SLOTS, b = slot * CW_RED + ((turn >> slot) & 1u);
+            if (!at_wait(&r_full[b], (rph >> b) & 1u, ctl)) { ok = false; break; }
+            rph ^= 1u << b;
+            turn ^= 1u << slot;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += red[b * 128 + e * 32 + lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&r_empty[b]);
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at[e] >= 0) a.out[at[e]] = w[e] + sum[e];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&l_empty[st]);
-        if (++st == CW_QST) { st = 0; ph ^= 1u; }
+        if (n > 0) slot0 = (slot0 + n) % CW_SLOTS;
       }
-      if (ok && mine) {
-        const int page = page_of(a.c, x.seq, key);
-        if (page >= 0 && page < a.c.n_pages) {
-          const int64_t at = page_row(a.c, page, x.head, key);
-          if (in_bounds<float>(a.out, a.page_rows, a.out + at, 1, a.err, 64))
-            a.out[at] = (a.in != nullptr ? a.in[at] : 0.0f) + sum;
-        } else if (see_lo < min(see_hi, x.rows)) {
-          record_error(a.err, DEVERR_INDEX);
+    }
+  } else {
+    // ------------------------------------------------------------ exponentials and sums
+    const uint32_t odd = (uint32_t)(warp - 4) >> 2;   // slots of this parity
+    const int qq = warp & 3;
+    const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), 0);
+    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+    uint32_t slot0 = 0, sph = 0, rph = 0, turn = 0;   // a bit per slot (rph: and buffer)
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const CwUnit x = cw_unit(a, pre, per_head, u);
+      for (int p = 0; p < x.nq && ok; p += CW_SLOTS) {
+        const int n = min(CW_SLOTS, x.nq - p);
+        for (int k = 0; k < x.tiles && ok; ++k) {
+          const int key = min(x.key0 + k * 128 + qq * 32 + lane, x.keys - 1), unit = win_unit(a.w, key);
+          const int see_lo = win_row_lo_of(a.w, unit, x.keys) - x.pos0;   // rows that see the key
+          const int see_hi = win_row_hi_of(a.w, unit, key, x.keys) - x.pos0;
+          for (int i = 0; i < n; ++i) {
+            const uint32_t slot = (slot0 + i) % CW_SLOTS;
+            if ((slot & 1u) != odd) continue;
+            const int at = (x.q0 + p + i) * a.R;            // the slot's first row
+            const int ncol = min(a.R, x.rows - at) * a.G;
+            // columns that see the key
+            const int ca = min(max(see_lo - at, 0), a.R) * a.G, cb = min(min(max(see_hi - at, 0), a.R) * a.G, ncol);
+            if (!at_wait(&s_full[slot], (sph >> slot) & 1u, ctl)) { ok = false; break; }
+            sph ^= 1u << slot;
+            tc_fence_after();
+            float2 acc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
+            const uint32_t s_at = s_base + slot * 128u;
+            if (ncol <= 32) cw_sums<1>(s_at, ca, cb, sl2, acc, &s_empty[slot]);
+            else cw_sums<4>(s_at, ca, cb, sl2, acc, &s_empty[slot]);
+            const uint32_t b = slot * CW_RED + ((turn >> slot) & 1u);
+            if (!at_wait(&r_empty[b], ((rph >> b) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            rph ^= 1u << b;
+            turn ^= 1u << slot;
+            const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+            red[b * 128 + qq * 32 + lane] = sum.x + sum.y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&r_full[b]);
+          }
         }
+        slot0 = (slot0 + n) % CW_SLOTS;
       }
     }
   }
@@ -431,7 +555,31 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
     const float* w = a.weights + page_row(a.from, page, head, slot);
     return in_bounds<float>(a.weights, a.from_rows, w, 1, a.err, 65) ? weight_key(*w) : 0u;
   };
-  for (int i = m0 + tid; i < min(m1, m0 + held); i += EV_THREADS) keys[i - m0] = weight_at(i);
+  // four slots a thread at a time: table entries, then weights, in flight together
+  // (one by one: 25 us of a call of 15,860 slots)
+  for (int i0 = m0 + tid; i0 < min(m1, m0 + held); i0 += 4 * EV_THREADS) {
+    int page[4];
+    float w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * EV_THREADS;
+      page[e] = i < min(m1, m0 + held) ? page_of(a.from, s, i) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * EV_THREADS;
+      w[e] = NAN;
+      if (page[e] < 0 || page[e] >= a.from.n_pages) {
+        if (i < min(m1, m0 + held)) record_error(a.err, DEVERR_INDEX);
+        continue;
+      }
+      const float* at = a.weights + page_row(a.from, page[e], head, i);
+      if (in_bounds<float>(a.weights, a.from_rows, at, 1, a.err, 65)) w[e] = *at;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i0 + e * EV_THREADS < min(m1, m0 + held)) keys[i0 + e * EV_THREADS - m0] = weight_key(w[e]);
+  }
   __syncthreads();
   auto key_at = [&](int slot) -> uint32_t { return slot - m0 < held ? keys[slot - m0] : weight_at(slot); };
   uint32_t prefix = 0, mask = 0;
@@ -513,7 +661,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
 }
 
 // Moves the kept rows: a warp a row, K by the lower and V by the upper half of
-// its lanes, eight rows in flight.  Bound by HBM.
+// its lanes, eight rows in flight.  Bound by HBM: %EVICT%
 namespace {
 constexpr int EM_ROWS = 8;   // rows of a warp
 }
@@ -525,36 +673,34 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   const int32_t* kept = a.kept + ((int64_t)s * a.from.n_kv_heads + head) * a.budget;
   const __nv_bfloat16* src = lane < 16 ? a.k_from : a.v_from;
   __nv_bfloat16* dst = lane < 16 ? a.k_to : a.v_to;
-  int64_t from[EM_ROWS], to[EM_ROWS];
-  uint4 row[EM_ROWS];
-  float w[EM_ROWS];
-#pragma unroll
-  for (int e = 0; e < EM_ROWS; ++e) {
-    const int d = d0 + e, slot = d < a.budget ? kept[d] : -1;
-    from[e] = to[e] = -1;
-    if (slot < 0) continue;
-    const int pf = page_of(a.from, s, slot), pt = page_of(a.to, s, d);
-    if (pf < 0 || pf >= a.from.n_pages || pt < 0 || pt >= a.to.n_pages) {
-      if (lane == 0) record_error(a.err, DEVERR_INDEX);
-      continue;
+  // lane e % 8 finds row e's places
+  int64_t from_row = -1, to_row = -1;
+  {
+    const int d = d0 + (lane & (EM_ROWS - 1)), slot = d < a.budget ? kept[d] : -1;
+    if (slot >= 0) {
+      const int pf = page_of(a.from, s, slot), pt = page_of(a.to, s, d);
+      if (pf >= 0 && pf < a.from.n_pages && pt >= 0 && pt < a.to.n_pages) {
+        from_row = page_row(a.from, pf, head, slot);
+        to_row = page_row(a.to, pt, head, d);
+      } else if (lane < EM_ROWS) {
+        record_error(a.err, DEVERR_INDEX);
+      }
     }
-    from[e] = page_row(a.from, pf, head, slot);
-    to[e] = page_row(a.to, pt, head, d);
-    if (!in_bounds<__nv_bfloat16>(src, a.from_rows * 128, src + from[e] * 128, 128, a.err, 66) ||
-        !in_bounds<__nv_bfloat16>(dst, a.to_rows * 128, dst + to[e] * 128, 128, a.err, 67))
-      to[e] = -1;
   }
+  const bool moves = to_row >= 0 && in_bounds<__nv_bfloat16>(src, a.from_rows * 128, src + from_row * 128, 128, a.err, 66) &&
+                     in_bounds<__nv_bfloat16>(dst, a.to_rows * 128, dst + to_row * 128, 128, a.err, 67);
+  const unsigned rows = __ballot_sync(0xffffffffu, moves);
+  uint4 row[EM_ROWS];
 #pragma unroll
   for (int e = 0; e < EM_ROWS; ++e) {
-    if (to[e] < 0) continue;
-    row[e] = reinterpret_cast<const uint4*>(src + from[e] * 128)[lane & 15];
-    if (lane == 0 && a.weights_to != nullptr) w[e] = a.weights[from[e]];
+    const int64_t at = __shfl_sync(0xffffffffu, from_row, e);
+    if ((rows >> e) & 1u) row[e] = __ldcs(reinterpret_cast<const uint4*>(src + at * 128) + (lane & 15));
   }
+  if (moves && lane < EM_ROWS && a.weights_to != nullptr) a.weights_to[to_row] = a.weights[from_row];
 #pragma unroll
   for (int e = 0; e < EM_ROWS; ++e) {
-    if (to[e] < 0) continue;
-    reinterpret_cast<uint4*>(dst + to[e] * 128)[lane & 15] = row[e];
-    if (lane == 0 && a.weights_to != nullptr) a.weights_to[to[e]] = w[e];
+    const int64_t at = __shfl_sync(0xffffffffu, to_row, e);
+    if ((rows >> e) & 1u) reinterpret_cast<uint4*>(dst + at * 128)[lane & 15] = row[e];
   }
 }
 
@@ -575,16 +721,28 @@ cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   if (!tmem_exclusive(CW_SMEM)) return cudaErrorNotSupported;
   cudaError_t e = cudaFuncSetAttribute(cache_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CW_SMEM);
   if (e != cudaSuccess) return e;
-  // units of four key tiles where they fill the SMs at the tables' width
+  // Units of one to sixteen key tiles: the fewest rounds of the grid, a tile of rows
+  // that a unit loads counted as half a product (at the tables' width and the
+  // sequences' average rows).
   const int64_t tiles = ((int64_t)a.c.table_width * a.c.page_size + 127) / 128;
   const int64_t lists = (int64_t)a.c.n_kv_heads * a.c.n_seqs;
-  a.tiles = CW_KT;
-  while (a.tiles > 1 && lists * ((tiles + a.tiles - 1) / a.tiles) < num_sms()) a.tiles >>= 1;
-  const int64_t units = lists * ((tiles + a.tiles - 1) / a.tiles);
+  const int64_t per_seq = (a.n_rows + a.c.n_seqs - 1) / a.c.n_seqs;
+  const double nq = (double)((per_seq + a.R - 1) / a.R);
+  double best = 0.0;
+  int64_t units = 0;
+  for (int t = 1; t <= 16; ++t) {
+    const int64_t n = lists * ((tiles + t - 1) / t), rounds = (n + num_sms() - 1) / num_sms();
+    const double cost = (double)rounds * ((double)t * nq + 0.5 * nq + 0.5);
+    if (t == 1 || cost < best) {
+      best = cost;
+      a.tiles = t;
+      units = n;
+    }
+  }
   const int grid = (int)(units < num_sms() ? units : num_sms());
   e = launch_kernel(cache_weights_kernel, dim3((unsigned)grid), dim3(CW_THREADS), CW_SMEM, stream, tmQ, tmK, a);
   if (e != cudaSuccess) return e;
-  set_kernel_info("cache_weights_kernel tcgen05.mma.cta_group::1.kind::f16 key_tiles=%dx128 rows/tile=%d shared=%d acc=f32 "
+  set_kernel_info("cache_weights_kernel tcgen05.mma.cta_group::1.kind::f16 unit=%dx128 keys rows/tile=%d shared=%d acc=f32 "
                   "grid=%d", a.tiles, a.R, a.G, grid);
   return cudaGetLastError();
 }
