@@ -520,6 +520,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 }  // namespace
 
+// HELD: shared memory holds all keys; otherwise the first `held`.
+template <bool HELD>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArgs a, int held) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem_raw);
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
       if (i0 + e * EV_THREADS < min(m1, m0 + held)) keys[i0 + e * EV_THREADS - m0] = weight_key(w[e]);
   }
   __syncthreads();
-  auto key_at = [&](int slot) -> uint32_t { return slot - m0 < held ? keys[slot - m0] : weight_at(slot); };
+  auto key_at = [&](int slot) -> uint32_t { return HELD || slot - m0 < held ? keys[slot - m0] : weight_at(slot); };
   uint32_t prefix = 0, mask = 0;
   if (want > 0) {
 #pragma unroll 1
@@ -590,10 +592,10 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
       for (int b = tid; b < EV_BINS; b += EV_THREADS) hist[b] = 0;
       __syncthreads();
       const uint32_t digit = pass == 2 ? 1023u : 2047u;
-      for (int i0 = m0; i0 < m1; i0 += EV_THREADS) {
-        const int i = i0 + tid;
-        const uint32_t key = i < m1 ? key_at(i) : 0u;
-        if (i < m1 && (key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
+#pragma unroll 4
+      for (int i = m0 + tid; i < m1; i += EV_THREADS) {
+        const uint32_t key = key_at(i);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
       }
       __syncthreads();
       // from the highest bin down: thread t holds bins 2047 - 2t and 2046 - 2t
@@ -606,8 +608,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
       }
       if (lane == 31) misc[warp] = sum;
       __syncthreads();
-      uint32_t before = sum - h0 - h1;
-      for (int w = 0; w < warp; ++w) before += misc[w];
+      const uint32_t warps = __reduce_add_sync(0xffffffffu, lane < warp ? misc[lane] : 0u);
+      const uint32_t before = warps + sum - h0 - h1;
       if (before < want && want <= before + h0) {
         misc[32] = (uint32_t)(EV_BINS - 1 - 2 * tid);
         misc[33] = want - before;
@@ -633,6 +635,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
     return k > prefix ? 2 : (k == prefix ? 1 : 0);
   };
   uint32_t above = 0, equal = 0;
+#pragma unroll 4
   for (int i0 = r0; i0 < r1; i0 += 32) {
     const int c = classify(i0 + lane);
     above += __popc(__ballot_sync(0xffffffffu, c == 2));
@@ -643,12 +646,10 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
     hist[32 + warp] = equal;
   }
   __syncthreads();
-  uint32_t out = 0, seen = 0;
-  for (int w = 0; w < warp; ++w) {
-    out += hist[w];
-    seen += hist[32 + w];
-  }
+  uint32_t out = __reduce_add_sync(0xffffffffu, lane < warp ? hist[lane] : 0u);
+  uint32_t seen = __reduce_add_sync(0xffffffffu, lane < warp ? hist[32 + lane] : 0u);
   out += min(seen, want);
+#pragma unroll 4
   for (int i0 = r0; i0 < r1; i0 += 32) {
     const int i = i0 + lane, c = classify(i);
     const unsigned eq = __ballot_sync(0xffffffffu, c == 1), below = (1u << lane) - 1u;
@@ -751,10 +752,10 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t slots = (int64_t)a.from.table_width * a.from.page_size;
   const int held = (int)(slots < EV_KEYS ? slots : EV_KEYS);
   const size_t smem = EV_SMEM + (size_t)held * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       EV_SMEM + EV_KEYS * 4);
+  const auto kernel = held == slots ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_SMEM + EV_KEYS * 4);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(evict_select_kernel, dim3((unsigned)a.from.n_kv_heads, (unsigned)a.from.n_seqs), dim3(EV_THREADS),
+  e = launch_kernel(kernel, dim3((unsigned)a.from.n_kv_heads, (unsigned)a.from.n_seqs), dim3(EV_THREADS),
                     smem, stream, a, held);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.budget + 8 * EM_ROWS - 1) / (8 * EM_ROWS)), (unsigned)a.from.n_kv_heads,
