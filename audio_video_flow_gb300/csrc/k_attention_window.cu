@@ -46,6 +46,7 @@
 #include "attention_device.cuh"
 #include "h3_internal.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace h3 {
@@ -135,9 +136,9 @@ __device__ __forceinline__ int aw_group(const AttnWinArgs& a, const AwSeq& q, in
 struct AwBorder {
   int each, rest;
   uint64_t inv;                  // 2^32 / gangs + 1; rest g is below 2^16
-  __device__ __forceinline__ AwBorder(const AttnWinArgs& a, int all)
-      : each((int)aw_div(all, a.gangs)), rest(all - each * a.gangs), inv(a.gangs_inv) {}
-  __device__ __forceinline__ int at(int g) const { return each * g + (int)(((uint32_t)(rest * g) * inv) >> 32); }
+  __host__ __device__ __forceinline__ AwBorder(int all, int gangs, uint64_t gangs_inv)
+      : each(all / gangs), rest(all - each * gangs), inv(gangs_inv) {}
+  __host__ __device__ __forceinline__ int at(int g) const { return each * g + (int)(((uint32_t)(rest * g) * inv) >> 32); }
 };
 // Where a run begins: `off` of the weight n of group `group` of sequence `seq`,
 // head `head`; off = n: at the end of that group.
@@ -146,6 +147,26 @@ struct AwShared {
   AwLoc loc[2];
   int total;
 };
+// A document's runs are known to the host, which passes where they begin (the
+// device's own setup: 3 us of a call).
+constexpr int kMaxGangs = 160;
+template <int MODE>
+struct AwRuns {};
+template <>
+struct AwRuns<0> {
+  int all;
+  struct { int head, group, off, n, x; } begin[kMaxGangs + 1];
+};
+// The move of a run's end to a group's that is near.
+__host__ __device__ __forceinline__ void aw_snap(int& off, int n, int& x) {
+  if (off <= kSnap) {
+    x -= off;
+    off = 0;
+  } else if (n - off <= kSnap) {
+    x += n - off;
+    off = n;
+  }
+}
 
 __device__ __forceinline__ int warp_prefix(int v) {   // inclusive
 #pragma unroll
@@ -188,13 +209,7 @@ __device__ __forceinline__ AwLoc aw_locate(const AttnWinArgs& a, const int* pre,
     }
     y -= __shfl_sync(0xffffffffu, sum, 31);
   }
-  if (l.off <= kSnap) {
-    l.x -= l.off;
-    l.off = 0;
-  } else if (l.n - l.off <= kSnap) {
-    l.x += l.n - l.off;
-    l.off = l.n;
-  }
+  aw_snap(l.off, l.n, l.x);
   return l;
 }
 
@@ -356,7 +371,8 @@ __device__ __forceinline__ float aw_max(const uint32_t (&s)[32]) {
 template <int MODE>
 __global__ void __launch_bounds__(AW_THREADS, 1)
     attention_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnWinArgs a) {
+                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnWinArgs a,
+                            const __grid_constant__ AwRuns<MODE> runs) {
   // no static shared memory: the dynamic part starts at a multiple of 1024
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   AwSmem sm;
@@ -419,58 +435,68 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   griddep_wait();
 
-  // ---- the run of this CTA: weights of each sequence, their prefix sums (in the
+  // ---- the run of this CTA.  A cache: weights of each sequence, their prefix sums (in the
   // K ring, before its first load), both ends of the run
-  int* pre = reinterpret_cast<int*>(sm.k);
-  const int ns = a.c.n_seqs;
-  constexpr int kWarps = AW_THREADS / 32;
-  if (ns == 1) {   // the whole CTA sums one sequence
-    const AwSeq q = aw_seq<PAGED>(a, 0);
-    if (PAGED && q.keys < 0 && blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, DEVERR_INDEX);
-    int n = 0;
-    for (int p = threadIdx.x, ng = aw_groups(a, q.rows); p < ng; p += AW_THREADS) n += aw_group(a, q, p);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) pre[1 + warp] = n;
-    __syncthreads();
-    n = lane < kWarps ? pre[1 + lane] : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (threadIdx.x == 0) {
-      pre[0] = 0;
-      sh->total = n;
+  int all = 0;
+  const int gang = (int)aw_div(blockIdx.x, a.M);
+  if constexpr (MODE == AW_DOC) {
+    all = runs.all;
+    if (threadIdx.x < 2) {
+      const auto& r = runs.begin[gang + threadIdx.x];
+      sh->loc[threadIdx.x] = {r.head, 0, r.group, r.off, r.n, r.x};
     }
   } else {
-    for (int s = threadIdx.x; s < ns; s += AW_THREADS) {
-      const AwSeq q = aw_seq<PAGED>(a, s);
-      if (PAGED && q.keys < 0 && blockIdx.x == 0) record_error(a.err, DEVERR_INDEX);
-      const int ng = aw_groups(a, q.rows);
-      pre[s] = ng > 2 ? -1 : (ng > 0 ? aw_group(a, q, 0) : 0) + (ng > 1 ? aw_group(a, q, 1) : 0);
-    }
-    __syncthreads();
-    for (int s = warp; s < ns; s += kWarps) {
-      if (pre[s] >= 0) continue;
-      const AwSeq q = aw_seq<PAGED>(a, s);
+    int* pre = reinterpret_cast<int*>(sm.k);
+    const int ns = a.c.n_seqs;
+    constexpr int kWarps = AW_THREADS / 32;
+    if (ns == 1) {   // the whole CTA sums one sequence
+      const AwSeq q = aw_seq<PAGED>(a, 0);
+      if (PAGED && q.keys < 0 && blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, DEVERR_INDEX);
       int n = 0;
-      for (int p = lane, ng = aw_groups(a, q.rows); p < ng; p += 32) n += aw_group(a, q, p);
+      for (int p = threadIdx.x, ng = aw_groups(a, q.rows); p < ng; p += AW_THREADS) n += aw_group(a, q, p);
       n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) pre[s] = n;
+      if (lane == 0) pre[1 + warp] = n;
+      __syncthreads();
+      n = lane < kWarps ? pre[1 + lane] : 0;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (threadIdx.x == 0) {
+        pre[0] = 0;
+        sh->total = n;
+      }
+    } else {
+      for (int s = threadIdx.x; s < ns; s += AW_THREADS) {
+        const AwSeq q = aw_seq<PAGED>(a, s);
+        if (PAGED && q.keys < 0 && blockIdx.x == 0) record_error(a.err, DEVERR_INDEX);
+        const int ng = aw_groups(a, q.rows);
+        pre[s] = ng > 2 ? -1 : (ng > 0 ? aw_group(a, q, 0) : 0) + (ng > 1 ? aw_group(a, q, 1) : 0);
+      }
+      __syncthreads();
+      for (int s = warp; s < ns; s += kWarps) {
+        if (pre[s] >= 0) continue;
+        const AwSeq q = aw_seq<PAGED>(a, s);
+        int n = 0;
+        for (int p = lane, ng = aw_groups(a, q.rows); p < ng; p += 32) n += aw_group(a, q, p);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) pre[s] = n;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        int carry = 0;
+        for (int s0 = 0; s0 < ns; s0 += 32) {
+          const int mine = s0 + lane < ns ? pre[s0 + lane] : 0, sum = warp_prefix(mine);
+          if (s0 + lane < ns) pre[s0 + lane] = carry + sum - mine;
+          carry += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) sh->total = carry;
+      }
     }
     __syncthreads();
-    if (warp == 0) {
-      int carry = 0;
-      for (int s0 = 0; s0 < ns; s0 += 32) {
-        const int mine = s0 + lane < ns ? pre[s0 + lane] : 0, sum = warp_prefix(mine);
-        if (s0 + lane < ns) pre[s0 + lane] = carry + sum - mine;
-        carry += __shfl_sync(0xffffffffu, sum, 31);
-      }
-      if (lane == 0) sh->total = carry;
+    const int per_head = sh->total;
+    all = per_head * a.c.n_kv_heads;
+    if (warp < 2 && all > 0) {
+      const AwLoc l = aw_locate<PAGED>(a, pre, per_head, AwBorder(all, a.gangs, a.gangs_inv).at(gang + warp));
+      if (lane == 0) sh->loc[warp] = l;
     }
-  }
-  __syncthreads();
-  const int per_head = sh->total, all = per_head * a.c.n_kv_heads;
-  const int gang = (int)aw_div(blockIdx.x, a.M);
-  if (warp < 2 && all > 0) {
-    const AwLoc l = aw_locate<PAGED>(a, pre, per_head, AwBorder(a, all).at(gang + warp));
-    if (lane == 0) sh->loc[warp] = l;
   }
   fence_proxy_async_smem();   // the sums were read; the ring's loads may overwrite them
   tc_fence_before();
@@ -549,7 +575,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           if (g.cnt < p.n) {
             // the gangs whose runs hold the group's beginning and its end: the last
             // whose border, as it is after the move, is no later
-            const AwBorder border(a, all);
+            const AwBorder border(all, a.gangs, a.gangs_inv);
             int first = gang, last = gang;
             while (off > 0 && border.at(first) > x0 + kSnap) --first;
             while (last + 1 < a.gangs && border.at(last + 1) < x0 + weight - kSnap) ++last;
@@ -1063,6 +1089,46 @@ __global__ void __launch_bounds__(256) attention_window_start_kernel(int* ctrl, 
 // to cost 0.12 / M^2.
 size_t attn_win_ctrl_bytes(int ctas) { return ((size_t)ctas * kCtrl * 4 + 255) & ~size_t(255); }
 size_t attn_win_part_bytes(int ctas, int rows) { return (size_t)ctas * 4 * rows * kPartRow * 4; }
+namespace {
+// Where the runs of a document's gangs begin.
+void aw_doc_runs(const AttnWinArgs& a, const AttnWinPlan& p, AwRuns<AW_DOC>* runs) {
+  const int units = (a.n_rows + a.U - 1) / a.U, groups = (units + a.M - 1) / a.M;
+  auto tiles = [&](int unit) -> int {   // aw_unit's n
+    const int pos0 = unit * a.U, last = std::min(pos0 + a.U, a.n_rows) - 1;
+    const int lo = win_lo(a.w, pos0, a.n_rows), first = std::min(a.w.first, win_lo(a.w, last, a.n_rows));
+    return std::min((first + 127) >> 7, lo >> 7) + ((win_hi(a.w, last, a.n_rows) + 127) >> 7) - (lo >> 7);
+  };
+  auto weight = [&](int g) -> int {     // aw_weight
+    const int p0 = g * a.M, p1 = std::min(p0 + a.M, units) - 1;
+    return a.M == 1 ? tiles(p0) : ((tiles(p0) + tiles(p1)) * (p1 - p0 + 1) + 2 * a.M - 1) / (2 * a.M);
+  };
+  int64_t per_head = 0;
+  for (int g = 0; g < groups; ++g) per_head += weight(g);
+  runs->all = (int)(per_head * a.c.n_kv_heads);
+  const AwBorder border(runs->all, a.gangs, a.gangs_inv);
+  int g = 0, at = 0, n = weight(0), head = 0;         // the group that holds a border, its beginning in the head
+  for (int i = 0; i <= p.gangs; ++i) {
+    auto& r = runs->begin[i];
+    r = {a.c.n_kv_heads, 0, 0, 0, border.at(i)};
+    for (; head < r.x / per_head && head < a.c.n_kv_heads; ++head) {
+      g = at = 0;
+      n = weight(0);
+    }
+    if (head == a.c.n_kv_heads) continue;
+    const int y = r.x - (int)(head * per_head);
+    while (at + n <= y) {
+      at += n;
+      n = weight(++g);
+    }
+    r.head = head;
+    r.group = g;
+    r.n = n;
+    r.off = y - at;
+    aw_snap(r.off, r.n, r.x);
+  }
+}
+}  // namespace
+
 bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_seqs, int G, int64_t max_keys, bool paged,
                    const WindowArgs& w) {
   const int64_t R = 128 / G;
@@ -1079,7 +1145,7 @@ bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_s
   const __int128 all = (__int128)units * (tiles + 1) * kv_heads;
   if (all >= (__int128)1 << 31) return false;        // the runs are counted in 32 bits
   const int64_t sms = num_sms(), work = units * (tiles > 0 ? tiles : 1) * kv_heads;
-  const int ctas = (int)(work < sms ? work : sms);
+  const int ctas = (int)std::min<int64_t>(std::min(work, sms), kMaxGangs);
   const int64_t per_seq = ((n_rows + n_seqs - 1) / n_seqs + p->U - 1) / p->U;   // units of a sequence, on average
   double best = 0.0;
   p->M = 1;
@@ -1102,35 +1168,43 @@ bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_s
   return true;
 }
 
-cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream) {
-  static_assert(tmem_footprint_exclusive(AwPlan<AW_DOC>::smem) && tmem_footprint_exclusive(AwPlan<AW_CHUNK>::smem) &&
-                    tmem_footprint_exclusive(AwPlan<AW_ROWS>::smem),
-                "an attention CTA must hold its SM's TMEM alone");
-  const int smem = p.mode == AW_DOC ? AwPlan<AW_DOC>::smem
-                                    : (p.mode == AW_CHUNK ? AwPlan<AW_CHUNK>::smem : AwPlan<AW_ROWS>::smem);
+template <int MODE>
+static cudaError_t launch_mode(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnWinArgs& a,
+                               const AwRuns<MODE>& runs, int ctas, cudaStream_t stream) {
+  const auto kernel = attention_window_kernel<MODE>;
+  constexpr int smem = AwPlan<MODE>::smem;
+  static_assert(tmem_footprint_exclusive(smem), "an attention CTA must hold its SM's TMEM alone");
   if (!tmem_exclusive(smem)) return cudaErrorNotSupported;
-  const auto kernel = p.mode == AW_DOC ? attention_window_kernel<AW_DOC>
-                                       : (p.mode == AW_CHUNK ? attention_window_kernel<AW_CHUNK>
-                                                             : attention_window_kernel<AW_ROWS>);
   // the register split waits for registers that only AW_REGS at launch leave
-  static bool regs_ok[3] = {false, false, false};
-  if (!regs_ok[p.mode]) {
+  static const cudaError_t fits = [kernel] {
     cudaFuncAttributes attr;
     const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != AW_REGS) return cudaErrorNotSupported;
-    regs_ok[p.mode] = true;
-  }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : (attr.numRegs == AW_REGS ? cudaSuccess : cudaErrorNotSupported);
+  }();
+  if (fits != cudaSuccess) return fits;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3((unsigned)ctas), dim3(AW_THREADS), (size_t)smem, stream, tmQ, tmK, tmV, a, runs);
+}
+
+cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream) {
   if (p.split) {
     const int words = p.ctas * kCtrl;
-    e = launch_kernel(attention_window_start_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, a.ctrl,
-                      words);
+    const cudaError_t e = launch_kernel(attention_window_start_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0,
+                                        stream, a.ctrl, words);
     if (e != cudaSuccess) return e;
   }
-  e = launch_kernel(kernel, dim3((unsigned)p.ctas), dim3(AW_THREADS), (size_t)smem, stream, tmQ, tmK, tmV, a);
+  cudaError_t e;
+  if (p.mode == AW_DOC) {
+    AwRuns<AW_DOC> runs;
+    aw_doc_runs(a, p, &runs);
+    e = launch_mode<AW_DOC>(tmQ, tmK, tmV, a, runs, p.ctas, stream);
+  } else if (p.mode == AW_CHUNK) {
+    e = launch_mode<AW_CHUNK>(tmQ, tmK, tmV, a, {}, p.ctas, stream);
+  } else {
+    e = launch_mode<AW_ROWS>(tmQ, tmK, tmV, a, {}, p.ctas, stream);
+  }
   if (e != cudaSuccess) return e;
   set_kernel_info("attention_window_kernel<%s> tcgen05.mma.cta_group::1.kind::f16 unit=%d rows kv_tile=128 shared=%d "
                   "acc=f32 P-in-TMEM lazy-rescale=%g grid=%d gang=%d%s",
