@@ -162,4 +162,15 @@ __device__ __forceinline__ uint32_t win_bits(int x) {
   return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
 }
 
+// ---------------------------------------------------------------------------
+// Sequences of a cache
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int64_t cache_slots(const CacheArgs& c) { return (int64_t)c.table_width * c.page_size; }
+// Whether a sequence's new rows and length are in range: rows that begin where no
+// earlier sequence's do and end within n_rows, and slots for all of them.
+__device__ __forceinline__ bool cache_seq_ok(const CacheArgs& c, int n_rows, int s) {
+  const int before = s > 0 ? c.start[s - 1] : 0, b = c.start[s], e = c.start[s + 1], len = c.length[s];
+  return b >= before && b >= 0 && e >= b && e <= n_rows && len >= e - b && (int64_t)len <= cache_slots(c);
+}
+
 }  // namespace h3

@@ -1586,16 +1586,22 @@ size_t attn_win_ws_bytes(int64_t n_rows, int64_t n_heads, int64_t n_kv_heads) {
   return al256(attn_win_ctrl_bytes(ctas) + attn_win_part_bytes(ctas, (int)(n_rows < R ? n_rows : R) * G));
 }
 
-// The call over one document (c null) or a cache, its arguments checked.
-h3_status run_attention_window(const h3_window& w, const h3_cache* c, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
-                               const int32_t* start, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               void* o, float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream) {
-  AttnWinArgs a{};
-  AttnWinPlan p{};
+// How a call over one document (c null) or a cache runs, and whether its workspace
+// is large enough.
+h3_status plan_attention_window(const h3_window& w, const h3_cache* c, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                                size_t ws_bytes, AttnWinPlan* p) {
   const int64_t seqs = c ? c->n_seqs : 1, keys = c ? (int64_t)c->table_width * c->page_size : n_rows;
+  if (!attn_win_plan(p, n_rows, n_kv_heads, seqs, n_heads / n_kv_heads, keys, c != nullptr, window_args(w)))
+    return H3_ERR_UNSUPPORTED;
+  return ws_bytes < attn_win_ws_bytes(n_rows, n_heads, n_kv_heads) ? H3_ERR_WORKSPACE : H3_OK;
+}
+
+// The call, its arguments checked.
+h3_status run_attention_window(const AttnWinPlan& p, const h3_window& w, const h3_cache* c, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                               const int32_t* start, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               void* o, float* lse, void* workspace, cudaStream_t stream) {
+  AttnWinArgs a{};
   a.w = window_args(w);
-  if (!attn_win_plan(&p, n_rows, n_kv_heads, seqs, n_heads / n_kv_heads, keys, c != nullptr, a.w)) return H3_ERR_UNSUPPORTED;
-  if (ws_bytes < attn_win_ws_bytes(n_rows, n_heads, n_kv_heads)) return H3_ERR_WORKSPACE;
   if (c) {
     a.c = cache_args(*c, start);
   } else {
@@ -1643,14 +1649,16 @@ h3_status h3_attention_window(const h3_window* window, int32_t n_rows, int32_t n
   if (!al16(q) || !al16(k) || !al16(v) || !al16(o) || !al4(lse_opt) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return H3_ERR_ALIGN;
   if (o == q || o == k || o == v || o == workspace || lse_opt == o || lse_opt == workspace) return H3_ERR_SHAPE;
+  AttnWinPlan plan{};
+  if ((s = plan_attention_window(*window, nullptr, n_rows, n_heads, n_kv_heads, ws_bytes, &plan)) != H3_OK) return s;
   CUtensorMap tq, tk, tv;
   const uint32_t G = (uint32_t)(n_heads / n_kv_heads);
   if (!make_tmap_q_shared(&tq, q, n_rows, n_kv_heads, G, q_row_stride_elems, q_head_stride_elems, 128 / G) ||
       !make_tmap_qkv(&tk, k, n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems, 128) ||
       !make_tmap_qkv(&tv, v, n_rows, n_kv_heads, kv_row_stride_elems, kv_head_stride_elems, 128))
     return H3_ERR_CUDA;
-  return run_attention_window(*window, nullptr, n_rows, n_heads, n_kv_heads, nullptr, tq, tk, tv, o, lse_opt, workspace,
-                              ws_bytes, stream);
+  return run_attention_window(plan, *window, nullptr, n_rows, n_heads, n_kv_heads, nullptr, tq, tk, tv, o, lse_opt,
+                              workspace, stream);
 }
 
 size_t h3_attention_window_backward_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_kv_heads) {
@@ -1772,14 +1780,16 @@ h3_status h3_attention_cached(const h3_cache* cache, const h3_window* window, in
     return H3_ERR_ALIGN;
   if (o == q || o == cache->k || o == cache->v || o == workspace || lse_opt == o || lse_opt == workspace)
     return H3_ERR_SHAPE;
+  AttnWinPlan plan{};
+  if ((s = plan_attention_window(*window, cache, n_rows, n_heads, cache->n_kv_heads, ws_bytes, &plan)) != H3_OK) return s;
   CUtensorMap tq, tk, tv;
   const uint32_t G = (uint32_t)(n_heads / cache->n_kv_heads);
   if (!make_tmap_q_shared(&tq, q, n_rows, cache->n_kv_heads, G, q_row_stride_elems, q_head_stride_elems, 128 / G) ||
       !make_tmap_pages(&tk, cache->k, cache->n_pages, cache->n_kv_heads, cache->page_size) ||
       !make_tmap_pages(&tv, cache->v, cache->n_pages, cache->n_kv_heads, cache->page_size))
     return H3_ERR_CUDA;
-  return run_attention_window(*window, cache, n_rows, n_heads, cache->n_kv_heads, seq_start, tq, tk, tv, o, lse_opt,
-                              workspace, ws_bytes, stream);
+  return run_attention_window(plan, *window, cache, n_rows, n_heads, cache->n_kv_heads, seq_start, tq, tk, tv, o, lse_opt,
+                              workspace, stream);
 }
 
 h3_status h3_cache_weights(const h3_cache* cache, const h3_window* window, int32_t n_rows, int32_t n_heads,

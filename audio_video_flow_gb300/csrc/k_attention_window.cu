@@ -90,9 +90,8 @@ struct AwSeq { int row0, rows, keys; };
 template <bool PAGED>
 __device__ __forceinline__ AwSeq aw_seq(const AttnWinArgs& a, int s) {
   if (!PAGED) return {0, a.n_rows, a.n_rows};
+  if (!cache_seq_ok(a.c, a.n_rows, s)) return {0, 0, -1};
   const int b = a.c.start[s], e = a.c.start[s + 1], len = a.c.length[s];
-  if (b < 0 || e < b || e > a.n_rows || len < e - b || (int64_t)len > (int64_t)a.c.table_width * a.c.page_size)
-    return {0, 0, -1};
   return {b, e - b, len};
 }
 // The setup and the segments are straight-line code that each CTA runs a few
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           // the gang's part of the group's weight, in proportion of this CTA's unit.
           // The members take turns, so that units of growing windows even out.
           const int weight = first_group ? b.n : aw_group(a, q, group), part = min(rem, weight - off);
-          int turn = member + group + head;
+          int turn = member + group + head + seq;
           turn -= (int)aw_div(turn, a.M) * a.M;
           const int unit = group * a.M + turn;
           first_group = false;

@@ -19,7 +19,6 @@ __device__ __forceinline__ int64_t page_row(const CacheArgs& c, int page, int he
 __device__ __forceinline__ int page_of(const CacheArgs& c, int seq, int slot) {
   return c.table[(int64_t)seq * c.table_width + (slot >> c.page_shift)];
 }
-__device__ __forceinline__ int64_t cache_slots(const CacheArgs& c) { return (int64_t)c.table_width * c.page_size; }
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -43,7 +42,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
   if (s < 0) return;
   const int b = a.c.start[s], e = a.c.start[s + 1], len = a.c.length[s];
   if (row >= e && e >= b && s == a.c.n_seqs - 1) return;   // behind the last sequence
-  if (b < 0 || e < b || row >= e || e > a.n_rows || len < e - b || len > cache_slots(a.c)) {
+  if (row >= e || !cache_seq_ok(a.c, a.n_rows, s)) {
     if (lane == 0) record_error(a.err, DEVERR_INDEX);
     return;
   }
@@ -99,10 +98,6 @@ struct CwUnit {
   int row0, pos0, keys, rows;    // the sequence: first new row, its position, keys, new rows
   int q0, nq;                    // tiles of rows that see any of the keys
 };
-__device__ __forceinline__ bool cw_seq_ok(const CacheArgs& c, int n_rows, int s) {
-  const int b = c.start[s], e = c.start[s + 1], len = c.length[s];
-  return b >= 0 && e >= b && e <= n_rows && len >= e - b && (int64_t)len <= cache_slots(c);
-}
 // Not inlined: every role calls it once per unit, and fetching the code is what a
 // first call costs.
 __device__ __noinline__ CwUnit cw_unit(const CacheWeightsArgs& a, const int* pre, int per_head, int u) {
@@ -223,7 +218,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const int s = s0 + lane;
       int mine = 0;
       if (s < a.c.n_seqs) {
-        if (cw_seq_ok(a.c, a.n_rows, s)) mine = (a.c.length[s] + a.tiles * 128 - 1) / (a.tiles * 128);
+        if (cache_seq_ok(a.c, a.n_rows, s)) mine = (a.c.length[s] + a.tiles * 128 - 1) / (a.tiles * 128);
         else if (blockIdx.x == 0) record_error(a.err, DEVERR_INDEX);
       }
       int sum = mine;

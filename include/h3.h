@@ -430,10 +430,11 @@ h3_status h3_attention_window_backward(const h3_window *window, int32_t n_rows, 
  * 16, 32, 64, 128 or 256.  At most 1024 sequences and heads, and 2^24 slots in a
  * table's width (H3_ERR_UNSUPPORTED).  table and length are read on the device
  * when a call runs, so a captured call follows them.  A length above the table's
- * width or below the sequence's new rows, a seq_start that decreases or leaves
- * [0, n_rows], and a page that a row needs outside [0, n_pages) are reported
- * (H3_ERR_INDEX from h3_sync_check): such a sequence's results are left as they
- * were or, for a page, undefined; nothing outside the buffers is read or written. */
+ * width or below the sequence's new rows, rows that do not begin at or after the
+ * sequence before's or leave [0, n_rows], and a page that a row needs outside
+ * [0, n_pages) are reported (H3_ERR_INDEX from h3_sync_check): such a sequence's
+ * results are left as they were or, for a page or rows that two sequences claim,
+ * undefined; nothing outside the buffers is read or written. */
 typedef struct {
   void *k, *v;               /* device page pools */
   int32_t n_pages, page_size, n_kv_heads;

@@ -475,3 +475,239 @@ def test_window_backward_split_key_tiles(S, H, Hk, w):
     grads = run_backward(*args)
     ok()
     check_backward(*args, grads, f"S={S} H={H}/{Hk}")
+
+
+# ---------------------------------------------------------------------------
+# the cache in other shapes, bad metadata, streams and graphs, the operators together
+# ---------------------------------------------------------------------------
+
+def test_cached_attention_of_rows_with_one_longer_document():
+    """Single rows on average, so units of one tile; one document has several."""
+    lengths, new = [900] + [50] * 20, [300] + [1] * 20
+    c = Paged(lengths, 1, 16, 3)
+    q = draw(sum(new), 1, torch.Generator().manual_seed(3))
+    w = dict(left=200, right=0, n_first=4)
+    o, lse = run_cached(c, w, q, starts(new), 1)
+    ok()
+    check_cached(c, w, q, new, 1, o, lse, "rows")
+
+
+def test_a_long_cache_of_one_head_and_a_chunk():
+    """Units that every SM has a part of, of a chunk and of one row."""
+    for new, H in (([200], 1), ([1], 1), ([2], 5)):
+        c = Paged([12345], 1, 128, 4)
+        q = draw(sum(new), H, torch.Generator().manual_seed(4))
+        o, lse = run_cached(c, dict(right=0), q, starts(new), H)
+        ok()
+        check_cached(c, dict(right=0), q, new, H, o, lse, str(new))
+
+
+def test_pages_past_32_bits():
+    """A pool of more than 2^31 elements: the pages in use are its last ones."""
+    n_pages, page = 8200, 256                     # x 8 heads x 128: 2.15e9 elements a pool
+    g = torch.Generator().manual_seed(6)
+    k = torch.empty(n_pages, 8, page, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    table = torch.tensor([[n_pages - 1, n_pages - 2]], dtype=torch.int32, device="cuda")
+    length = torch.tensor([300], dtype=torch.int32, device="cuda")
+    cache = h3.make_cache(k, v, table, length)
+    kn, vn = draw(300, 8, g), draw(300, 8, g)
+    start = starts([300])
+    weights = torch.zeros(n_pages, 8, page, device="cuda")
+    h3.h3_cache_append(cache, 300, start, kn, vn, kn.stride(0), kn.stride(1), weights)
+    ok()
+    for t, new in ((k, kn), (v, vn)):
+        assert torch.equal(t[-1].transpose(0, 1), new[:256]) and torch.equal(t[-2, :, :44].transpose(0, 1), new[256:])
+    c = Paged([1], 8, 16, 1)
+    c.cache, c.lengths, c.data = cache, [300], [(kn, vn, None)]
+    q = draw(300, 8, g)
+    o, lse = run_cached(c, dict(right=0), q, start, 8)
+    h3.h3_cache_weights(cache, h3.make_window(right=0), 300, 8, start, q, q.stride(0), q.stride(1), lse, weights, weights)
+    ok()
+    check_cached(c, dict(right=0), q, [300], 8, o, lse, "far pages")
+    total = weights[-1].double().sum() + weights[-2].double().sum()
+    # every row's probabilities sum to 1: 300 rows x 8 heads, within the sums' own rounding
+    assert abs(float(total) - 2400.0) <= 2400 * 2.0 ** -16
+    to = Paged([100], 8, 16, 2)
+    kept = torch.empty(1, 8, 100, dtype=torch.int32, device="cuda")
+    h3.h3_cache_evict(cache, to.cache, 100, 1, 1, weights, to.w, kept, to.length)
+    ok()
+    for h in range(8):
+        w = torch.cat([weights[-1, h], weights[-2, h, :44]]).cpu().numpy()
+        want = O.kept_slots(w, 100, 1, 1)
+        assert np.array_equal(kept[0, h].cpu().numpy(), want)
+        pages, places = to.at(0, np.arange(100))
+        assert torch.equal(to.k[pages, h, places], kn[torch.from_numpy(want).cuda(), h])
+
+
+@pytest.mark.parametrize("what", ["length", "short", "start", "page"])
+def test_bad_metadata_is_reported(what):
+    """Found on the device: the status says so, the other sequences are right, and nothing of the bad one is written
+    (a bad page leaves its rows undefined)."""
+    lengths, new = [100, 80, 60], [3, 2, 1]
+    c = Paged(lengths, 2, 16, 31)
+    q = draw(6, 2, torch.Generator().manual_seed(7))
+    start = starts(new)
+    if what == "length":
+        c.length[1] = 1 << 20
+    elif what == "short":
+        c.length[1] = 1                          # fewer than its new rows
+    elif what == "start":
+        start[2] = 2                             # sequence 1 ends before it begins
+    else:
+        c.table[1, 2] = 12345
+    o, lse = run_cached(c, dict(right=0), q, start, 2)
+    ok(h3.H3_ERR_INDEX)
+    good = [3, 0, 1] if what != "start" else [3, 0, 0]
+    for s, n in enumerate(good):
+        if n:
+            at = [0, 3, 5][s]
+            k, v, _ = c.data[s]
+            mask = O.visible(np.arange(lengths[s] - n, lengths[s]), lengths[s], right=0)
+            for h in range(2):
+                (ro, _), (bo, _) = O.forward(f64(q[at:at + n, h]), f64(k[:, h]), f64(v[:, h]), mask)
+                within(o[at:at + n, h], ro, bo, f"sequence {s}")
+    if what in ("length", "short"):
+        assert (o[3:5] == 7.0).all() and (lse[:, 3:5] == 7.0).all()
+    before = c.k.clone()
+    k = draw(6, 2, torch.Generator().manual_seed(8))
+    if what != "page":                            # (new rows lie in the document's last page)
+        h3.h3_cache_append(c.cache, 6, start, k, k, k.stride(0), k.stride(1))
+        ok(h3.H3_ERR_INDEX)
+        pages, _ = c.at(1, np.arange(80))
+        assert torch.equal(c.k[pages].view(torch.int16), before[pages].view(torch.int16))
+    out = torch.full_like(c.w, 5.0)
+    lse = torch.zeros(2, 6, device="cuda")
+    h3.h3_cache_weights(c.cache, h3.make_window(right=0), 6, 2, start, q, q.stride(0), q.stride(1), lse, c.w, out)
+    ok(h3.H3_ERR_INDEX)
+    if what in ("length", "page"):
+        kept = torch.empty(3, 2, 20, dtype=torch.int32, device="cuda")
+        to = Paged([20, 20, 20], 2, 16, 5)
+        h3.h3_cache_evict(c.cache, to.cache, 20, 2, 2, c.w, to.w, kept, to.length)
+        ok(h3.H3_ERR_INDEX)
+        for s in (0, 2):
+            for h in range(2):
+                want = O.kept_slots(c.data[s][2][:, h].cpu().numpy(), 20, 2, 2)
+                assert np.array_equal(kept[s, h].cpu().numpy(), want)
+
+
+def calls(seed):
+    """One call of each operator, ready to be made: (run(stream), its outputs)."""
+    g = torch.Generator().manual_seed(seed)
+    w = h3.make_window(2, 0, 17, 60, 17)
+    S, H, Hk = 700, 6, 3
+    q, k, v = draw(S, H, g), draw(S, Hk, g), draw(S, Hk, g)
+    o, lse = torch.empty(S, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, S, device="cuda")
+    ws = ws_of(h3.h3_attention_window_workspace_bytes(S, H, Hk))
+    d_o = draw(S, H, g).contiguous()
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws2 = ws_of(h3.h3_attention_window_backward_workspace_bytes(S, H, Hk))
+    c = Paged([1500, 40], Hk, 32, seed)
+    qc, kc, vc = draw(210, H, g), draw(210, Hk, g), draw(210, Hk, g)
+    start = starts([200, 10])
+    oc, lc = torch.empty(210, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, 210, device="cuda")
+    ws3 = ws_of(h3.h3_attention_cached_workspace_bytes(c.cache, 210, H))
+    out = c.w.clone()
+    to = Paged([300, 40], Hk, 64, seed + 1)
+    to.k.zero_(), to.v.zero_(), to.w.zero_()
+    kept = torch.empty(2, Hk, 300, dtype=torch.int32, device="cuda")
+
+    def run(stream=None):
+        h3.h3_attention_window(w, S, H, Hk, q, q.stride(0), 128, k, v, k.stride(0), 128, o, lse, ws, stream)
+        h3.h3_attention_window_backward(w, S, H, Hk, q, q.stride(0), 128, k, v, k.stride(0), 128, o, d_o, lse, dq,
+                                        dq.stride(0), 128, dk, dv, dk.stride(0), 128, ws2, stream)
+        h3.h3_cache_append(c.cache, 210, start, kc, vc, kc.stride(0), 128, c.w, stream)
+        h3.h3_attention_cached(c.cache, w, 210, H, start, qc, qc.stride(0), 128, oc, lc, ws3, stream)
+        h3.h3_cache_weights(c.cache, w, 210, H, start, qc, qc.stride(0), 128, lc, c.w, out, stream)
+        h3.h3_cache_evict(c.cache, to.cache, 300, 17, 200, out, to.w, kept, to.length, stream)
+    return run, [o, lse, dq, dk, dv, oc, lc, out, kept, to.k, to.v, to.w]
+
+
+def test_streams_graphs_and_repeats_give_the_same_bits():
+    runs = [calls(seed) for seed in (1, 2, 3)]
+    want = []
+    for run, outs in runs:
+        run()
+        ok()
+        want.append([t.clone() for t in outs])
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(10):                           # several at once
+        for (run, _), s in zip(runs, streams):
+            run(s)
+    ok()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                 # captured, and replayed beside an eager call
+        runs[0][0]()
+    for _ in range(5):
+        graph.replay()
+        runs[1][0](streams[1])
+    ok()
+    for (_, outs), ref in zip(runs, want):
+        for t, r in zip(outs, ref):
+            assert torch.equal(t.view(torch.uint8), r.view(torch.uint8))
+
+
+def test_a_clip_generated_frame_by_frame():
+    """Frames appended and attended to one after the other give what the window gives over the whole clip; the weights
+    that they collect go by every row's probabilities; and after the cache is cut, the next frame attends to what was
+    kept."""
+    H, Hk, frame, text, frames = 4, 2, 45, 10, 6
+    S = text + frame * frames
+    w = dict(left=2, right=0, n_first=text, unit=frame, origin=text)
+    g = torch.Generator().manual_seed(12)
+    q, k, v = draw(S, H, g), draw(S, Hk, g), draw(S, Hk, g)
+    whole, whole_lse = run_window(w, q, k, v)
+    table = torch.tensor([[7, 2, 5, 0, 1, 6, 3, 4, 9, 8]], dtype=torch.int32, device="cuda")
+    pools = [torch.full((10, Hk, 32, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    weights = torch.full((10, Hk, 32), float("nan"), device="cuda")
+    length = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = h3.make_cache(*pools, table, length)
+    window = h3.make_window(**w)
+    row, total = 0, 0.0
+    for n in [text] + [frame] * frames:
+        part = slice(row, row + n)
+        row += n
+        length.fill_(row)
+        start = starts([n])
+        h3.h3_cache_append(cache, n, start, k[part], v[part], k.stride(0), k.stride(1), weights)
+        o, lse = torch.empty(n, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, n, device="cuda")
+        h3.h3_attention_cached(cache, window, n, H, start, q[part], q.stride(0), q.stride(1), o, lse,
+                               ws_of(h3.h3_attention_cached_workspace_bytes(cache, n, H)))
+        h3.h3_cache_weights(cache, window, n, H, start, q[part], q.stride(0), q.stride(1), lse, weights, weights)
+        ok()
+        mask = O.visible(np.arange(row - n, row), S, **w)
+        for h in range(H):
+            (ro, rl), (bo, bl) = O.forward(f64(q[part, h]), f64(k[:, h * Hk // H]), f64(v[:, h * Hk // H]), mask)
+            within(o.view(n, H, 128)[:, h], ro, bo, f"rows {part} head {h}")
+            within(lse[h], rl, bl, f"rows {part} head {h} lse")
+            within(whole[part, h], ro, bo, f"whole clip, rows {part} head {h}")
+            within(whole_lse[h][part], rl, bl, f"whole clip, rows {part} head {h} lse")
+    slots = torch.arange(S, device="cuda")
+    mine = weights[table[0, slots // 32].long(), :, slots % 32]
+    assert abs(float(mine.double().sum()) - S * H) <= S * H * 2.0 ** -16
+    # cut to 120 rows, the text and the last frame kept
+    to_table = torch.tensor([[3, 1, 4, 0, 2, 5]], dtype=torch.int32, device="cuda")
+    to_pools = [torch.full((6, Hk, 32, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    to_weights = torch.full((6, Hk, 32), float("nan"), device="cuda")
+    to_length = torch.zeros(1, dtype=torch.int32, device="cuda")
+    to = h3.make_cache(*to_pools, to_table, to_length)
+    kept = torch.empty(1, Hk, 120, dtype=torch.int32, device="cuda")
+    h3.h3_cache_evict(cache, to, 120, text, frame, weights, to_weights, kept, to_length)
+    ok()
+    assert to_length.item() == 120
+    kn, vn, qn = draw(frame, Hk, g), draw(frame, Hk, g), draw(frame, H, g)
+    to_length.fill_(120 + frame)
+    start = starts([frame])
+    h3.h3_cache_append(to, frame, start, kn, vn, kn.stride(0), kn.stride(1), to_weights)
+    o, lse = torch.empty(frame, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, frame, device="cuda")
+    h3.h3_attention_cached(to, h3.make_window(), frame, H, start, qn, qn.stride(0), qn.stride(1), o, lse,
+                           ws_of(h3.h3_attention_cached_workspace_bytes(to, frame, H)))
+    ok()
+    every = np.ones((frame, 120 + frame), bool)
+    for h in range(H):
+        rows = kept[0, h * Hk // H].long()
+        kk = np.concatenate([f64(k[rows, h * Hk // H]), f64(kn[:, h * Hk // H])])
+        vv = np.concatenate([f64(v[rows, h * Hk // H]), f64(vn[:, h * Hk // H])])
+        (ro, _), (bo, _) = O.forward(f64(qn[:, h]), kk, vv, every)
+        within(o.view(frame, H, 128)[:, h], ro, bo, f"after the cut, head {h}")
