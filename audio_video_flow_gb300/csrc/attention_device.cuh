@@ -122,6 +122,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
       : "memory");
 }
 
+__device__ __forceinline__ void at_tma_store_4d(const CUtensorMap* tm, const void* src, int32_t x, int32_t y, int32_t z,
+                                                int32_t w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Waits until this thread's stores have read their source.
+__device__ __forceinline__ void at_tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // Windows (see h3_window): unit(i) = floor((i - origin) / unit).  Row i sees
 // the keys [win_lo, win_hi) and, of the first ones, [0, min(first, win_hi)).

@@ -1627,7 +1627,13 @@ h3_status run_attention_window(const AttnWinPlan& p, const h3_window& w, const h
   a.o_elems = (size_t)n_rows * n_heads * 128;
   a.lse_elems = lse ? (size_t)n_rows * n_heads : 0;
   a.err = device_error_word();
-  return cuda_st(launch_attention_window(tq, tk, tv, a, p, stream));
+  CUtensorMap to{};
+  if (!c) {
+    a.o_tma = 32 % a.G == 0;
+    const uint32_t G = (uint32_t)a.G;
+    if (a.o_tma && !make_tmap_q_shared(&to, o, n_rows, n_kv_heads, G, (uint64_t)n_heads * 128, 128, 32 / G)) return H3_ERR_CUDA;
+  }
+  return cuda_st(launch_attention_window(tq, tk, tv, c ? nullptr : &to, a, p, stream));
 }
 }  // namespace
 

@@ -336,6 +336,7 @@ struct AttnWinArgs {
   WindowArgs w;
   CacheArgs c;
   int M, U;                   // CTAs of a gang (consecutive ones), rows of a unit
+  int o_tma;                  // results leave by TMA: a warp's 32 (row, head) pairs are whole rows
   int gangs;
   uint64_t gangs_inv;         // 2^32 / gangs + 1
   int n_rows, H, G, R;        // G query heads share a KV head; a 128-row tile holds R rows x G heads
@@ -358,8 +359,9 @@ size_t attn_win_part_bytes(int ctas, int rows);   // at most, for tiles of that 
 // False where a call has more than 2^31 pairs of a unit and a key tile.
 bool attn_win_plan(AttnWinPlan* p, int64_t n_rows, int64_t kv_heads, int64_t n_seqs, int G, int64_t max_keys, bool paged,
                    const WindowArgs& w);
+// tmO: the results of a document (null otherwise), used where a.o_tma
 cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream);
+                                    const CUtensorMap* tmO, const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream);
 
 struct AppendArgs {
   CacheArgs c;

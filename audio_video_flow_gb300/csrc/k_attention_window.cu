@@ -153,6 +153,7 @@ template <int MODE>
 struct AwRuns {};
 template <>
 struct AwRuns<0> {
+  CUtensorMap o;      // the results: boxes of a softmax warp's 32 (row, head) pairs x 64 channels
   int all;
   struct { int head, group, off, n, x; } begin[kMaxGangs + 1];
 };
@@ -1002,7 +1003,17 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
                 *reinterpret_cast<uint4*>(stg + lane * 128 + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4)) = w[u];
-              if (c & 1) {
+              if ((c & 1) && a.o_tma) {
+                // rows past the document are outside the map and not written
+                fence_proxy_async_smem();
+                __syncwarp();
+                if constexpr (MODE == AW_DOC)
+                  if (lane == 0) {
+                    at_tma_store_4d(&runs.o, stg, (c >> 1) * 64, 0, g->head, g->row0 + rbase + row_r);
+                    at_tma_store_read();   // before the stage is written again
+                  }
+                __syncwarp();
+              } else if (c & 1) {
                 __syncwarp();
 #pragma unroll
                 for (int it = 0; it < 8; ++it) {
@@ -1187,7 +1198,7 @@ static cudaError_t launch_mode(const CUtensorMap& tmQ, const CUtensorMap& tmK, c
 }
 
 cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream) {
+                                    const CUtensorMap* tmO, const AttnWinArgs& a, const AttnWinPlan& p, cudaStream_t stream) {
   if (p.split) {
     const int words = p.ctas * kCtrl;
     const cudaError_t e = launch_kernel(attention_window_start_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0,
@@ -1198,6 +1209,7 @@ cudaError_t launch_attention_window(const CUtensorMap& tmQ, const CUtensorMap& t
   if (p.mode == AW_DOC) {
     AwRuns<AW_DOC> runs;
     aw_doc_runs(a, p, &runs);
+    runs.o = *tmO;
     e = launch_mode<AW_DOC>(tmQ, tmK, tmV, a, runs, p.ctas, stream);
   } else if (p.mode == AW_CHUNK) {
     e = launch_mode<AW_CHUNK>(tmQ, tmK, tmV, a, {}, p.ctas, stream);

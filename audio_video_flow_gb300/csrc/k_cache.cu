@@ -23,17 +23,20 @@ __device__ __forceinline__ int page_of(const CacheArgs& c, int seq, int slot) {
 
 // ---------------------------------------------------------------------------
 // Append: row i of sequence s, the rows-before-it-in-s'th of its new ones, goes
-// to slot length[s] - new + that.  A warp copies one row of one head: K by the
-// lower, V by the upper half of its lanes.  Bound by HBM (or by its launch).
+// to slot length[s] - new + that.  A warp copies up to eight heads of one row, all
+// in flight: K by the lower, V by the upper half of its lanes.  Bound by HBM, or by
+// its launch.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
+namespace {
+constexpr int CA_HEADS = 8;
+}
+__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, int warps_per_row) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t units = (int64_t)a.n_rows * a.c.n_kv_heads;
   const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (u >= units) return;
-  const int row = (int)(u / a.c.n_kv_heads), head = (int)(u - (int64_t)row * a.c.n_kv_heads);
+  if (u >= (int64_t)a.n_rows * warps_per_row) return;
+  const int row = (int)(u / warps_per_row), head0 = (int)(u - (int64_t)row * warps_per_row) * CA_HEADS;
   int s = -1;
   for (int lo = 0, hi = a.c.n_seqs - 1; lo <= hi;) {   // the last sequence that starts at or before the row
     const int mid = (lo + hi) >> 1;
@@ -51,14 +54,24 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
     if (lane == 0) record_error(a.err, DEVERR_INDEX);
     return;
   }
-  const int64_t to = page_row(a.c, page, head, slot);
-  const __nv_bfloat16* src = (lane < 16 ? a.k : a.v) + (int64_t)row * a.row_stride + (int64_t)head * a.head_stride;
-  __nv_bfloat16* dst = (lane < 16 ? a.k_pages : a.v_pages) + to * 128;
-  if (in_bounds<__nv_bfloat16>(lane < 16 ? a.k_pages : a.v_pages, a.page_elems, dst, 128, a.err, 60) &&
-      in_bounds<__nv_bfloat16>(lane < 16 ? a.k : a.v, a.src_elems, src, 128, a.err, 61))
-    reinterpret_cast<uint4*>(dst)[lane & 15] = reinterpret_cast<const uint4*>(src)[lane & 15];
-  if (lane == 0 && a.weights != nullptr && in_bounds<float>(a.weights, a.page_elems / 128, a.weights + to, 1, a.err, 62))
-    a.weights[to] = 0.0f;
+  const __nv_bfloat16* src = lane < 16 ? a.k : a.v;
+  __nv_bfloat16* dst = lane < 16 ? a.k_pages : a.v_pages;
+  uint4 x[CA_HEADS];
+#pragma unroll
+  for (int h = 0; h < CA_HEADS; ++h) {
+    const __nv_bfloat16* from = src + (int64_t)row * a.row_stride + (int64_t)(head0 + h) * a.head_stride;
+    if (head0 + h < a.c.n_kv_heads && in_bounds<__nv_bfloat16>(src, a.src_elems, from, 128, a.err, 61))
+      x[h] = reinterpret_cast<const uint4*>(from)[lane & 15];
+  }
+#pragma unroll
+  for (int h = 0; h < CA_HEADS; ++h) {
+    if (head0 + h >= a.c.n_kv_heads) break;
+    const int64_t to = page_row(a.c, page, head0 + h, slot);
+    if (in_bounds<__nv_bfloat16>(dst, a.page_elems, dst + to * 128, 128, a.err, 60))
+      reinterpret_cast<uint4*>(dst + to * 128)[lane & 15] = x[h];
+    if (lane == h && a.weights != nullptr && in_bounds<float>(a.weights, a.page_elems / 128, a.weights + to, 1, a.err, 62))
+      a.weights[to] = 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -402,9 +415,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const CwUnit x = cw_unit(a, pre, per_head, u);
       for (int p = 0; p < max(x.nq, 1) && ok; p += CW_SLOTS) {
         const int n = min(CW_SLOTS, x.nq - p);   // 0: no row sees the unit, its weights stay
-        for (int k = 0; k < x.tiles && ok; ++k) {
-          int64_t at[4];
-          float w[4];
+        // this lane's four keys of key tile k: their places (-1: none) and weights
+        auto weights_of = [&](int k, int64_t (&at)[4], float (&w)[4]) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = x.key0 + k * 128 + e * 32 + lane;
@@ -422,6 +434,17 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
               if (at[e] >= 0) w[e] = p > 0 ? a.out[at[e]] : (a.in != nullptr ? a.in[at[e]] : 0.0f);
             }
           }
+        };
+        int64_t at[4], next_at[4];
+        float w[4], next_w[4];
+        weights_of(0, next_at, next_w);
+        for (int k = 0; k < x.tiles && ok; ++k) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            at[e] = next_at[e];
+            w[e] = next_w[e];
+          }
+          if (k + 1 < x.tiles) weights_of(k + 1, next_at, next_w);   // arrive during the waits
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int i = 0; i < n; ++i) {
             const uint32_t slot = (slot0 + i) % CW_SLOTS, b = slot * CW_RED + ((turn >> slot) & 1u);
@@ -704,8 +727,10 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
 // launchers
 // ---------------------------------------------------------------------------
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t units = (int64_t)a.n_rows * a.c.n_kv_heads;
-  const cudaError_t e = launch_kernel(cache_append_kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, a);
+  const int warps_per_row = (a.c.n_kv_heads + CA_HEADS - 1) / CA_HEADS;
+  const int64_t units = (int64_t)a.n_rows * warps_per_row;
+  const cudaError_t e = launch_kernel(cache_append_kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, a,
+                                      warps_per_row);
   if (e != cudaSuccess) return e;
   set_kernel_info("cache_append_kernel rows=%d heads=%d", a.n_rows, a.c.n_kv_heads);
   return cudaGetLastError();
@@ -717,9 +742,11 @@ cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   if (!tmem_exclusive(CW_SMEM)) return cudaErrorNotSupported;
   cudaError_t e = cudaFuncSetAttribute(cache_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CW_SMEM);
   if (e != cudaSuccess) return e;
-  // Units of one to sixteen key tiles: the fewest rounds of the grid, a tile of rows
-  // that a unit loads counted as half a product (at the tables' width and the
-  // sequences' average rows).
+  // Units of one to sixteen key tiles: against the rounds of the grid (between full
+  // ones at the tables' width and a last one half full: the lengths are on the
+  // device) stands what each unit costs beside its products, one product's time for
+  // each of its tiles of rows (at the sequences' average) and two for its start
+  // (405 rows: 15 key tiles 114 us, 4 key tiles 123).
   const int64_t tiles = ((int64_t)a.c.table_width * a.c.page_size + 127) / 128;
   const int64_t lists = (int64_t)a.c.n_kv_heads * a.c.n_seqs;
   const int64_t per_seq = (a.n_rows + a.c.n_seqs - 1) / a.c.n_seqs;
@@ -728,7 +755,7 @@ cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   int64_t units = 0;
   for (int t = 1; t <= 16; ++t) {
     const int64_t n = lists * ((tiles + t - 1) / t), rounds = (n + num_sms() - 1) / num_sms();
-    const double cost = (double)rounds * ((double)t * nq + 0.5 * nq + 0.5);
+    const double cost = ((double)rounds + (double)n / num_sms() + 0.5) * ((double)t * nq + nq + 2.0);
     if (t == 1 || cost < best) {
       best = cost;
       a.tiles = t;

@@ -393,8 +393,9 @@ typedef struct {
  * [n_heads*128], lse_opt NULL or fp32 [n_heads][n_rows] as for h3_attention;
  * neither may overlap an input.  A non-finite k or v of a row makes the results of the rows
  * near it that see its 128-row tile undefined, as well as of those that see it.
- * Only tiles that some row sees are read.  Up to 2^24 rows and 32767 heads
- * (H3_ERR_UNSUPPORTED).  The key tiles are split over the SMs, so the result is
+ * Only tiles that some row sees are read.  Up to 2^24 rows, 32767 heads and 2^31
+ * tiles of 256 (row, sharing head) pairs x 128 visible keys (H3_ERR_UNSUPPORTED).
+ * The key tiles are split over the SMs, so the result is
  * bitwise repeatable on a given GPU, but the order of its sums follows the row
  * count.  workspace: device, 256-byte aligned, at least
  * h3_attention_window_workspace_bytes (0 for invalid sizes) on the device that
