@@ -6,6 +6,7 @@
 #include "attention_device.cuh"
 #include "h3_internal.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace h3 {
@@ -522,19 +523,26 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Eviction.  evict_select_kernel, one CTA per sequence and head: which of n
 // slots stay.  The weights become 32-bit keys that order as they do (NaN lowest);
-// three passes of 11, 11 and 10 bits find the key that the last kept slot has,
-// and one ordered pass writes the slots above it and the earliest of those equal
-// to it.  Counts are integers: the result is exact and repeatable.
+// up to three passes of 11, 11 and 10 bits find the key that the last kept slot
+// has, or a border between keys, and one ordered pass writes the slots above it and
+// the earliest of those equal to it.  Counts are integers: the result is exact and
+// repeatable.  Bound by instructions (issue slots 65 % busy), so each pass over the
+// keys does little: 56 x 15,860 slots, 20 us and the call 84, with classes of slots
+// in each pass and always three; now the call is 81.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int EV_THREADS = 1024, EV_BINS = 2048;
 constexpr int EV_KEYS = 48 * 1024;               // keys held in shared memory; further ones are read again
+constexpr int EV_BATCH = 4;                      // slots of a thread in flight
 constexpr int EV_SMEM = EV_BINS * 4 + 256;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t b = __float_as_uint(w == 0.0f ? 0.0f : w);   // -0 as 0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ bool evict_bad(const EvictArgs& a, int n) {
+  return n < 0 || (int64_t)n > cache_slots(a.from) || (int64_t)min(n, a.budget) > cache_slots(a.to);
 }
 }  // namespace
 
@@ -543,15 +551,14 @@ template <bool HELD>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArgs a, int held) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem_raw);
-  uint32_t* misc = hist + EV_BINS;                 // [0, 32) warp sums, [32] the bin, [33] what is still to keep in it
+  uint32_t* misc = hist + EV_BINS;                 // [0, 32) warp sums, [32] the bin, [33] what is still to keep in it, [34] its keys
   uint32_t* keys = misc + 64;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();   // after the wait: the move begins with what earlier kernels left
   const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = a.from.length[s];
   int32_t* kept = a.kept + ((int64_t)s * a.from.n_kv_heads + head) * a.budget;
-  const bool bad = n < 0 || (int64_t)n > cache_slots(a.from) || (int64_t)min(n, a.budget) > cache_slots(a.to);
-  if (bad) {   // nothing of this sequence is moved
+  if (evict_bad(a, n)) {   // nothing of this sequence is moved
     if (tid == 0) {
       record_error(a.err, DEVERR_INDEX);
       if (head == 0) a.length[s] = 0;
@@ -564,7 +571,9 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
     for (int i = tid; i < a.budget; i += EV_THREADS) kept[i] = i < n ? i : -1;
     return;
   }
-  const int m0 = a.first, m1 = n - a.recent;       // slots that go by weight
+  const int m0 = a.first, m = n - a.recent - m0;   // slots [m0, m0 + m) go by weight
+  for (int i = tid; i < m0; i += EV_THREADS) kept[i] = i;
+  for (int i = tid; i < a.recent; i += EV_THREADS) kept[a.budget - a.recent + i] = m0 + m + i;
   uint32_t want = (uint32_t)(a.budget - a.first - a.recent);
   auto weight_at = [&](int slot) -> uint32_t {
     const int page = page_of(a.from, s, slot);
@@ -575,35 +584,38 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
     const float* w = a.weights + page_row(a.from, page, head, slot);
     return in_bounds<float>(a.weights, a.from_rows, w, 1, a.err, 65) ? weight_key(*w) : 0u;
   };
-  // four slots a thread at a time: table entries, then weights, in flight together
+  // a few slots a thread at a time: table entries, then weights, in flight together
   // (one by one: 25 us of a call of 15,860 slots)
-  for (int i0 = m0 + tid; i0 < min(m1, m0 + held); i0 += 4 * EV_THREADS) {
-    int page[4];
-    float w[4];
+  const int in_smem = min(m, held);
+  for (int i0 = tid; i0 < in_smem; i0 += EV_BATCH * EV_THREADS) {
+    int page[EV_BATCH];
+    float w[EV_BATCH];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < EV_BATCH; ++e) {
       const int i = i0 + e * EV_THREADS;
-      page[e] = i < min(m1, m0 + held) ? page_of(a.from, s, i) : -1;
+      page[e] = i < in_smem ? page_of(a.from, s, m0 + i) : -1;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < EV_BATCH; ++e) {
       const int i = i0 + e * EV_THREADS;
       w[e] = NAN;
       if (page[e] < 0 || page[e] >= a.from.n_pages) {
-        if (i < min(m1, m0 + held)) record_error(a.err, DEVERR_INDEX);
+        if (i < in_smem) record_error(a.err, DEVERR_INDEX);
         continue;
       }
-      const float* at = a.weights + page_row(a.from, page[e], head, i);
+      const float* at = a.weights + page_row(a.from, page[e], head, m0 + i);
       if (in_bounds<float>(a.weights, a.from_rows, at, 1, a.err, 65)) w[e] = *at;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i0 + e * EV_THREADS < min(m1, m0 + held)) keys[i0 + e * EV_THREADS - m0] = weight_key(w[e]);
+    for (int e = 0; e < EV_BATCH; ++e)
+      if (i0 + e * EV_THREADS < in_smem) keys[i0 + e * EV_THREADS] = weight_key(w[e]);
   }
   __syncthreads();
-  auto key_at = [&](int slot) -> uint32_t { return HELD || slot - m0 < held ? keys[slot - m0] : weight_at(slot); };
-  uint32_t prefix = 0, mask = 0;
+  auto key_at = [&](int i) -> uint32_t { return HELD || i < held ? keys[i] : weight_at(m0 + i); };
+  // Slots with a key above `last` stay, and the first `want` of those equal to it.
+  uint32_t last = 0xffffffffu, mask = 0;           // no weight has that key
   if (want > 0) {
+    last = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
@@ -611,9 +623,9 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
       __syncthreads();
       const uint32_t digit = pass == 2 ? 1023u : 2047u;
 #pragma unroll 4
-      for (int i = m0 + tid; i < m1; i += EV_THREADS) {
+      for (int i = tid; i < m; i += EV_THREADS) {
         const uint32_t key = key_at(i);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
+        if ((key & mask) == last) atomicAdd(&hist[(key >> shift) & digit], 1u);
       }
       __syncthreads();
       // from the highest bin down: thread t holds bins 2047 - 2t and 2046 - 2t
@@ -631,71 +643,91 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictArg
       if (before < want && want <= before + h0) {
         misc[32] = (uint32_t)(EV_BINS - 1 - 2 * tid);
         misc[33] = want - before;
+        misc[34] = h0;
       } else if (before + h0 < want && want <= before + h0 + h1) {
         misc[32] = (uint32_t)(EV_BINS - 2 - 2 * tid);
         misc[33] = want - before - h0;
+        misc[34] = h1;
       }
       __syncthreads();
-      prefix |= misc[32] << shift;
+      last |= misc[32] << shift;
       mask |= digit << shift;
       want = misc[33];
+      const bool whole = want == misc[34] && last > 0;
       __syncthreads();
+      if (whole) {                                 // all of the bin stay: distinct weights seldom need the third pass
+        --last;
+        want = 0;
+        break;
+      }
     }
   }
   // In order: warp w takes an equal run of the slots, counts what it keeps and
   // how many equal the last key, and then writes from the sum of those before.
-  const int run = ((n + 31) / 32 + 31) & ~31, r0 = min(n, warp * run), r1 = min(n, r0 + run);
-  auto classify = [&](int i) -> int {              // 2: stays, 1: as the last key, 0: goes
-    if (i >= r1) return 0;
-    if (i < m0 || i >= m1) return 2;
-    if (mask == 0u) return 0;
-    const uint32_t k = key_at(i);
-    return k > prefix ? 2 : (k == prefix ? 1 : 0);
-  };
+  const int run = ((m + 31) / 32 + 31) & ~31, r0 = min(m, warp * run), r1 = min(m, r0 + run);
   uint32_t above = 0, equal = 0;
 #pragma unroll 4
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int c = classify(i0 + lane);
-    above += __popc(__ballot_sync(0xffffffffu, c == 2));
-    equal += __popc(__ballot_sync(0xffffffffu, c == 1));
+  for (int i = r0 + lane; i < r1; i += 32) {
+    const uint32_t key = key_at(i);
+    above += key > last;
+    equal += key == last;
   }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) {
     hist[warp] = above;
     hist[32 + warp] = equal;
   }
   __syncthreads();
-  uint32_t out = __reduce_add_sync(0xffffffffu, lane < warp ? hist[lane] : 0u);
+  uint32_t out = (uint32_t)m0 + __reduce_add_sync(0xffffffffu, lane < warp ? hist[lane] : 0u);
   uint32_t seen = __reduce_add_sync(0xffffffffu, lane < warp ? hist[32 + lane] : 0u);
   out += min(seen, want);
+  const unsigned below = (1u << lane) - 1u;
 #pragma unroll 4
   for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int i = i0 + lane, c = classify(i);
-    const unsigned eq = __ballot_sync(0xffffffffu, c == 1), below = (1u << lane) - 1u;
-    const bool stays = c == 2 || (c == 1 && seen + __popc(eq & below) < want);
+    const int i = i0 + lane;
+    const uint32_t key = i < r1 ? key_at(i) : 0u;
+    bool stays = i < r1 && key > last;
+    const unsigned eq = want > 0 ? __ballot_sync(0xffffffffu, i < r1 && key == last) : 0u;
+    if (eq != 0u) {
+      stays = stays || (((eq >> lane) & 1u) && seen + __popc(eq & below) < want);
+      seen += __popc(eq);
+    }
     const unsigned st = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept[out + __popc(st & below)] = i;
+    if (stays) kept[out + __popc(st & below)] = m0 + i;
     out += __popc(st);
-    seen += __popc(eq);
   }
 }
 
 // Moves the kept rows: a warp a row, K by the lower and V by the upper half of
-// its lanes, eight rows in flight.  Bound by HBM: %EVICT%
+// its lanes, eight rows in flight.  The first and the recent rows, and sequences
+// that fit the budget, move whatever the selection says, so their tiles come first
+// and do not wait for it: it has let this grid start once it had itself waited for
+// all before it, and it neither reads nor writes what they touch (a tenth of the rows
+// of a call of 56 heads x 15,860 slots: 90 -> 87 us as a graph).  Bound by HBM:
+// that call moves 7930 of each, 464 MB, in 81 us, 5.7 TB/s with the selection, 12 us
+// of which nothing overlaps.
 namespace {
-constexpr int EM_ROWS = 8;   // rows of a warp
+constexpr int EM_ROWS = 8, EM_TILE = 8 * EM_ROWS;   // rows of a warp and of a CTA
 }
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int head = blockIdx.y, s = blockIdx.z, lane = threadIdx.x & 31;
-  const int d0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * EM_ROWS;
+// Grid: tiles x heads, sequences; first_tile, that of the first recent row, is first.
+// The next kernel starts with the last of its CTAs, not earlier: one that comes to
+// select for another call would take places of these (95 us for 84).
+__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int tiles, int first_tile) {
+  const int y = (int)(blockIdx.x / (unsigned)a.from.n_kv_heads), head = (int)blockIdx.x - y * a.from.n_kv_heads;
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const int tile = first_tile + y - (y >= tiles - first_tile ? tiles : 0);
+  const int d0 = tile * EM_TILE + (int)(threadIdx.x >> 5) * EM_ROWS, n = a.from.length[s];
   const int32_t* kept = a.kept + ((int64_t)s * a.from.n_kv_heads + head) * a.budget;
+  const bool sure = !evict_bad(a, n) && (n <= a.budget || d0 + EM_ROWS <= a.first || d0 >= a.budget - a.recent);
+  if (!sure) griddep_wait();
+  auto slot_of = [&](int d) { return !sure ? kept[d] : (n > a.budget && d >= a.first ? n - a.budget + d : (d < n ? d : -1)); };
   const __nv_bfloat16* src = lane < 16 ? a.k_from : a.v_from;
   __nv_bfloat16* dst = lane < 16 ? a.k_to : a.v_to;
   // lane e % 8 finds row e's places
   int64_t from_row = -1, to_row = -1;
   {
-    const int d = d0 + (lane & (EM_ROWS - 1)), slot = d < a.budget ? kept[d] : -1;
+    const int d = d0 + (lane & (EM_ROWS - 1)), slot = d < a.budget ? slot_of(d) : -1;
     if (slot >= 0) {
       const int pf = page_of(a.from, s, slot), pt = page_of(a.to, s, d);
       if (pf >= 0 && pf < a.from.n_pages && pt >= 0 && pt < a.to.n_pages) {
@@ -721,6 +753,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
     const int64_t at = __shfl_sync(0xffffffffu, to_row, e);
     if ((rows >> e) & 1u) reinterpret_cast<uint4*>(dst + at * 128)[lane & 15] = row[e];
   }
+  if (sure) griddep_wait();   // this grid ends after the selection's
 }
 
 // ---------------------------------------------------------------------------
@@ -780,9 +813,10 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   e = launch_kernel(kernel, dim3((unsigned)a.from.n_kv_heads, (unsigned)a.from.n_seqs), dim3(EV_THREADS),
                     smem, stream, a, held);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((a.budget + 8 * EM_ROWS - 1) / (8 * EM_ROWS)), (unsigned)a.from.n_kv_heads,
-                  (unsigned)a.from.n_seqs);
-  e = launch_kernel(evict_move_kernel, grid, dim3(256), 0, stream, a);
+  const int tiles = (a.budget + EM_TILE - 1) / EM_TILE;
+  const dim3 grid((unsigned)tiles * (unsigned)a.from.n_kv_heads, (unsigned)a.from.n_seqs);
+  e = launch_kernel(evict_move_kernel, grid, dim3(256), 0, stream, a, tiles,
+                    std::min(tiles - 1, (a.budget - a.recent) / EM_TILE));
   if (e != cudaSuccess) return e;
   set_kernel_info("evict_select_kernel + evict_move_kernel heads=%d sequences=%d budget=%d held=%d", a.from.n_kv_heads,
                   a.from.n_seqs, a.budget, held);
