@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(256) attention_bwd_join_kernel(const AttnBwdAr
 // than an SM's share of all the work (a key step counts 4 products, a query step
 // 3) would run alone at the end, and is cut into pieces of half that share, at
 // least kPieceSteps (4099 rows, 24 heads over 4, 640 keys and 3 first: one CTA of
-// 198 steps, 281 us; in pieces %SHARED% us).
+// 198 steps, 281 us; in pieces 135 us).
 constexpr int kPieceSteps = 16, kMaxPieces = 520;
 void attn_bwd_split(AttnBwdArgs* a) {
   a->first_tiles = a->w.left < 0 ? 0 : (int)std::min<int64_t>(a->tiles, ((int64_t)a->w.first + 127) / 128);

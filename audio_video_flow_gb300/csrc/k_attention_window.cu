@@ -96,7 +96,7 @@ __device__ __forceinline__ AwSeq aw_seq(const AttnWinArgs& a, int s) {
 }
 // The setup and the segments are straight-line code that each CTA runs a few
 // times, so their time is that of fetching it: divisions and the key tiles of a
-// unit are functions that are not inlined (setup 6000 -> %SETUP% cycles).
+// unit are functions that are not inlined (405 rows over a cache: 101 -> 95 us).
 __device__ __noinline__ uint32_t aw_div(uint32_t a, uint32_t b) { return a / b; }
 __device__ __forceinline__ int aw_unit_of(const WindowArgs& w, int i) {   // win_unit
   return w.unit == 1 ? i : (int)aw_div((uint32_t)(i - w.origin + w.unit), (uint32_t)w.unit) - 1;

@@ -83,34 +83,43 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
 //   A unit is a few 128-key tiles of one KV head and sequence; CTA c takes units
 // c, c + grid, ...  The tiles of 128 (row, head) pairs that see any of its keys
 // are held in shared memory, up to four at a time (a pass), and the key tiles
-// stream past them, each half (64 channels) a stage of the ring.  Of a pass, tile
-// i of rows lies in slot (s + i) % 4, s where the pass before ended, so that the
-// next pass's rows load while this one's last are used.
+// stream past them, each half (64 channels) a stage of the ring.  Two tiles of rows
+// make a product of 256 columns (tile by tile, its issue and waits took 940 cycles
+// where the tensor core had 580 to do, and K was read twice: 117 -> 109 us of a call
+// of 405 rows).  Of a pass,
+// pair i lies in half (h + i) % 2, h where the pass before ended, so that the next
+// pass's rows load while this one's last are used.
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 the rows' log-sum-exp,
-//   warps 4-7 exponentials and sums of slots 0 and 2, 8-11 of 1 and 3 (a key per
-//   thread),
-//   warp 3 adds the slots' sums of a key tile, in their order, to the weights.
-// TMEM: S of slot i at [128 i, 128 i + 128).  A product has as many columns as
-// its tile has pairs, rounded up to 16: single rows cost little beside reading K.
+//   warps 4-7 exponentials and sums of the pairs' first tiles, 8-11 of their second
+//   (a key per thread),
+//   warp 3 adds the two groups' sums of a key tile to the weights (one sum per group,
+//   not per tile of rows, and no window arithmetic where all rows see a unit: 109 ->
+//   105 us).
+// TMEM: S of pair i at [256 i, 256 i + 256).  A product has as many columns as its
+// tiles have pairs, rounded up to 16: single rows cost little beside reading K.
 // Shared memory is what the products themselves fill, so the rows' log-sum-exp is
 // not read from it column by column by every thread (16 KB a product and warp, as
 // much as the operands: 124 us of a call of 405 rows) but comes with the product,
 // as a K step of its own: ones times -lse sqrt(128) in three bf16 parts, 2^-26 of
 // it off.
-// Measured: %WEIGHTS%
+// Measured (56 heads, 405 rows over 14,836 keys): 101 us, 855 TFLOP/s; a key tile
+// takes 3400 cycles, of which the tensor core has 1950 and the exponentials 1660 to
+// do, the rest is waits between the two, and a CTA's first product starts after 9500.
+// Single rows (6 sequences): 22 us, by the start and the latency of a few key tiles.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int CW_THREADS = 32 * 12;
-constexpr int CW_SLOTS = 4, CW_KST = 4, CW_RED = 2;
+constexpr int CW_SLOTS = 4, CW_PAIRS = 2, CW_KST = 4, CW_RED = 2;
 constexpr int CW_TILE = 128 * 128 * 2, CW_BOX = 128 * 64 * 2;
 constexpr int CW_STEP = 128 * 16 * 2;   // an operand of one K step
 constexpr int CW_SMEM =
-    CW_TILE * CW_SLOTS + CW_BOX * CW_KST + CW_STEP * (CW_SLOTS + 1) + 4 * kCacheMaxSeqs + CW_SLOTS * CW_RED * 512 + 512;
+    CW_TILE * CW_SLOTS + CW_BOX * CW_KST + CW_STEP * (CW_SLOTS + 1) + 4 * kCacheMaxSeqs + 2 * CW_RED * 512 + 512;
 
 struct CwUnit {
   int head, seq, key0, tiles;    // key tiles of the unit, from key0
   int row0, pos0, keys, rows;    // the sequence: first new row, its position, keys, new rows
   int q0, nq;                    // tiles of rows that see any of the keys
+  bool whole;                    // all rows see all of them
 };
 // Not inlined: every role calls it once per unit, and fetching the code is what a
 // first call costs.
@@ -135,6 +144,9 @@ __device__ __noinline__ CwUnit cw_unit(const CacheWeightsArgs& a, const int* pre
   const int hi = max(win_row_hi(a.w, x.key0, x.keys), win_row_hi(a.w, last, x.keys)) - x.pos0;
   x.q0 = lo / a.R;
   x.nq = hi > lo ? (hi + a.R - 1) / a.R - x.q0 : 0;
+  // a key's first row never falls from key to key, its last one only behind the first keys
+  x.whole = win_row_lo(a.w, last, x.keys) <= x.pos0 &&
+            win_row_hi(a.w, min(max(x.key0, a.w.first), last), x.keys) >= x.keys;
   return x;
 }
 // exp2(s scale) over the columns [ca, cb) of 32 Q, added to acc; s_empty is
@@ -176,38 +188,38 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
   uint8_t* sk = sq + CW_SLOTS * CW_TILE;
   uint8_t* sl = sk + CW_KST * CW_BOX;                          // [slot] the rows' part of the last K step, then the ones
   int* pre = reinterpret_cast<int*>(sl + (CW_SLOTS + 1) * CW_STEP);
-  float* red = reinterpret_cast<float*>(pre + kCacheMaxSeqs);  // [slot][CW_RED][128] sums of a product
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(red + CW_SLOTS * CW_RED * 128);
+  float* red = reinterpret_cast<float*>(pre + kCacheMaxSeqs);  // [group][CW_RED][128] sums of a key tile
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(red + 2 * CW_RED * 128);
   uint64_t* k_empty = k_full + CW_KST;
   uint64_t* q_full = k_empty + CW_KST;
-  uint64_t* q_empty = q_full + CW_SLOTS;
-  uint64_t* l_full = q_empty + CW_SLOTS;
-  uint64_t* l_empty = l_full + CW_SLOTS;
-  uint64_t* s_full = l_empty + CW_SLOTS;
-  uint64_t* s_empty = s_full + CW_SLOTS;
-  uint64_t* r_full = s_empty + CW_SLOTS;                       // [slot][CW_RED]
-  uint64_t* r_empty = r_full + CW_SLOTS * CW_RED;
-  uint64_t* drain = r_empty + CW_SLOTS * CW_RED;
+  uint64_t* q_empty = q_full + CW_PAIRS;
+  uint64_t* l_full = q_empty + CW_PAIRS;
+  uint64_t* l_empty = l_full + CW_PAIRS;
+  uint64_t* s_full = l_empty + CW_PAIRS;
+  uint64_t* s_empty = s_full + CW_PAIRS;
+  uint64_t* r_full = s_empty + CW_PAIRS;                       // [group][CW_RED]
+  uint64_t* r_empty = r_full + 2 * CW_RED;
+  uint64_t* drain = r_empty + 2 * CW_RED;
   int* total = reinterpret_cast<int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  static_assert((2 * CW_KST + 6 * CW_SLOTS + 2 * CW_SLOTS * CW_RED + 1) * 8 + 12 <= 512, "barriers fit");
+  static_assert((2 * CW_KST + 6 * CW_PAIRS + 4 * CW_RED + 1) * 8 + 12 <= 512, "barriers fit");
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < CW_KST; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-    for (int i = 0; i < CW_SLOTS; ++i) {
+    for (int i = 0; i < CW_PAIRS; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&l_full[i], 1);
       mbar_init(&l_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
-      for (int b = 0; b < CW_RED; ++b) {
-        mbar_init(&r_full[i * CW_RED + b], 4);
-        mbar_init(&r_empty[i * CW_RED + b], 1);
-      }
+      mbar_init(&s_empty[i], 8);
+    }
+    for (int b = 0; b < 2 * CW_RED; ++b) {
+      mbar_init(&r_full[b], 4);
+      mbar_init(&r_empty[b], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = timeout_recorded(a.err) ? 1 : 0;   // sticky timeout of an earlier launch
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    uint32_t qph = 0, slot = 0, st = 0, ph = 0, issued = 0, loaded = 0;   // qph: a phase bit per slot
+    uint32_t qph = 0, pair = 0, st = 0, ph = 0, issued = 0, loaded = 0;   // qph: a phase bit per pair
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
       const int rows = min(a.c.page_size, 128);
@@ -285,16 +297,17 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           }
           page = next;
           if (k > 0) continue;
-          for (int i = 0; i < n && ok; ++i) {                      // the pass's rows, after its first keys
-            if (!at_wait(&q_empty[slot], ((qph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
-            qph ^= 1u << slot;
-            loaded |= 1u << slot;
-            if (lane == 0) mbar_arrive_expect_tx(&q_full[slot], (uint32_t)(a.R * a.G * 256));
+          for (int i = 0; i < n && ok; i += 2) {                   // the pass's rows, after its first keys
+            if (!at_wait(&q_empty[pair], ((qph >> pair) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            qph ^= 1u << pair;
+            loaded |= 1u << pair;
+            const int both = min(2, n - i);
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[pair], (uint32_t)(both * a.R * a.G * 256));
             __syncwarp();
-            if (lane < 2)
-              tma_load_4d(sq + slot * CW_TILE + lane * CW_BOX, &tmQ, &q_full[slot], lane * 64, 0, x.head,
-                          x.row0 + (x.q0 + p + i) * a.R);
-            slot = (slot + 1) % CW_SLOTS;
+            if (lane < 2 * both)   // lane: half of the channels, and tile in bit 1
+              tma_load_4d(sq + pair * 2 * CW_TILE + (lane & 1) * CW_TILE + (lane >> 1) * CW_BOX, &tmQ, &q_full[pair],
+                          (lane & 1) * 64, 0, x.head, x.row0 + (x.q0 + p + i + (lane >> 1)) * a.R);
+            pair ^= 1u;
           }
         }
       }
@@ -302,19 +315,19 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     if (*ctl.flag && lane == 0) {   // a wait ran out: let issued loads land before the CTA exits
       for (uint32_t j = issued > CW_KST ? issued - CW_KST : 0; j < issued; ++j)
         at_drain(&k_full[j % CW_KST], (j / CW_KST) & 1u);
-      for (uint32_t i = 0; i < CW_SLOTS; ++i)
+      for (uint32_t i = 0; i < CW_PAIRS; ++i)
         if ((loaded >> i) & 1u) at_drain(&q_full[i], ((qph >> i) & 1u) ^ 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc0 = idesc_bf16(128, 0, false, false);
-    constexpr uint64_t kTile = CW_TILE >> 4, kBox = CW_BOX >> 4;
+    constexpr uint64_t kTile = CW_TILE >> 4, kBox = CW_BOX >> 4, kStep = CW_STEP >> 4;
     const uint32_t one = at_elect();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     const uint64_t kd = sdesc_kmajor(smem_u32(sk)), qd = sdesc_kmajor(smem_u32(sq));
-    const uint64_t ld = at_sdesc_plain16(smem_u32(sl)), ones = ld + CW_SLOTS * (CW_STEP >> 4);
-    uint32_t qph = 0, sph = 0, slot0 = 0, st = 0, ph = 0;   // phase bits per slot
+    const uint64_t ld = at_sdesc_plain16(smem_u32(sl)), ones = ld + CW_SLOTS * kStep;
+    uint32_t qph = 0, sph = 0, pair0 = 0, st = 0, ph = 0;   // phase bits per pair
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
@@ -327,34 +340,36 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             ok = at_wait(&k_full[st], ph, ctl);
             if (++st == CW_KST) { st = 0; ph ^= 1u; }
           }
-          for (int i = 0; i < n && ok; ++i) {
-            const uint32_t slot = (slot0 + i) % CW_SLOTS;
+          uint32_t pair = pair0;
+          for (int i = 0; i < n && ok; i += 2, pair ^= 1u) {
             if (k == 0) {
-              if (!at_wait(&q_full[slot], (qph >> slot) & 1u, ctl) || !at_wait(&l_full[slot], (qph >> slot) & 1u, ctl)) {
+              if (!at_wait(&q_full[pair], (qph >> pair) & 1u, ctl) || !at_wait(&l_full[pair], (qph >> pair) & 1u, ctl)) {
                 ok = false;
                 break;
               }
-              qph ^= 1u << slot;
+              qph ^= 1u << pair;
             }
-            if (!at_wait(&s_empty[slot], ((sph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
-            sph ^= 1u << slot;
+            if (!at_wait(&s_empty[pair], ((sph >> pair) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            sph ^= 1u << pair;
             tc_fence_after();
-            const int cols = min(a.R, x.rows - (x.q0 + p + i) * a.R) * a.G;
+            const int tile = min(i + 1, n - 1);   // the pair's last
+            const int cols = (tile - i) * 128 + min(a.R, x.rows - (x.q0 + p + tile) * a.R) * a.G;
             const uint32_t idesc = idesc0 | (uint32_t)((cols + 15) >> 4) << 18;   // columns / 8 at bit 17
-            const uint64_t q = qd + slot * kTile;
-            at_mma4_ss<2, 2>(tm + slot * 128u, kd + s[0] * kBox, q, idesc, 0u, one);
-            at_mma4_ss<2, 2>(tm + slot * 128u, kd + s[1] * kBox, q + kBox, idesc, 1u, one);
-            at_mma1_ss(tm + slot * 128u, ones, ld + slot * (CW_STEP >> 4), idesc, 1u, one);
-            at_commit(&s_full[slot], one);
+            const uint32_t d = tm + pair * 256u;
+            const uint64_t q = qd + pair * 2 * kTile;
+            at_mma4_ss<2, 2>(d, kd + s[0] * kBox, q, idesc, 0u, one);
+            at_mma4_ss<2, 2>(d, kd + s[1] * kBox, q + kTile, idesc, 1u, one);
+            at_mma1_ss(d, ones, ld + pair * 2 * kStep, idesc, 1u, one);
+            at_commit(&s_full[pair], one);
             if (k == x.tiles - 1) {
-              at_commit(&q_empty[slot], one);
-              at_commit(&l_empty[slot], one);
+              at_commit(&q_empty[pair], one);
+              at_commit(&l_empty[pair], one);
             }
           }
           at_commit(&k_empty[s[0]], one);
           at_commit(&k_empty[s[1]], one);
         }
-        slot0 = (slot0 + n) % CW_SLOTS;
+        pair0 ^= (uint32_t)((n + 1) >> 1) & 1u;
       }
     }
     if (*ctl.flag) {   // a wait ran out: let issued products end
@@ -364,53 +379,57 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ log-sum-exp of the rows
-    uint32_t lph = 0, slot = 0;
+    // One copy of the loads, its divisions before the loop: fetching the code is what
+    // the first tiles wait for.
+    uint32_t lph = 0, pair = 0;
     bool ok = true;
+    int r[4], head_of[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = e * 32 + lane;
+      r[e] = c / a.G;
+      head_of[e] = c - r[e] * a.G;
+    }
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
-      auto values = [&](int i, float (&v)[4]) {           // -lse sqrt(128) of this lane's rows of tile i
+      float v[4], next[4] = {};
+#pragma unroll 1
+      for (int i = -1; i < x.nq; ++i) {                   // the next tile's values arrive during the wait
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int c = e * 32 + lane, r = c / a.G, row = (x.q0 + i) * a.R + r;
-          v[e] = -1e30f;                                  // a row that adds nothing
-          if (i < x.nq && r < a.R && row < x.rows) {
-            const float* at = a.lse + (int64_t)(x.head * a.G + c - r * a.G) * a.n_rows + x.row0 + row;
-            if (in_bounds<float>(a.lse, a.lse_elems, at, 1, a.err, 63)) v[e] = *at * -11.313708498984761f;
-            if (v[e] == INFINITY) v[e] = -1e30f;          // it saw nothing
+          const int row = (x.q0 + i + 1) * a.R + r[e];
+          v[e] = next[e];
+          next[e] = INFINITY;
+          if (i + 1 < x.nq && r[e] < a.R && row < x.rows) {
+            const float* at = a.lse + (int64_t)(x.head * a.G + head_of[e]) * a.n_rows + x.row0 + row;
+            if (in_bounds<float>(a.lse, a.lse_elems, at, 1, a.err, 63)) next[e] = *at;
           }
         }
-      };
-      float v[4], ahead[2][4];                            // the next two tiles' arrive during the waits
-      values(0, v);
-      values(1, ahead[0]);
-      values(2, ahead[1]);
-      for (int i = 0; i < x.nq; ++i) {
-        if (i > 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = ahead[0][e];
-            ahead[0][e] = ahead[1][e];
-          }
-          values(i + 2, ahead[1]);
+        if (i < 0) continue;
+        if ((i & 1) == 0) {
+          if (!at_wait(&l_empty[pair], ((lph >> pair) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          lph ^= 1u << pair;
         }
-        if (!at_wait(&l_empty[slot], ((lph >> slot) & 1u) ^ 1u, ctl)) { ok = false; break; }
-        lph ^= 1u << slot;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c = e * 32 + lane;
-          const float hi = bf16_round(v[e]), mid = bf16_round(v[e] - hi), lo = v[e] - hi - mid;
-          *reinterpret_cast<uint4*>(sl + slot * CW_STEP + (c >> 3) * 256 + (c & 7) * 16) =
+          // -lse sqrt(128); a row that saw nothing (lse -inf) adds nothing, and so does none
+          float l = v[e] * -11.313708498984761f;
+          if (fabsf(l) == INFINITY) l = -1e30f;
+          const float hi = bf16_round(l), mid = bf16_round(l - hi), lo = l - hi - mid;
+          *reinterpret_cast<uint4*>(sl + (2 * pair + (i & 1)) * CW_STEP + (c >> 3) * 256 + (c & 7) * 16) =
               make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.0f), 0u, 0u);
         }
+        if ((i & 1) == 0 && i + 1 < x.nq) continue;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&l_full[slot]);
-        slot = (slot + 1) % CW_SLOTS;
+        if (lane == 0) mbar_arrive(&l_full[pair]);
+        pair ^= 1u;
       }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ sums to weights
-    uint32_t rph = 0, slot0 = 0, turn = 0;   // rph: a phase bit per slot and buffer; turn: a buffer bit per slot
+    uint32_t turn[2] = {0, 0};               // sums taken of each group
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
@@ -447,11 +466,12 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           }
           if (k + 1 < x.tiles) weights_of(k + 1, next_at, next_w);   // arrive during the waits
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int i = 0; i < n; ++i) {
-            const uint32_t slot = (slot0 + i) % CW_SLOTS, b = slot * CW_RED + ((turn >> slot) & 1u);
-            if (!at_wait(&r_full[b], (rph >> b) & 1u, ctl)) { ok = false; break; }
-            rph ^= 1u << b;
-            turn ^= 1u << slot;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g >= n) break;
+            const uint32_t b = g * CW_RED + (turn[g] & (CW_RED - 1));
+            if (!at_wait(&r_full[b], (turn[g] / CW_RED) & 1u, ctl)) { ok = false; break; }
+            ++turn[g];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] += red[b * 128 + e * 32 + lane];
             __syncwarp();
@@ -462,52 +482,59 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           for (int e = 0; e < 4; ++e)
             if (at[e] >= 0) a.out[at[e]] = w[e] + sum[e];
         }
-        if (n > 0) slot0 = (slot0 + n) % CW_SLOTS;
       }
     }
   } else {
     // ------------------------------------------------------------ exponentials and sums
-    const uint32_t odd = (uint32_t)(warp - 4) >> 2;   // slots of this parity
+    const int group = (warp - 4) >> 2;                // the pair's tile
     const int qq = warp & 3;
     const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), 0);
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    uint32_t slot0 = 0, sph = 0, rph = 0, turn = 0;   // a bit per slot (rph: and buffer)
+    uint32_t pair0 = 0, sph = 0, turn = 0;            // sph: a phase bit per pair; turn: sums written
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
       for (int p = 0; p < x.nq && ok; p += CW_SLOTS) {
         const int n = min(CW_SLOTS, x.nq - p);
         for (int k = 0; k < x.tiles && ok; ++k) {
-          const int key = min(x.key0 + k * 128 + qq * 32 + lane, x.keys - 1), unit = win_unit(a.w, key);
-          const int see_lo = win_row_lo_of(a.w, unit, x.keys) - x.pos0;   // rows that see the key
-          const int see_hi = win_row_hi_of(a.w, unit, key, x.keys) - x.pos0;
-          for (int i = 0; i < n; ++i) {
-            const uint32_t slot = (slot0 + i) % CW_SLOTS;
-            if ((slot & 1u) != odd) continue;
-            const int at = (x.q0 + p + i) * a.R;            // the slot's first row
+          int see_lo = 0, see_hi = x.rows;                  // rows that see the key
+          if (!x.whole) {
+            const int key = min(x.key0 + k * 128 + qq * 32 + lane, x.keys - 1), unit = win_unit(a.w, key);
+            see_lo = win_row_lo_of(a.w, unit, x.keys) - x.pos0;
+            see_hi = win_row_hi_of(a.w, unit, key, x.keys) - x.pos0;
+          }
+          float2 acc[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
+          uint32_t pair = pair0;
+          for (int i = group; i < n + group; i += 2, pair ^= 1u) {
+            const int at = (x.q0 + p + i) * a.R;            // the tile's first row
             const int ncol = min(a.R, x.rows - at) * a.G;
             // columns that see the key
             const int ca = min(max(see_lo - at, 0), a.R) * a.G, cb = min(min(max(see_hi - at, 0), a.R) * a.G, ncol);
-            if (!at_wait(&s_full[slot], (sph >> slot) & 1u, ctl)) { ok = false; break; }
-            sph ^= 1u << slot;
+            if (!at_wait(&s_full[pair], (sph >> pair) & 1u, ctl)) { ok = false; break; }
+            sph ^= 1u << pair;
+            if (i >= n) {                                   // a pass's last tile stands alone
+              if (lane == 0) mbar_arrive(&s_empty[pair]);
+              continue;
+            }
             tc_fence_after();
-            float2 acc[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
-            const uint32_t s_at = s_base + slot * 128u;
-            if (ncol <= 32) cw_sums<1>(s_at, ca, cb, sl2, acc, &s_empty[slot]);
-            else cw_sums<4>(s_at, ca, cb, sl2, acc, &s_empty[slot]);
-            const uint32_t b = slot * CW_RED + ((turn >> slot) & 1u);
-            if (!at_wait(&r_empty[b], ((rph >> b) & 1u) ^ 1u, ctl)) { ok = false; break; }
-            rph ^= 1u << b;
-            turn ^= 1u << slot;
+            const uint32_t s_at = s_base + pair * 256u + (uint32_t)group * 128u;
+            if (ncol <= 32) cw_sums<1>(s_at, ca, cb, sl2, acc, &s_empty[pair]);
+            else cw_sums<4>(s_at, ca, cb, sl2, acc, &s_empty[pair]);
+          }
+          if (!ok) break;
+          if (group < n) {
+            const uint32_t b = turn & (CW_RED - 1);
+            if (!at_wait(&r_empty[group * CW_RED + b], ((turn / CW_RED) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            ++turn;
             const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-            red[b * 128 + qq * 32 + lane] = sum.x + sum.y;
+            red[(group * CW_RED + b) * 128 + qq * 32 + lane] = sum.x + sum.y;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&r_full[b]);
+            if (lane == 0) mbar_arrive(&r_full[group * CW_RED + b]);
           }
         }
-        slot0 = (slot0 + n) % CW_SLOTS;
+        pair0 ^= (uint32_t)((n + 1) >> 1) & 1u;
       }
     }
   }
