@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
 //   warp 3 adds the two groups' sums of a key tile to the weights (one sum per group,
 //   not per tile of rows, and no window arithmetic where all rows see a unit: 109 ->
 //   105 us).
-// TMEM: S of pair i at [256 i, 256 i + 256).  A product has as many columns as its
+// TMEM: S of every second product at 0, of the others at 256.  A product has as many columns as its
 // tiles have pairs, rounded up to 16: single rows cost little beside reading K.
 // Shared memory is what the products themselves fill, so the rows' log-sum-exp is
 // not read from it column by column by every thread (16 KB a product and warp, as
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     const uint64_t kd = sdesc_kmajor(smem_u32(sk)), qd = sdesc_kmajor(smem_u32(sq));
     const uint64_t ld = at_sdesc_plain16(smem_u32(sl)), ones = ld + CW_SLOTS * kStep;
-    uint32_t qph = 0, sph = 0, pair0 = 0, st = 0, ph = 0;   // phase bits per pair
+    uint32_t qph = 0, prod = 0, pair0 = 0, st = 0, ph = 0;   // qph: a phase bit per pair; prod: products issued
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
@@ -349,18 +349,19 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
               }
               qph ^= 1u << pair;
             }
-            if (!at_wait(&s_empty[pair], ((sph >> pair) & 1u) ^ 1u, ctl)) { ok = false; break; }
-            sph ^= 1u << pair;
+            const uint32_t sb = prod & 1u;
+            if (!at_wait(&s_empty[sb], ((prod >> 1) & 1u) ^ 1u, ctl)) { ok = false; break; }
+            ++prod;
             tc_fence_after();
             const int tile = min(i + 1, n - 1);   // the pair's last
             const int cols = (tile - i) * 128 + min(a.R, x.rows - (x.q0 + p + tile) * a.R) * a.G;
             const uint32_t idesc = idesc0 | (uint32_t)((cols + 15) >> 4) << 18;   // columns / 8 at bit 17
-            const uint32_t d = tm + pair * 256u;
+            const uint32_t d = tm + sb * 256u;
             const uint64_t q = qd + pair * 2 * kTile;
             at_mma4_ss<2, 2>(d, kd + s[0] * kBox, q, idesc, 0u, one);
             at_mma4_ss<2, 2>(d, kd + s[1] * kBox, q + kTile, idesc, 1u, one);
             at_mma1_ss(d, ones, ld + pair * 2 * kStep, idesc, 1u, one);
-            at_commit(&s_full[pair], one);
+            at_commit(&s_full[sb], one);
             if (k == x.tiles - 1) {
               at_commit(&q_empty[pair], one);
               at_commit(&l_empty[pair], one);
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const int qq = warp & 3;
     const uint32_t s_base = tmem_addr(tmem_base, (uint32_t)(qq * 32), 0);
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    uint32_t pair0 = 0, sph = 0, turn = 0;            // sph: a phase bit per pair; turn: sums written
+    uint32_t prod = 0, turn = 0;                      // products seen, sums written
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const CwUnit x = cw_unit(a, pre, per_head, u);
@@ -506,22 +507,22 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           float2 acc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
-          uint32_t pair = pair0;
-          for (int i = group; i < n + group; i += 2, pair ^= 1u) {
+          for (int i = group; i < n + group; i += 2) {
             const int at = (x.q0 + p + i) * a.R;            // the tile's first row
             const int ncol = min(a.R, x.rows - at) * a.G;
             // columns that see the key
             const int ca = min(max(see_lo - at, 0), a.R) * a.G, cb = min(min(max(see_hi - at, 0), a.R) * a.G, ncol);
-            if (!at_wait(&s_full[pair], (sph >> pair) & 1u, ctl)) { ok = false; break; }
-            sph ^= 1u << pair;
+            const uint32_t sb = prod & 1u;
+            if (!at_wait(&s_full[sb], (prod >> 1) & 1u, ctl)) { ok = false; break; }
+            ++prod;
             if (i >= n) {                                   // a pass's last tile stands alone
-              if (lane == 0) mbar_arrive(&s_empty[pair]);
+              if (lane == 0) mbar_arrive(&s_empty[sb]);
               continue;
             }
             tc_fence_after();
-            const uint32_t s_at = s_base + pair * 256u + (uint32_t)group * 128u;
-            if (ncol <= 32) cw_sums<1>(s_at, ca, cb, sl2, acc, &s_empty[pair]);
-            else cw_sums<4>(s_at, ca, cb, sl2, acc, &s_empty[pair]);
+            const uint32_t s_at = s_base + sb * 256u + (uint32_t)group * 128u;
+            if (ncol <= 32) cw_sums<1>(s_at, ca, cb, sl2, acc, &s_empty[sb]);
+            else cw_sums<4>(s_at, ca, cb, sl2, acc, &s_empty[sb]);
           }
           if (!ok) break;
           if (group < n) {
@@ -534,7 +535,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             if (lane == 0) mbar_arrive(&r_full[group * CW_RED + b]);
           }
         }
-        pair0 ^= (uint32_t)((n + 1) >> 1) & 1u;
       }
     }
   }
@@ -806,7 +806,7 @@ cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   // ones at the tables' width and a last one half full: the lengths are on the
   // device) stands what each unit costs beside its products, one product's time for
   // each of its tiles of rows (at the sequences' average) and two for its start
-  // (405 rows: 15 key tiles 114 us, 4 key tiles 123).
+  // (405 rows: 15 key tiles 101 us, 4 key tiles 116, 8 126).
   const int64_t tiles = ((int64_t)a.c.table_width * a.c.page_size + 127) / 128;
   const int64_t lists = (int64_t)a.c.n_kv_heads * a.c.n_seqs;
   const int64_t per_seq = (a.n_rows + a.c.n_seqs - 1) / a.c.n_seqs;

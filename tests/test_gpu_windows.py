@@ -711,3 +711,49 @@ def test_a_clip_generated_frame_by_frame():
         vv = np.concatenate([f64(v[rows, h * Hk // H]), f64(vn[:, h * Hk // H])])
         (ro, _), (bo, _) = O.forward(f64(qn[:, h]), kk, vv, every)
         within(o.view(frame, H, 128)[:, h], ro, bo, f"after the cut, head {h}")
+
+
+@pytest.mark.parametrize("lengths, new, H, Hk, page, w", [
+    ([1500], [700], 2, 2, 64, dict(right=0)),                                     # six tiles of rows: passes of four and two
+    ([1500, 700], [600, 130], 1, 1, 16, dict(left=300, right=0, n_first=200)),    # five and two
+    ([900, 64, 513], [385, 1, 300], 6, 2, 128, dict(left=3, right=0, n_first=70, unit=50, origin=70)),
+    ([2500, 2100], [129, 2100], 1, 1, 256, dict(left=2, right=1, n_first=0, unit=405, origin=100)),
+])
+def test_collected_weights_of_many_rows(lengths, new, H, Hk, page, w):
+    """Several tiles of rows to a key tile, odd and even many, over one pass and more."""
+    test_collected_weights(lengths, new, H, Hk, page, w)
+
+
+def test_evictions_in_a_row():
+    """What the eviction moves early (first, recent, short sequences') is what the call before it left: weights
+    collected, then three evictions from pool to pool, none waited for."""
+    lengths, heads, page = [3000, 250, 700, 0, 33], 4, 32
+    budgets = [(1500, 100, 700), (900, 300, 40), (350, 0, 350)]
+    c = Paged(lengths, heads, page, 31)
+    stages = [c] + [Paged([min(n, b) for n in lengths], heads, page, 32 + i) for i, (b, _, _) in enumerate(budgets)]
+    new = [5, 5, 5, 0, 5]
+    start, rows = starts(new), sum(new)
+    q = draw(rows, heads, torch.Generator().manual_seed(8))
+    lse = torch.full((heads, rows), 3.0, device="cuda")
+
+    def run(wait):
+        weights = [torch.full_like(x.w, float("nan")) for x in stages]
+        pools = [(c.k, c.v)] + [(torch.full_like(x.k, 3.0), torch.full_like(x.v, 3.0)) for x in stages[1:]]
+        lens = [c.length] + [torch.zeros_like(x.length) for x in stages[1:]]
+        caches = [h3.make_cache(k, v, x.table, n) for (k, v), x, n in zip(pools, stages, lens)]
+        kept = [torch.zeros(len(lengths), heads, b, dtype=torch.int32, device="cuda") for b, _, _ in budgets]
+        torch.cuda.synchronize()
+        h3.h3_cache_weights(c.cache, h3.make_window(right=0), rows, heads, start, q, q.stride(0), q.stride(1), lse, c.w,
+                            weights[0])
+        for i, (b, first, recent) in enumerate(budgets):
+            if wait:
+                torch.cuda.synchronize()
+            h3.h3_cache_evict(caches[i], caches[i + 1], b, first, recent, weights[i], weights[i + 1], kept[i], lens[i + 1])
+        ok()
+        return weights[1:] + [t for pair in pools[1:] for t in pair] + kept + lens[1:]
+
+    slow = run(True)
+    assert slow[-1].tolist() == [min(n, 350) for n in lengths]
+    for _ in range(5):
+        for a, b in zip(run(False), slow):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
