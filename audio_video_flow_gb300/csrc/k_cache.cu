@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
 // much as the operands: 124 us of a call of 405 rows) but comes with the product,
 // as a K step of its own: ones times -lse sqrt(128) in three bf16 parts, 2^-26 of
 // it off.
-// Measured (56 heads, 405 rows over 14,836 keys): 101 us, 855 TFLOP/s; a key tile
-// takes 3400 cycles, of which the tensor core has 1950 and the exponentials 1660 to
+// Measured (56 heads, 405 rows over 14,836 keys): 98 us, 875 TFLOP/s; a key tile
+// takes about 3300 cycles, of which the tensor core has 1950 and the exponentials 1660 to
 // do, the rest is waits between the two, and a CTA's first product starts after 9500.
 // Single rows (6 sequences): 22 us, by the start and the latency of a few key tiles.
 // ---------------------------------------------------------------------------
@@ -806,7 +806,7 @@ cudaError_t launch_cache_weights(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   // ones at the tables' width and a last one half full: the lengths are on the
   // device) stands what each unit costs beside its products, one product's time for
   // each of its tiles of rows (at the sequences' average) and two for its start
-  // (405 rows: 15 key tiles 101 us, 4 key tiles 116, 8 126).
+  // (405 rows: 15 key tiles 101 us, 8 of them 126, 4 116).
   const int64_t tiles = ((int64_t)a.c.table_width * a.c.page_size + 127) / 128;
   const int64_t lists = (int64_t)a.c.n_kv_heads * a.c.n_seqs;
   const int64_t per_seq = (a.n_rows + a.c.n_seqs - 1) / a.c.n_seqs;
