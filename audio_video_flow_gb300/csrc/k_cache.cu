@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
 // much as the operands: 124 us of a call of 405 rows) but comes with the product,
 // as a K step of its own: ones times -lse sqrt(128) in three bf16 parts, 2^-26 of
 // it off.
-// Measured (56 heads, 405 rows over 14,836 keys): 98 us, 875 TFLOP/s; a key tile
+// Measured (56 heads, 405 rows over 14,836 keys): 97 us, 886 TFLOP/s; a key tile
 // takes about 3300 cycles, of which the tensor core has 1950 and the exponentials 1660 to
 // do, the rest is waits between the two, and a CTA's first product starts after 9500.
 // Single rows (6 sequences): 22 us, by the start and the latency of a few key tiles.
@@ -438,15 +438,20 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         const int n = min(CW_SLOTS, x.nq - p);   // 0: no row sees the unit, its weights stay
         // this lane's four keys of key tile k: their places (-1: none) and weights
         auto weights_of = [&](int k, int64_t (&at)[4], float (&w)[4]) {
+          int page[4];                           // all in flight
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = x.key0 + k * 128 + e * 32 + lane;
+            page[e] = key < x.keys ? page_of(a.c, x.seq, key) : -1;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = x.key0 + k * 128 + e * 32 + lane;
             at[e] = -1;
             w[e] = 0.0f;
             if (key < x.keys) {
-              const int page = page_of(a.c, x.seq, key);
-              if (page >= 0 && page < a.c.n_pages) {
-                at[e] = page_row(a.c, page, x.head, key);
+              if (page[e] >= 0 && page[e] < a.c.n_pages) {
+                at[e] = page_row(a.c, page[e], x.head, key);
                 if (!in_bounds<float>(a.out, a.page_rows, a.out + at[e], 1, a.err, 64)) at[e] = -1;
               } else if (p == 0 && max(win_row_lo(a.w, key, x.keys), x.pos0) < win_row_hi(a.w, key, x.keys)) {
                 record_error(a.err, DEVERR_INDEX);   // a page that some row sees
@@ -456,16 +461,17 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             }
           }
         };
-        int64_t at[4], next_at[4];
-        float w[4], next_w[4];
-        weights_of(0, next_at, next_w);
-        for (int k = 0; k < x.tiles && ok; ++k) {
+        int64_t at[4], next_at[4] = {};
+        float w[4], next_w[4] = {};
+#pragma unroll 1
+        for (int k = -1; k < x.tiles && ok; ++k) {       // one copy of the loads, as above
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             at[e] = next_at[e];
             w[e] = next_w[e];
           }
           if (k + 1 < x.tiles) weights_of(k + 1, next_at, next_w);   // arrive during the waits
+          if (k < 0) continue;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 namespace {
 constexpr int EV_THREADS = 1024, EV_BINS = 2048;
 constexpr int EV_KEYS = 48 * 1024;               // keys held in shared memory; further ones are read again
-constexpr int EV_BATCH = 4;                      // slots of a thread in flight
+constexpr int EV_BATCH = 4;                      // slots of a thread in flight (8: 80.2 us of 80.8, short caches 10.1 of 9.4)
 constexpr int EV_SMEM = EV_BINS * 4 + 256;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
