@@ -95,17 +95,19 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
 //   warp 3 adds the two groups' sums of a key tile to the weights (one sum per group,
 //   not per tile of rows, and no window arithmetic where all rows see a unit: 109 ->
 //   105 us).
-// TMEM: S of every second product at 0, of the others at 256.  A product has as many columns as its
-// tiles have pairs, rounded up to 16: single rows cost little beside reading K.
+// TMEM: S of every second product at 0, of the others at 256.  A product has as
+// many columns as its tiles have pairs, rounded up to 16: single rows cost little
+// beside reading K.
 // Shared memory is what the products themselves fill, so the rows' log-sum-exp is
 // not read from it column by column by every thread (16 KB a product and warp, as
 // much as the operands: 124 us of a call of 405 rows) but comes with the product,
 // as a K step of its own: ones times -lse sqrt(128) in three bf16 parts, 2^-26 of
 // it off.
 // Measured (56 heads, 405 rows over 14,836 keys): 97 us, 886 TFLOP/s; a key tile
-// takes about 3300 cycles, of which the tensor core has 1950 and the exponentials 1660 to
-// do, the rest is waits between the two, and a CTA's first product starts after 9500.
-// Single rows (6 sequences): 22 us, by the start and the latency of a few key tiles.
+// takes about 3300 cycles, of which the tensor core has 1950 and the exponentials
+// 1660 to do, the rest is waits between the two, and a CTA's first product starts
+// after 9500.  Single rows (8 sequences of up to 4096 keys): 22 us, by the start and
+// the latency of a few key tiles.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int CW_THREADS = 32 * 12;
