@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(AT2_THREADS, 1)
       uint32_t r[4][32];
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(s_base + (uint32_t)(q4 * 32), r[q4]);
-      tmem_ld_wait(r[0]);
+      tmem_ld_wait(r);
       if (valid < KV_TILE) {
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4)

@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
             uint32_t s[4][32];
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(s_base + (uint32_t)(q4 * 32), s[q4]);
-            tmem_ld_wait(s[0]);
+            tmem_ld_wait(s);
             if (!__all_sync(0xffffffffu, (k0 >= lo && k0 + 128 <= hi) || k0 + 128 <= first)) {
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4) {

@@ -158,7 +158,7 @@ __device__ __forceinline__ void cw_sums(uint32_t s_at, int ca, int cb, float2 sc
   uint32_t s[Q][32];
 #pragma unroll
   for (int q = 0; q < Q; ++q) tmem_ld32(s_at + (uint32_t)(q * 32), s[q]);
-  tmem_ld_wait(s[0]);
+  tmem_ld_wait(s);
   tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(s_empty);
