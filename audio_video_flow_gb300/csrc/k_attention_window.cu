@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       const int64_t tile_elems = (int64_t)a.part_rows * kPartRow;
       const int ts = a.part_slots / 2;
       const bool whole = g->cnt == g->n;
-      float fa = 1.0f, fb = 0.0f, l = l_run, m = m_used;
+      float fa = 1.0f, fb = 0.0f, l = l_run, m = m_used, f_own = 1.0f;
       if (joint) {
         if (!at_wait(sm.b_ready, jph, ctl)) { ok = false; break; }
         jph ^= 1u;
@@ -915,9 +915,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
           }
           m = mt;
           l = lt;
-          const float f = at_ex2(mo - (mt == -INFINITY ? 0.0f : mt));
-          fa *= f;
-          fb *= f;
+          f_own = at_ex2(mo - (mt == -INFINITY ? 0.0f : mt));
         }
       }
       float inv = 1.0f;
@@ -947,8 +945,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
               o[e] = __float_as_uint(__fmaf_rn(__uint_as_float(ob[e]), fb, __uint_as_float(o[e])));
           }
           if (last && !whole) {
-            // the parts in their order: products rounded before they are added, so
-            // that the sums do not depend on which part is the own one
+            // the parts in their order, each scaled to the common maximum as it would be
+            // out of the workspace (both slots' accumulators joined, then one rounded
+            // product), so that the sums do not depend on which part is the own one
             float sum[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) sum[e] = 0.0f;
@@ -957,7 +956,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
               const int k = __ffs(h) - 1;
               if ((own >> k) & 1u) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) sum[e] = __fadd_rn(sum[e], __uint_as_float(o[e]));
+                for (int e = 0; e < 32; ++e) sum[e] = __fadd_rn(sum[e], __fmul_rn(__uint_as_float(o[e]), f_own));
                 continue;
               }
               const float* p = from + k * next + (k == 0 ? ts * tile_elems : 0);
