@@ -1,7 +1,7 @@
 """Calls whose work is cut between CTAs give the same bits whichever of them ends last: units of one and of two tiles of
 rows in two to four parts (joined by the last CTA with its own part still in its accumulators) and in many (joined from
-the workspace).  Each call is repeated beside other work, which changes the order in which CTAs begin and end, and
-replayed from a graph."""
+the workspace), and key tiles of the gradient in pieces.  Each call is repeated beside other work, which changes the order
+in which CTAs begin and end, and replayed from a graph."""
 import pytest
 import torch
 
@@ -28,6 +28,21 @@ def cached(lengths, new, H, Hk, page, w):
     ws = ws_of(h3.h3_attention_cached_workspace_bytes(c.cache, rows, H))
     return lambda: h3.h3_attention_cached(c.cache, h3.make_window(**w), rows, H, start, q, q.stride(0), 128, o, lse,
                                           ws), [o, lse]
+
+
+def gradient(S, H, Hk, w):
+    q, k, v = window_case(S, H, Hk, S + H)
+    o, lse = torch.empty(S, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, S, device="cuda")
+    ws = ws_of(h3.h3_attention_window_workspace_bytes(S, H, Hk))
+    window = h3.make_window(**w)
+    h3.h3_attention_window(window, S, H, Hk, q, q.stride(0), 128, k, v, k.stride(0), 128, o, lse, ws)
+    d_o = draw(S, H, torch.Generator().manual_seed(6)).contiguous()
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    back = ws_of(h3.h3_attention_window_backward_workspace_bytes(S, H, Hk))
+    ok()
+    return lambda: h3.h3_attention_window_backward(window, S, H, Hk, q, q.stride(0), 128, k, v, k.stride(0), 128, o, d_o,
+                                                   lse, grads[0], q.stride(0), 128, grads[1], grads[2], k.stride(0), 128,
+                                                   back), grads
 
 
 def differences(outs, want):
@@ -89,3 +104,12 @@ def check_repeats(run, outs, info, repeats):
 def test_cut_units_repeat(make, args):
     run, outs = make(*args)
     check_repeats(run, outs, lambda s: s.endswith(" split"), 200)
+
+
+@pytest.mark.parametrize("S, H, Hk, w", [
+    (2600, 2, 1, dict(left=100, right=0, n_first=5)),       # the first key tile alone in pieces
+    (2600, 4, 1, dict(right=0)),                            # all of them
+    (4099, 24, 4, dict(left=511, right=128, n_first=3))])
+def test_gradient_in_pieces_repeats(S, H, Hk, w):
+    run, outs = gradient(S, H, Hk, w)
+    check_repeats(run, outs, lambda s: not s.endswith("pieces=1,1"), 50)
