@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       }
       const int r = row_r, qhead = g->head * a.G + row - r * a.G;
       const int64_t at = ((int64_t)(g->row0 + rbase + r) * a.H + qhead) * 128;   // the row in o
-      const int who = (dual ? t : 0) * 4 + qq, few = MODE != AW_ROWS && g->parts <= 2 * kFew + 1;
+      const int who = (dual ? t : 0) * 4 + qq;
+      const bool few = MODE != AW_ROWS && g->parts <= 2 * kFew + 1;
       // A part of a unit.  Few parts: counted in now; who completes the count
       // goes on, with the others' parts (have: those, by the order of the gangs).
       bool last = whole;
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       float* to = a.part + ((int64_t)blockIdx.x * a.part_slots + (g->tail() ? ts : 0) + (dual ? t : 0)) * tile_elems;
       const float* from = nullptr;
       const int64_t next = (int64_t)a.M * a.part_slots * tile_elems;
-      if (active && !whole && few) {
+      if (few && active && !whole) {
         int done = 0;
         if (lane == 0) done = atomicAdd(a.ctrl + g->owner * kCtrl + who, g->cnt) + g->cnt;
         last = __shfl_sync(0xffffffffu, done, 0) == g->n;
@@ -906,8 +907,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
             if (!((own >> k) & 1u)) {
               const float* p = from + k * next + (k == 0 ? ts * tile_elems : 0);
               const int64_t rr = min(row, nrows * a.G - 1);
-              mk = __ldcg(p + (MODE == AW_ROWS ? rr * kPartRow + 128 : 128 * (int64_t)a.part_rows + rr));
-              lk = __ldcg(p + (MODE == AW_ROWS ? rr * kPartRow + 129 : 129 * (int64_t)a.part_rows + rr));
+              mk = __ldcg(p + 128 * (int64_t)a.part_rows + rr);
+              lk = __ldcg(p + 129 * (int64_t)a.part_rows + rr);
             }
             const float top = fmaxf(mt, mk), ref = top == -INFINITY ? 0.0f : top;
             lt = __fadd_rn(__fmul_rn(lt, at_ex2(mt - ref)), __fmul_rn(lk, at_ex2(mk - ref)));
@@ -927,7 +928,6 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
       uint8_t* stg = sm.stage + (warp - 4) * AW_STAGE;
       const unsigned rows_out = __ballot_sync(
           0xffffffffu, last && valid && in_bounds<__nv_bfloat16>(a.o, a.o_elems, a.o + at, 128, a.err, 50));
-      const bool by_row = MODE == AW_ROWS || !few;
       if (active) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {          // 32 channels at a time
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
             for (int e = 0; e < 32; ++e)
               o[e] = __float_as_uint(__fmaf_rn(__uint_as_float(ob[e]), fb, __uint_as_float(o[e])));
           }
-          if (last && !whole) {
+          if (few && last && !whole) {   // (few: never of single rows)
             // the parts in their order, each scaled to the common maximum as it would be
             // out of the workspace (both slots' accumulators joined, then one rounded
             // product), so that the sums do not depend on which part is the own one
@@ -962,20 +962,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
               const float* p = from + k * next + (k == 0 ? ts * tile_elems : 0);
               const int64_t rr = min(row, nrows * a.G - 1);
               float v[32];
-              const float mk = __ldcg(p + (MODE == AW_ROWS ? rr * kPartRow + 128 : 128 * (int64_t)a.part_rows + rr));
-              if (MODE == AW_ROWS) {
+              const float mk = __ldcg(p + 128 * (int64_t)a.part_rows + rr);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 x = __ldcg(reinterpret_cast<const float4*>(p + rr * kPartRow + c * 32 + e));
-                  v[e] = x.x;
-                  v[e + 1] = x.y;
-                  v[e + 2] = x.z;
-                  v[e + 3] = x.w;
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __ldcg(p + (int64_t)(c * 32 + e) * a.part_rows + rr);
-              }
+              for (int e = 0; e < 32; ++e) v[e] = __ldcg(p + (int64_t)(c * 32 + e) * a.part_rows + rr);
               const float f = at_ex2(mk - m_ref);
 #pragma unroll
               for (int e = 0; e < 32; ++e) sum[e] = __fadd_rn(sum[e], __fmul_rn(v[e], f));
@@ -1026,7 +1015,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
               }
             }
           } else if (valid && in_bounds<float>(a.part, a.part_elems, to, (size_t)tile_elems, a.err, 51)) {
-            if (by_row) {
+            if (!few) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<uint4*>(to + (int64_t)row * kPartRow + c * 32 + e) =
@@ -1051,8 +1040,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
         continue;
       }
       if (valid && in_bounds<float>(a.part, a.part_elems, to, (size_t)tile_elems, a.err, 53)) {
-        to[by_row ? (int64_t)row * kPartRow + 128 : 128 * (int64_t)a.part_rows + row] = m;
-        to[by_row ? (int64_t)row * kPartRow + 129 : 129 * (int64_t)a.part_rows + row] = l;
+        to[few ? 128 * (int64_t)a.part_rows + row : (int64_t)row * kPartRow + 128] = m;
+        to[few ? 129 * (int64_t)a.part_rows + row : (int64_t)row * kPartRow + 129] = l;
       }
       __threadfence();
       __syncwarp();
