@@ -476,8 +476,11 @@ h3_status h3_attention_cached(const h3_cache *cache, const h3_window *window, in
  * share the KV head of exp(q_i . k_j / sqrt(128) - lse_i), visible ones.  Rows,
  * window and q as for h3_attention_cached, lse [n_heads][n_rows] as that call
  * left it.  weights fp32 [n_pages][n_kv_heads][page_size]; weights_in NULL: 0, or
- * weights_out itself.  Slots of no sequence are left as they were.  Bitwise
- * repeatable: no atomics. */
+ * weights_out itself.  Slots of no sequence are left as they were.  With weights_in
+ * weights_out itself, slots that no new row sees are not looked at, so their pages may
+ * be another sequence's by now, as for h3_attention_cached; otherwise every page that
+ * a sequence's table names up to its length is written for it, and belongs to it
+ * alone.  Bitwise repeatable: no atomics. */
 h3_status h3_cache_weights(const h3_cache *cache, const h3_window *window, int32_t n_rows, int32_t n_heads,
                            const int32_t *seq_start, const void *q, int64_t q_row_stride_elems,
                            int64_t q_head_stride_elems, const float *lse, const float *weights_in_opt,
