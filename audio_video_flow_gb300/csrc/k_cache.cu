@@ -25,8 +25,9 @@ __device__ __forceinline__ int page_of(const CacheArgs& c, int seq, int slot) {
 // ---------------------------------------------------------------------------
 // Append: row i of sequence s, the rows-before-it-in-s'th of its new ones, goes
 // to slot length[s] - new + that.  A warp copies up to eight heads of one row, all
-// in flight: K by the lower, V by the upper half of its lanes.  Bound by HBM, or by
-// its launch.
+// in flight: K by the lower, V by the upper half of its lanes.  The last CTA copies
+// nothing: it looks at the sequences, which the others meet only by their rows.  Bound
+// by HBM, or by its launch.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int CA_HEADS = 8;
@@ -34,6 +35,11 @@ constexpr int CA_HEADS = 8;
 __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, int warps_per_row) {
   griddep_launch_dependents();
   griddep_wait();
+  if (blockIdx.x == gridDim.x - 1) {
+    for (int s = threadIdx.x; s < a.c.n_seqs; s += 256)
+      if (!cache_seq_ok(a.c, a.n_rows, s)) record_error(a.err, DEVERR_INDEX);
+    return;
+  }
   const int lane = threadIdx.x & 31;
   const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (u >= (int64_t)a.n_rows * warps_per_row) return;
@@ -45,11 +51,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, i
   }
   if (s < 0) return;
   const int b = a.c.start[s], e = a.c.start[s + 1], len = a.c.length[s];
-  if (row >= e && e >= b && s == a.c.n_seqs - 1) return;   // behind the last sequence
-  if (row >= e || !cache_seq_ok(a.c, a.n_rows, s)) {
-    if (lane == 0) record_error(a.err, DEVERR_INDEX);
-    return;
-  }
+  // behind the last sequence, or of one that the last CTA reports
+  if (row >= e || !cache_seq_ok(a.c, a.n_rows, s)) return;
   const int slot = len - (e - b) + (row - b), page = page_of(a.c, s, slot);
   if (page < 0 || page >= a.c.n_pages) {
     if (lane == 0) record_error(a.err, DEVERR_INDEX);
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
   const int warps_per_row = (a.c.n_kv_heads + CA_HEADS - 1) / CA_HEADS;
   const int64_t units = (int64_t)a.n_rows * warps_per_row;
-  const cudaError_t e = launch_kernel(cache_append_kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, a,
+  const cudaError_t e = launch_kernel(cache_append_kernel, dim3((unsigned)((units + 7) / 8 + 1)), dim3(256), 0, stream, a,
                                       warps_per_row);
   if (e != cudaSuccess) return e;
   set_kernel_info("cache_append_kernel rows=%d heads=%d", a.n_rows, a.c.n_kv_heads);
