@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,10 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
           "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
+# Kernels that hand registers from warp to warp (setmaxnreg) and the registers a thread that their split counts on at
+# launch; with fewer the split would wait for registers that nobody gives up.
+REGISTERS = {"attention_window_kernel": 168}
+
 
 def _nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
@@ -38,6 +43,18 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def check_registers(src: str, log: str) -> None:
+    """Raises unless each kernel of REGISTERS that `src` splits registers in was compiled to its count (ptxas -v)."""
+    text = open(src).read()
+    for name, want in REGISTERS.items():
+        if "setmaxnreg" not in text or f" {name}(" not in text.replace("\n", " "):
+            continue
+        got = [int(n) for n in re.findall(r"Compiling entry function '[^']*\d%s(?:I[^']*)?'.*?Used (\d+) registers" % name,
+                                          log, flags=re.S)]
+        if not got or any(n != want for n in got):
+            raise RuntimeError(f"{os.path.basename(src)}: {name} takes {got} registers a thread, its split counts on {want}")
+
+
 def _compile(nvcc: str, src: str, extra, out_dir: str = BUILD) -> str:
     obj = os.path.join(out_dir, os.path.basename(src)[:-3] + ".o")
     cmd = [nvcc, *ARCH, *CFLAGS, *extra, "-c", src, "-o", obj]
@@ -47,6 +64,7 @@ def _compile(nvcc: str, src: str, extra, out_dir: str = BUILD) -> str:
         f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr[-4000:]}")
+    check_registers(src, r.stdout + r.stderr)
     return obj
 
 

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1)
   const bool skip = *ctl.flag != 0 || all <= 0 || sh->loc[1].x <= sh->loc[0].x;
 
   // The softmax warps get registers of the others' (their
-  // share at launch is AW_REGS each, where the scores spill).
+  // share at launch is AW_REGS each, where the scores spill; the build checks that it is).
   static_assert(128 * AW_REGS_FEW + 256 * AW_REGS_MANY <= AW_THREADS * AW_REGS, "the split is within the launch's registers");
   if (skip) {
   } else if (warp < 4) {
@@ -1173,13 +1173,6 @@ static cudaError_t launch_mode(const CUtensorMap& tmQ, const CUtensorMap& tmK, c
   constexpr int smem = AwPlan<MODE>::smem;
   static_assert(tmem_footprint_exclusive(smem), "an attention CTA must hold its SM's TMEM alone");
   if (!tmem_exclusive(smem)) return cudaErrorNotSupported;
-  // the register split waits for registers that only AW_REGS at launch leave
-  static const cudaError_t fits = [kernel] {
-    cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-    return e != cudaSuccess ? e : (attr.numRegs == AW_REGS ? cudaSuccess : cudaErrorNotSupported);
-  }();
-  if (fits != cudaSuccess) return fits;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kernel, dim3((unsigned)ctas), dim3(AW_THREADS), (size_t)smem, stream, tmQ, tmK, tmV, a, runs);
