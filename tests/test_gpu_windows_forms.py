@@ -196,3 +196,39 @@ def test_a_captured_call_follows_table_lengths_and_rows():
                                            f64(vp[pages, h // 2, places]), mask)
             within(o.view(rows, H, 128)[at:at + new[s], h], ro, bo, f"sequence {s} head {h}")
             within(lse[h, at:at + new[s]], rl, bl, f"sequence {s} head {h} lse")
+
+
+def test_offsets_past_32_bits():
+    """q, o and their gradients of more than 2^31 elements; the last rows of the document, which nothing before them
+    changes, as a document of their own."""
+    S, H, last = 131200, 128, 500
+    w = dict(left=200, right=0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, d_o = (torch.randn(S, H, 128, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn(S, 1, 128, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    assert q.numel() > 2 ** 31
+    o, lse = torch.empty(S, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, S, device="cuda")
+    window = h3.make_window(**w)
+    h3.h3_attention_window(window, S, H, 1, q, H * 128, 128, k, v, 128, 128, o, lse,
+                           ws_of(h3.h3_attention_window_workspace_bytes(S, H, 1)))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    h3.h3_attention_window_backward(window, S, H, 1, q, H * 128, 128, k, v, 128, 128, o, d_o, lse, dq, H * 128, 128, dk,
+                                    dv, 128, 128, ws_of(h3.h3_attention_window_backward_workspace_bytes(S, H, 1)))
+    ok()
+    o = o.view(S, H, 128)
+    mask = O.visible(np.arange(last), last, **w)
+    end = slice(S - last, S)
+    sure = slice(w["left"], last)                 # rows that see nothing before the end's first, and keys only it sees
+    kk, vv = f64(k[end, 0]), f64(v[end, 0])
+    # outside `sure`, the end's rows miss what they saw before it: their given output is taken as it is
+    for h in (0, 1, 63, 126, 127):
+        (ro, rl), (bo, bl) = O.forward(f64(q[end, h]), kk, vv, mask)
+        within(o[end, h][sure], ro[sure], bo[sure], f"head {h} o")
+        within(lse[h, end][sure], rl[sure], bl[sure], f"head {h} lse")
+    heads = range(H)
+    (rq, rk, rv), (bq, bk, bv) = O.backward([f64(q[end, h]) for h in heads], kk, vv, [f64(o[end, h]) for h in heads],
+                                            [f64(d_o[end, h]) for h in heads], [f64(lse[h, end]) for h in heads], mask)
+    for h in (0, 1, 63, 126, 127):
+        within(dq[end, h][sure], rq[h][sure], bq[h][sure], f"head {h} dq")
+    within(dk[end, 0][sure], rk[sure], bk[sure], "dk")
+    within(dv[end, 0][sure], rv[sure], bv[sure], "dv")
