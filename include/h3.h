@@ -430,12 +430,14 @@ h3_status h3_attention_window_backward(const h3_window *window, int32_t n_rows, 
  * use.  The page pools are bf16 [n_pages][n_kv_heads][page_size][128]; page_size
  * 16, 32, 64, 128 or 256.  At most 1024 sequences and heads, and 2^24 slots in a
  * table's width (H3_ERR_UNSUPPORTED).  table and length are read on the device
- * when a call runs, so a captured call follows them.  A length above the table's
- * width or below the sequence's new rows, rows that do not begin at or after the
- * sequence before's or leave [0, n_rows], and a page that a row needs outside
+ * when a call runs, so a captured call follows them; what the host decides before
+ * (limits, and how a call is split) goes by the table's width.  A length above the
+ * table's width or below the sequence's new rows, rows that do not begin at or after
+ * the sequence before's or leave [0, n_rows], and a page that a row needs outside
  * [0, n_pages) are reported (H3_ERR_INDEX from h3_sync_check): such a sequence's
  * results are left as they were or, for a page or rows that two sequences claim,
- * undefined; nothing outside the buffers is read or written. */
+ * undefined (h3_cache_evict: length 0, kept all -1); nothing outside the buffers is
+ * read or written. */
 typedef struct {
   void *k, *v;               /* device page pools */
   int32_t n_pages, page_size, n_kv_heads;
@@ -458,12 +460,16 @@ h3_status h3_cache_append(const h3_cache *cache, int32_t n_rows, const int32_t *
 /* Attention of new rows over the cache that holds them (after h3_cache_append),
  * single rows or chunks of any length, every sequence its own: new row r of
  * sequence s stands at slot length[s] - (seq_start[s+1] - seq_start[s]) + r and
- * sees the slots that the window gives, as in h3_attention_window.  q and its
- * heads as there; o bf16 [n_rows][n_heads*128], lse_opt NULL or fp32
- * [n_heads][n_rows]; rows of no sequence are left as they were.  Pages none of whose slots a
- * new row sees are not looked at (a window's old pages may be given back), nor is what
- * the pages hold past a sequence's last slot.  workspace: device, 256-byte
- * aligned, at least h3_attention_cached_workspace_bytes (0 for invalid
+ * sees the slots that the window gives, as in h3_attention_window.  One window holds
+ * for all sequences of a call, and its units count slots: after h3_cache_evict, slots
+ * no longer stand where their rows did, so a window in frames fits only what is kept
+ * in whole frames behind `origin`.  q and its heads as there, and its limits, with the
+ * table's width for the keys; o bf16 [n_rows][n_heads*128], lse_opt NULL or fp32
+ * [n_heads][n_rows]; rows of no sequence are left as they were.  Pages none of whose
+ * slots a new row sees are not looked at (a window's old pages may be given back), nor
+ * is what the pages hold past a sequence's last slot; a non-finite v in a slot that
+ * some row sees makes the rows near that one undefined, as there.  workspace: device,
+ * 256-byte aligned, at least h3_attention_cached_workspace_bytes (0 for invalid
  * arguments); scratch of one call. */
 size_t h3_attention_cached_workspace_bytes(const h3_cache *cache, int32_t n_rows, int32_t n_heads);
 h3_status h3_attention_cached(const h3_cache *cache, const h3_window *window, int32_t n_rows, int32_t n_heads,
@@ -480,7 +486,8 @@ h3_status h3_attention_cached(const h3_cache *cache, const h3_window *window, in
  * weights_out itself, slots that no new row sees are not looked at, so their pages may
  * be another sequence's by now, as for h3_attention_cached; otherwise every page that
  * a sequence's table names up to its length is written for it, and belongs to it
- * alone.  Bitwise repeatable: no atomics. */
+ * alone.  Sequences x KV heads x 128-slot tiles of the table's width are below 2^31
+ * (H3_ERR_UNSUPPORTED).  Bitwise repeatable: no atomics. */
 h3_status h3_cache_weights(const h3_cache *cache, const h3_window *window, int32_t n_rows, int32_t n_heads,
                            const int32_t *seq_start, const void *q, int64_t q_row_stride_elems,
                            int64_t q_head_stride_elems, const float *lse, const float *weights_in_opt,
@@ -491,7 +498,9 @@ h3_status h3_cache_weights(const h3_cache *cache, const h3_window *window, int32
  * the ones of the largest weight (the earlier of equal ones; a NaN counts as the
  * least).  They keep their order, which is that of their new slots 0, 1, ...; K,
  * V and, with weights_to, the weights move to the pages of `to` (pages that `from`
- * does not use: the two may lie in one pool).  Shorter sequences move whole.
+ * does not use, in a table of its own: the two may lie in one pool).  Shorter sequences
+ * move whole.  Every page up to a sequence's length is looked at: none of them may have
+ * been given back.
  * kept int32 [n_seqs][n_kv_heads][budget] receives the slots, -1 behind the last;
  * length_out [n_seqs] the new lengths (it may be to->length, which is not read,
  * and is not from->length).  The two caches have the same heads and sequences;
