@@ -63,3 +63,28 @@ def test_pages_that_another_sequence_took(new, H, Hk, page):
         pages, places = c.at(s, np.flatnonzero(mask.any(axis=0)))
         used[pages, :, places] = True
     assert torch.equal(weights[0][~used], c.w[~used])
+
+
+@pytest.mark.parametrize("page, new", [(16, 200), (64, 3), (32, 1)])
+def test_a_sequence_that_reuses_its_own_pages(page, new):
+    """A ring: the entries of slots that the window has left name pages that newer slots of the same sequence stand in."""
+    w, n, H, Hk = dict(left=50, right=0, n_first=20), 1280, 4, 2
+    free = np.arange(-(-20 // page), (n - new - 50) // page)
+    kept = np.arange((n - new - 50) // page, n // page)
+    c = Paged([n], Hk, page, 8)
+    q = draw(new, H, torch.Generator().manual_seed(2))
+    start = starts([new])
+    clean, ring = c.table.clone(), c.table.clone()
+    clean[0, torch.from_numpy(free).cuda()] = -5
+    ring[0, torch.from_numpy(free).cuda()] = c.table[0, torch.from_numpy(np.resize(kept, len(free))).cuda()]
+    results = []
+    for table in [clean] + [ring] * 10:
+        c.cache = h3.make_cache(c.k, c.v, table, c.length)
+        o, lse = run_cached(c, w, q, start, H)
+        weights = c.w.clone()
+        h3.h3_cache_weights(c.cache, h3.make_window(**w), new, H, start, q, q.stride(0), q.stride(1), lse, weights, weights)
+        results.append((o, lse, weights))
+    ok()
+    for r in results[1:]:
+        for a, b in zip(r, results[0]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
